@@ -22,6 +22,8 @@ __all__ = [
     "sgemm_device_status", "sgemm_release_workspace", "sgemm_num_configs",
     "sgemm_config_name", "sgemm_select_config", "sgemm_force_config",
     "sgemm_selftest_bounded_wait", "matmul",
+    "sgemm_linear", "sgemm_linear_backward", "sgemm_moe", "linear", "linear_backward", "moe",
+    "SGEMM_DTYPE_BF16", "SGEMM_DTYPE_F16",
     "SGEMM_OK", "SGEMM_ERR_INVALID_VALUE", "SGEMM_ERR_LAUNCH", "SGEMM_ERR_TIMEOUT",
     "SGEMM_ERR_UNSUPPORTED",
 ]
@@ -35,6 +37,9 @@ SGEMM_ERR_UNSUPPORTED = 4
 SGEMM_OP_N, SGEMM_OP_T = 0, 1
 SGEMM_PATH_SIMT, SGEMM_PATH_3XTF32, SGEMM_PATH_TF32 = 0, 1, 2
 _PATHS = {"simt": SGEMM_PATH_SIMT, "3xtf32": SGEMM_PATH_3XTF32, "tf32": SGEMM_PATH_TF32}
+SGEMM_DTYPE_BF16, SGEMM_DTYPE_F16 = 0, 1
+_DTYPES = {"torch.bfloat16": SGEMM_DTYPE_BF16, "torch.float16": SGEMM_DTYPE_F16,
+           "bf16": SGEMM_DTYPE_BF16, "f16": SGEMM_DTYPE_F16}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 _LIBRARY = Path(__file__).resolve().with_name("libsgemm_gb300.so")
@@ -82,6 +87,15 @@ def _bind(L):
     L.sgemm_fused.restype = i32
     L.sgemm_fused_strided_batched.argtypes = [i32, i32, i32] + batched[:-1] + [p, i32, p]
     L.sgemm_fused_strided_batched.restype = i32
+    L.sgemm_linear.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p, i64,
+                               p, i64, p]
+    L.sgemm_linear.restype = i32
+    L.sgemm_linear_backward.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, i32, p, i64, p,
+                                        i64, p, i64, p, i64, p, p]
+    L.sgemm_linear_backward.restype = i32
+    L.sgemm_moe.argtypes = [i32, i32, i64, i64, i64, i64, i64, p, i64, p, i64, p, p, i64, i64, p,
+                            i64, i64, i32, p, p, i64, p, i64, p, p, p]
+    L.sgemm_moe.restype = i32
     L.sgemm_status_string.argtypes = [i32]
     L.sgemm_status_string.restype = ctypes.c_char_p
     L.sgemm_last_error.argtypes = []
@@ -315,3 +329,190 @@ def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, tensor_cores: bo
     fn(M, N, K, alpha, A, max(A.stride(0), 1), B, max(B.stride(0), 1), beta, C,
        max(C.stride(0), 1), stream)
     return C
+
+
+# ---- layer operators on 16-bit values ------------------------------------------------------------
+
+def _ptr16(x, dtype):
+    """Address of a CUDA tensor of the call's 16-bit type (or an address, or None)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise TypeError("tensor arguments must live on a CUDA device")
+    if _DTYPES.get(str(x.dtype)) != dtype:
+        raise TypeError(f"expected every matrix of the call in one 16-bit type, got {x.dtype}")
+    return x.data_ptr()
+
+
+def _dtype_code(dtype) -> int:
+    return dtype if isinstance(dtype, int) else _DTYPES.get(str(dtype), -1)
+
+
+def _act_code(act) -> int:
+    return ACTIVATIONS[act] if isinstance(act, str) else int(act)
+
+
+def sgemm_linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z=None, ldz=0,
+                 stream=None) -> None:
+    """Z = X op(W) + bias, Y = act(Z) + R on bfloat16 or half matrices (asynchronous on
+    ``stream``); dtype is 'bf16' / 'f16', a torch dtype or the enum value. See
+    include/sgemm.h."""
+    dt = _dtype_code(dtype)
+    _check(lib().sgemm_linear(dt, _op(transw), M, N, K, _ptr16(X, dt), ldx, _ptr16(W, dt), ldw,
+                              _ptr16(bias, dt), _act_code(act), _ptr16(R, dt), ldr,
+                              _ptr16(Y, dt), ldy, _ptr16(Z, dt), ldz, _stream(stream)))
+
+
+def sgemm_linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx,
+                          dW, lddw, db, stream=None) -> None:
+    """The gradients of sgemm_linear (see include/sgemm.h); dX, dW and db may be None."""
+    dt = _dtype_code(dtype)
+    _check(lib().sgemm_linear_backward(dt, _op(transw), M, N, K, _ptr16(dY, dt), lddy,
+                                       _ptr16(Z, dt), ldz, _act_code(act), _ptr16(X, dt), ldx,
+                                       _ptr16(W, dt), ldw, _ptr16(dX, dt), lddx, _ptr16(dW, dt),
+                                       lddw, _ptr(db), _stream(stream)))
+
+
+def _ptr_as(x, names):
+    """Address of a CUDA tensor whose dtype is one of `names` (or an address, or None)."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_cuda:
+        raise TypeError("tensor arguments must live on a CUDA device")
+    if str(x.dtype) not in names:
+        raise TypeError(f"expected {' or '.join(names)}, got {x.dtype}")
+    return x.data_ptr()
+
+
+def sgemm_moe(dtype, act, T, E, topk, D, F, X, ldx, Wr, ldwr, Wgate, Wup, ldu, strideu, Wdown, ldd,
+              strided, renormalize, active, R, ldr, Y, ldy, topk_index=None, topk_weight=None,
+              stream=None) -> None:
+    """A whole mixture-of-experts layer for up to 64 tokens (see include/sgemm.h)."""
+    dt = _dtype_code(dtype)
+    _check(lib().sgemm_moe(dt, _act_code(act), T, E, topk, D, F, _ptr16(X, dt), ldx,
+                           _ptr16(Wr, dt), ldwr, _ptr16(Wgate, dt), _ptr16(Wup, dt), ldu, strideu,
+                           _ptr16(Wdown, dt), ldd, strided, int(bool(renormalize)),
+                           _ptr_as(active, ("torch.bool", "torch.uint8")), _ptr16(R, dt), ldr,
+                           _ptr16(Y, dt), ldy, _ptr_as(topk_index, ("torch.int32",)),
+                           _ptr_as(topk_weight, ("torch.float32",)), _stream(stream)))
+
+
+def _ld(t, what):
+    """Leading dimension of a 2-D tensor with contiguous rows."""
+    if t is None:
+        return 0
+    rows, cols = t.shape
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols, 1)
+
+
+def _shape(t, shape, what):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _same_device(first, *rest):
+    """Tensors of one call live on one device, which is the calling thread's current one."""
+    import torch
+    for t in (first, *rest):
+        if t is not None and t.device != first.device:
+            raise ValueError("the tensors of a call must be on one device")
+    if first.is_cuda and first.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {first.device}, which is not the current device")
+
+
+def _weight_shape(weight, transw):
+    """(N, K) of a weight stored N x K ('T') or K x N ('N')."""
+    if weight.dim() != 2:
+        raise ValueError("weight must be 2-D")
+    a, b = weight.shape
+    return (a, b) if _op(transw) == SGEMM_OP_T else (b, a)
+
+
+def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre=False, out=None,
+           stream=None):
+    """torch convenience: act(x op(weight) + bias) + residual on 2-D bfloat16 or half CUDA
+    tensors with contiguous rows. ``transw='T'`` takes a weight stored out x in (as
+    torch.nn.Linear keeps it), 'N' one stored in x out. Returns y, or (y, pre) with the
+    pre-activation that ``linear_backward`` reads when ``save_pre``. ``out`` may be
+    ``residual`` itself."""
+    import torch
+    N, K = _weight_shape(weight, transw)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError(f"x must be 2-D with {K} columns")
+    M = x.shape[0]
+    _shape(bias, (N,), "bias")
+    _shape(residual, (M, N), "residual")
+    _shape(out, (M, N), "out")
+    if bias is not None and N > 1 and bias.stride(0) != 1:
+        raise ValueError("bias must be contiguous")
+    _same_device(x, weight, bias, residual, out)
+    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else out
+    z = torch.empty((M, N), dtype=x.dtype, device=x.device) if save_pre else None
+    sgemm_linear(x.dtype, transw, M, N, K, x, _ld(x, "x"), weight, _ld(weight, "weight"), bias, act,
+                 residual, _ld(residual, "residual"), y, _ld(y, "out"), z, _ld(z, "pre"), stream)
+    return (y, z) if save_pre else y
+
+
+def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=True, need_dw=True,
+                    need_db=True, stream=None):
+    """torch convenience: (dx, dw, db) of ``linear`` from dy and the saved pre-activation
+    (None for those not needed; db is float32). The residual's gradient is dy itself."""
+    import torch
+    N, K = _weight_shape(weight, transw)
+    M = x.shape[0]
+    _shape(x, (M, K), "x")
+    _shape(dy, (M, N), "dy")
+    _shape(pre, (M, N), "pre")
+    _same_device(x, weight, dy, pre)
+    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_dx else None
+    dw = torch.empty(tuple(weight.shape), dtype=x.dtype, device=x.device) if need_dw else None
+    db = torch.empty(N, dtype=torch.float32, device=x.device) if need_db else None
+    sgemm_linear_backward(x.dtype, transw, M, N, K, dy, _ld(dy, "dy"), pre, _ld(pre, "pre"), act, x,
+                          _ld(x, "x"), weight, _ld(weight, "weight"), dx, _ld(dx, "dx"), dw,
+                          _ld(dw, "dw"), db, stream)
+    return dx, dw, db
+
+
+def _expert_ld(w, what):
+    """(leading dimension, expert stride) of an E x rows x cols tensor."""
+    E, rows, cols = w.shape
+    if w.stride(2) != 1 and cols > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    ld = w.stride(1) if rows > 1 else max(w.stride(1), cols, 1)
+    return ld, w.stride(0) if E > 1 else max(w.stride(0), rows * ld)
+
+
+def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, active=None,
+        residual=None, out=None, stream=None):
+    """torch convenience: a whole mixture-of-experts layer for up to 64 tokens. x T x D, router
+    E x D, w_gate (or None) and w_up E x F x D, w_down E x D x F, active T booleans or None.
+    Returns (y, index, weight) with the chosen experts (int32) and their weights (float32),
+    T x topk each."""
+    import torch
+    if w_up.dim() != 3:
+        raise ValueError("w_up must be 3-D (experts x hidden x width)")
+    E, F, D = w_up.shape
+    T = x.shape[0]
+    _shape(x, (T, D), "x")
+    _shape(router, (E, D), "router")
+    _shape(w_gate, (E, F, D), "w_gate")
+    _shape(w_down, (E, D, F), "w_down")
+    _shape(residual, (T, D), "residual")
+    _shape(out, (T, D), "out")
+    _shape(active, (T,), "active")
+    if active is not None and T > 1 and active.stride(0) != 1:
+        raise ValueError("active must be contiguous")
+    _same_device(x, router, w_gate, w_up, w_down, residual, out, active)
+    ldu, su = _expert_ld(w_up, "w_up")
+    if w_gate is not None and _expert_ld(w_gate, "w_gate") != (ldu, su):
+        raise ValueError("w_gate and w_up must have the same strides")
+    ldd, sd = _expert_ld(w_down, "w_down")
+    y = torch.empty((T, D), dtype=x.dtype, device=x.device) if out is None else out
+    index = torch.empty((T, topk), dtype=torch.int32, device=x.device)
+    weight = torch.empty((T, topk), dtype=torch.float32, device=x.device)
+    sgemm_moe(x.dtype, act, T, E, topk, D, F, x, _ld(x, "x"), router, _ld(router, "router"), w_gate,
+              w_up, ldu, su, w_down, ldd, sd, renormalize, active, residual,
+              _ld(residual, "residual"), y, _ld(y, "out"), index, weight, stream)
+    return y, index, weight

@@ -1,0 +1,54 @@
+// half16.cuh: 16-bit storage types (bfloat16, IEEE half) of the layer operators. Values are
+// widened exactly to fp32 when read and rounded once, to nearest even, when written.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace sg {
+
+enum Dtype16 : int { kBf16 = 0, kF16 = 1 };
+
+template <typename T>
+struct Half16;
+
+template <>
+struct Half16<__nv_bfloat16> {
+    static constexpr int kind = kBf16;
+    __device__ static __forceinline__ float widen(uint16_t v) {
+        return __uint_as_float(static_cast<uint32_t>(v) << 16);
+    }
+    __device__ static __forceinline__ uint16_t narrow(float v) {
+        return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    }
+    __device__ static __forceinline__ float2 widen2(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    }
+    // lo in the low half
+    __device__ static __forceinline__ uint32_t narrow2(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+template <>
+struct Half16<__half> {
+    static constexpr int kind = kF16;
+    __device__ static __forceinline__ float widen(uint16_t v) {
+        return __half2float(__ushort_as_half(v));
+    }
+    __device__ static __forceinline__ uint16_t narrow(float v) {
+        return __half_as_ushort(__float2half_rn(v));
+    }
+    __device__ static __forceinline__ float2 widen2(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    __device__ static __forceinline__ uint32_t narrow2(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+}  // namespace sg

@@ -12,6 +12,7 @@
 #include "config_table.h"
 #include "epilogue.cuh"
 #include "host_gemm.cuh"
+#include "layer16.cuh"
 #include "ptx.cuh"
 #include "simt_gemm.cuh"
 #include "tf32x3_gemm.cuh"
@@ -258,9 +259,287 @@ cudaError_t chunk_gemm(long long M, long long N, long long K, float alpha, const
     return cudaSuccess;
 }
 
+// ---- layer operators on 16-bit values -----------------------------------------------------------
+
+bool known_dtype(sgemm_dtype_t d) { return d == SGEMM_DTYPE_BF16 || d == SGEMM_DTYPE_F16; }
+bool known_op(sgemm_op_t op) { return op == SGEMM_OP_N || op == SGEMM_OP_T; }
+bool known_act(sgemm_activation_t a) { return a >= SGEMM_ACT_NONE && a <= SGEMM_ACT_SILU; }
+bool short_ld(long long ld, long long cols) { return ld < (cols > 1 ? cols : 1); }
+bool odd(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) != 0; }
+const uint16_t *in16(const void *p) { return static_cast<const uint16_t *>(p); }
+uint16_t *out16(void *p) { return static_cast<uint16_t *>(p); }
+
+sgemm_status_t check_linear(sgemm_dtype_t dtype, sgemm_op_t transw, sgemm_activation_t act,
+                            int64_t M, int64_t N, int64_t K) {
+    if (!known_dtype(dtype)) return fail(SGEMM_ERR_INVALID_VALUE, "unknown dtype");
+    if (!known_op(transw))
+        return fail(SGEMM_ERR_INVALID_VALUE, "transw must be SGEMM_OP_N or SGEMM_OP_T");
+    if (!known_act(act)) return fail(SGEMM_ERR_INVALID_VALUE, "unknown activation");
+    if (M < 0 || N < 0 || K < 0) return fail(SGEMM_ERR_INVALID_VALUE, "M, N and K must be >= 0");
+    return SGEMM_OK;
+}
+
+sgemm_status_t check_layer_limits(int64_t M, int64_t N, int64_t K) {
+    if (M > kMaxDim || N > kMaxDim || K > kMaxDim)
+        return fail(SGEMM_ERR_UNSUPPORTED, "a dimension exceeds 2^31 - 1");
+    if (!have_device()) return fail(SGEMM_ERR_UNSUPPORTED, "no CUDA device available");
+    return SGEMM_OK;
+}
+
+sgemm_status_t linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
+                      const void *X, int64_t ldx, const void *W, int64_t ldw, const void *bias,
+                      sgemm_activation_t act, const void *R, int64_t ldr, void *Y, int64_t ldy,
+                      void *Z, int64_t ldz, cudaStream_t stream) {
+    sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
+    if (st != SGEMM_OK) return st;
+    if (short_ld(ldx, K)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < max(1, K)");
+    if (short_ld(ldw, transw == SGEMM_OP_T ? K : N))
+        return fail(SGEMM_ERR_INVALID_VALUE, transw == SGEMM_OP_T ? "ldw < max(1, K) (W transposed)"
+                                                                  : "ldw < max(1, N)");
+    if (R && short_ld(ldr, N)) return fail(SGEMM_ERR_INVALID_VALUE, "ldr < max(1, N)");
+    if (short_ld(ldy, N)) return fail(SGEMM_ERR_INVALID_VALUE, "ldy < max(1, N)");
+    if (Z && short_ld(ldz, N)) return fail(SGEMM_ERR_INVALID_VALUE, "ldz < max(1, N)");
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (!Y) return fail(SGEMM_ERR_INVALID_VALUE, "Y is NULL");
+    if (K > 0 && (!X || !W)) return fail(SGEMM_ERR_INVALID_VALUE, "X or W is NULL");
+    if (odd(X) || odd(W) || odd(bias) || odd(R) || odd(Y) || odd(Z))
+        return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its 2-byte type");
+    if (Y == Z) return fail(SGEMM_ERR_INVALID_VALUE, "Y and Z are the same matrix");
+    if ((R == Y && ldr != ldy) || (Z && R == Z))
+        return fail(SGEMM_ERR_INVALID_VALUE, "R overlaps an output other than as Y itself");
+    st = check_layer_limits(M, N, K);
+    if (st != SGEMM_OK) return st;
+    sg::Gemm16 g;
+    g.dtype = dtype;
+    g.M = static_cast<int>(M);
+    g.N = static_cast<int>(N);
+    g.K = static_cast<int>(K);
+    g.A = in16(X);
+    g.lda = ldx;
+    g.B = in16(W);
+    g.ldb = ldw;
+    g.b_mn = transw == SGEMM_OP_N;
+    g.D = out16(Y);
+    g.ldd = ldy;
+    g.bias = in16(bias);
+    g.act = act;
+    g.res = in16(R);
+    g.ldr = ldr;
+    g.pre = out16(Z);
+    g.ldz = ldz;
+    const char *detail = "";
+    const cudaError_t err = sg::gemm16_launch(g, stream, &detail);
+    return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
+}
+
+sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                               int64_t K, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
+                               sgemm_activation_t act, const void *X, int64_t ldx, const void *W,
+                               int64_t ldw, void *dX, int64_t lddx, void *dW, int64_t lddw,
+                               float *db, cudaStream_t stream) {
+    sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
+    if (st != SGEMM_OK) return st;
+    const bool t = transw == SGEMM_OP_T;
+    const int64_t wcols = t ? K : N;
+    if (short_ld(lddy, N)) return fail(SGEMM_ERR_INVALID_VALUE, "lddy < max(1, N)");
+    if (act != SGEMM_ACT_NONE && short_ld(ldz, N)) return fail(SGEMM_ERR_INVALID_VALUE, "ldz < max(1, N)");
+    if (dW && short_ld(ldx, K)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < max(1, K)");
+    if (dX && short_ld(ldw, wcols))
+        return fail(SGEMM_ERR_INVALID_VALUE, t ? "ldw < max(1, K) (W transposed)" : "ldw < max(1, N)");
+    if (dX && short_ld(lddx, K)) return fail(SGEMM_ERR_INVALID_VALUE, "lddx < max(1, K)");
+    if (dW && short_ld(lddw, wcols))
+        return fail(SGEMM_ERR_INVALID_VALUE, t ? "lddw < max(1, K) (W transposed)" : "lddw < max(1, N)");
+    const bool want_dx = dX && M > 0 && K > 0, want_dw = dW && N > 0 && K > 0, want_db = db && N > 0;
+    if (!want_dx && !want_dw && !want_db) return SGEMM_OK;
+    const bool reads = M > 0 && N > 0;
+    if (reads && !dY) return fail(SGEMM_ERR_INVALID_VALUE, "dY is NULL");
+    if (reads && act != SGEMM_ACT_NONE && !Z)
+        return fail(SGEMM_ERR_INVALID_VALUE, "Z is NULL (the activation's gradient needs it)");
+    if (reads && want_dw && !X) return fail(SGEMM_ERR_INVALID_VALUE, "X is NULL (dW needs it)");
+    if (reads && want_dx && !W) return fail(SGEMM_ERR_INVALID_VALUE, "W is NULL (dX needs it)");
+    if (odd(dY) || odd(Z) || odd(X) || odd(W) || odd(dX) || odd(dW) ||
+        (reinterpret_cast<uintptr_t>(db) & 3u))
+        return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its type");
+    st = check_layer_limits(M, N, K);
+    if (st != SGEMM_OK) return st;
+
+    const char *detail = "";
+    const uint16_t *dz = in16(dY);
+    long long lddz = lddy;
+    cudaError_t err = cudaSuccess;
+    const bool products = want_dx || want_dw;
+    if (N > 0 && (want_db || (reads && products && act != SGEMM_ACT_NONE))) {
+        sg::ActGrad a;
+        a.dtype = dtype;
+        a.M = static_cast<int>(M);
+        a.N = static_cast<int>(N);
+        a.dy = in16(dY);
+        a.lddy = lddy;
+        a.z = in16(Z);
+        a.ldz = ldz;
+        a.act = act;
+        a.db = db;
+        if (reads && products && act != SGEMM_ACT_NONE) {
+            lddz = (N + 7) / 8 * 8;
+            void *p = nullptr;
+            err = sg::layer_scratch(sg::kScratchDz, stream, static_cast<size_t>(M) * lddz * 2, &p, &detail);
+            if (err != cudaSuccess) return fail_cuda(detail, err);
+            a.dz = static_cast<uint16_t *>(p);
+            a.lddz = lddz;
+            dz = a.dz;
+        }
+        err = sg::act_grad_launch(a, stream, &detail);
+        if (err != cudaSuccess) return fail_cuda(detail, err);
+    }
+    sg::Gemm16 g;
+    g.dtype = dtype;
+    if (want_dx) {  // dX = dZ . op(W)^T: K of this product is N, op(W)^T is N x K
+        g.M = static_cast<int>(M);
+        g.N = static_cast<int>(K);
+        g.K = static_cast<int>(N);
+        g.A = dz;
+        g.lda = lddz;
+        g.a_mn = false;
+        g.B = in16(W);
+        g.ldb = ldw;
+        g.b_mn = t;  // W stored N x K: rows run along this product's K
+        g.D = out16(dX);
+        g.ldd = lddx;
+        err = sg::gemm16_launch(g, stream, &detail);
+        if (err != cudaSuccess) return fail_cuda(detail, err);
+    }
+    if (want_dw) {  // dW = dZ^T . X (N x K) or X^T . dZ (K x N): K of this product is M
+        g.M = static_cast<int>(t ? N : K);
+        g.N = static_cast<int>(t ? K : N);
+        g.K = static_cast<int>(M);
+        g.A = t ? dz : in16(X);
+        g.lda = t ? lddz : ldx;
+        g.a_mn = true;
+        g.B = t ? in16(X) : dz;
+        g.ldb = t ? ldx : lddz;
+        g.b_mn = true;
+        g.D = out16(dW);
+        g.ldd = lddw;
+        err = sg::gemm16_launch(g, stream, &detail);
+        if (err != cudaSuccess) return fail_cuda(detail, err);
+    }
+    return SGEMM_OK;
+}
+
+sgemm_status_t moe(const sg::Moe16 &m, int64_t T, int64_t E, int64_t topk, int64_t D, int64_t F,
+                   cudaStream_t stream) {
+    if (m.dtype != SGEMM_DTYPE_BF16 && m.dtype != SGEMM_DTYPE_F16)
+        return fail(SGEMM_ERR_INVALID_VALUE, "unknown dtype");
+    if (m.act < SGEMM_ACT_NONE || m.act > SGEMM_ACT_SILU)
+        return fail(SGEMM_ERR_INVALID_VALUE, "unknown activation");
+    if (T < 0 || D < 0 || F < 0) return fail(SGEMM_ERR_INVALID_VALUE, "T, D and F must be >= 0");
+    if (E < 1) return fail(SGEMM_ERR_INVALID_VALUE, "E must be >= 1");
+    if (topk < 1 || topk > E) return fail(SGEMM_ERR_INVALID_VALUE, "topk must be between 1 and E");
+    if (short_ld(m.ldx, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < max(1, D)");
+    if (short_ld(m.ldr, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldwr < max(1, D)");
+    if (short_ld(m.ldu, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldu < max(1, D)");
+    if (short_ld(m.ldd, F)) return fail(SGEMM_ERR_INVALID_VALUE, "ldd < max(1, F)");
+    if (m.su < 0 || m.sd < 0 || (E > 1 && (F > m.su / m.ldu || D > m.sd / m.ldd)))
+        return fail(SGEMM_ERR_INVALID_VALUE, "strideu < F * ldu or strided < D * ldd");
+    if (m.R && short_ld(m.ldres, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldr < max(1, D)");
+    if (short_ld(m.ldy, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldy < max(1, D)");
+    if (T > sg::kMoeMaxTokens || E > sg::kMoeMaxExperts || topk > sg::kMoeMaxTopk)
+        return fail(SGEMM_ERR_UNSUPPORTED, "sgemm_moe takes at most 64 tokens, 512 experts and topk 16");
+    if (T == 0) return SGEMM_OK;
+    if (D > 0 && !m.Y) return fail(SGEMM_ERR_INVALID_VALUE, "Y is NULL");
+    if (D > 0 && (!m.X || !m.Wr)) return fail(SGEMM_ERR_INVALID_VALUE, "X or Wr is NULL");
+    if (D > 0 && F > 0 && (!m.Wu || !m.Wd)) return fail(SGEMM_ERR_INVALID_VALUE, "Wup or Wdown is NULL");
+    if (odd(m.X) || odd(m.Wr) || odd(m.Wg) || odd(m.Wu) || odd(m.Wd) || odd(m.R) || odd(m.Y) ||
+        (reinterpret_cast<uintptr_t>(m.index) & 3u) || (reinterpret_cast<uintptr_t>(m.weight) & 3u))
+        return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its type");
+    if (m.R && m.R == m.Y && m.ldres != m.ldy)
+        return fail(SGEMM_ERR_INVALID_VALUE, "R overlaps Y other than as Y itself");
+    const sgemm_status_t st = check_layer_limits(D, F, 0);
+    if (st != SGEMM_OK) return st;
+    sg::Moe16 q = m;
+    q.T = static_cast<int>(T);
+    q.E = static_cast<int>(E);
+    q.k = static_cast<int>(topk);
+    q.D = static_cast<int>(D);
+    q.F = static_cast<int>(F);
+    const char *detail = "";
+    const cudaError_t err = sg::moe16_launch(q, stream, &detail);
+    return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
+}
+
+// Runs `body`, turning a C++ exception (host memory exhausted) into a status. A call's launches
+// share the stream's scratch, so calls from several host threads queue theirs one call at a time.
+template <typename Body>
+sgemm_status_t guarded(Body body) {
+    static std::mutex queueing;
+    t_last_error[0] = '\0';
+    try {
+        std::lock_guard<std::mutex> lock(queueing);
+        return body();
+    } catch (...) {
+        return fail(SGEMM_ERR_LAUNCH, "out of host memory");
+    }
+}
+
 }  // namespace
 
 extern "C" {
+
+sgemm_status_t sgemm_linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                            int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                            const void *bias, sgemm_activation_t act, const void *R, int64_t ldr,
+                            void *Y, int64_t ldy, void *Z, int64_t ldz, void *stream) {
+    return guarded([&] {
+        return linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z, ldz,
+                      static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                                     int64_t K, const void *dY, int64_t lddy, const void *Z,
+                                     int64_t ldz, sgemm_activation_t act, const void *X,
+                                     int64_t ldx, const void *W, int64_t ldw, void *dX,
+                                     int64_t lddx, void *dW, int64_t lddw, float *db,
+                                     void *stream) {
+    return guarded([&] {
+        return linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX,
+                               lddx, dW, lddw, db, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T, int64_t E,
+                         int64_t topk, int64_t D, int64_t F, const void *X, int64_t ldx,
+                         const void *Wr, int64_t ldwr, const void *Wgate, const void *Wup,
+                         int64_t ldu, int64_t strideu, const void *Wdown, int64_t ldd,
+                         int64_t strided, int renormalize, const uint8_t *active, const void *R,
+                         int64_t ldr, void *Y, int64_t ldy, int32_t *topk_index,
+                         float *topk_weight, void *stream) {
+    return guarded([&] {
+        sg::Moe16 m;
+        m.dtype = static_cast<int>(dtype);
+        m.act = static_cast<int>(act);
+        m.X = in16(X);
+        m.ldx = ldx;
+        m.Wr = in16(Wr);
+        m.ldr = ldwr;
+        m.Wg = in16(Wgate);
+        m.Wu = in16(Wup);
+        m.ldu = ldu;
+        m.su = strideu;
+        m.Wd = in16(Wdown);
+        m.ldd = ldd;
+        m.sd = strided;
+        m.renormalize = renormalize != 0;
+        m.active = active;
+        m.R = in16(R);
+        m.ldres = ldr;
+        m.Y = out16(Y);
+        m.ldy = ldy;
+        m.index = topk_index;
+        m.weight = topk_weight;
+        return moe(m, T, E, topk, D, F, static_cast<cudaStream_t>(stream));
+    });
+}
 
 sgemm_status_t sgemm(int64_t M, int64_t N, int64_t K, float alpha, const float *A, int64_t lda,
                      const float *B, int64_t ldb, float beta, float *C, int64_t ldc,
@@ -461,6 +740,8 @@ sgemm_status_t sgemm_release_workspace(void) {
     cudaError_t err3 = sg::release_pack_workspaces();
     cudaError_t err4 = sg::release_host_buffers();
     if (err3 == cudaSuccess) err3 = err4;
+    cudaError_t err5 = sg::release_layer_workspaces();
+    if (err3 == cudaSuccess) err3 = err5;
     cudaError_t err2 = sg::tf32x3_release_workspaces();
     if (err == cudaSuccess) err = err3;
     if (err != cudaSuccess) return fail_cuda("workspace free", err);

@@ -17,8 +17,8 @@
  *   torch CUDA tensors). The library keeps no reference to them after the call returns.
  *   No entry point allocates device memory on every call: workspaces are allocated on first
  *   use (per device and stream: stream-K and split-K partial sums, repacked or transposed
- *   operand copies, the staged product of an unaligned C, the 3xTF32 / TF32 split operands;
- *   per device: the host-memory path's buffers), grown when a larger problem needs more, and
+ *   operand copies, the staged product of an unaligned C, the 3xTF32 / TF32 split operands,
+ *   the layer operators' intermediate values; per device: the host-memory path's buffers), grown when a larger problem needs more, and
  *   kept until sgemm_release_workspace(). sgemm_noalloc() uses none of them.
  * Streams: every compute call is asynchronous on `stream` (a cudaStream_t; NULL means the
  *   legacy default stream) and does not synchronise. Results are visible to later work on
@@ -258,6 +258,94 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
                           const float *A, int64_t lda, const float *B, int64_t ldb,
                           float beta, float *C, int64_t ldc, void *stream);
 
+/*
+ * Layer operators on 16-bit values
+ * --------------------------------
+ * The feed-forward layers around the products above, for models kept in 16 bits: X, W, bias, R,
+ * Y and the rest are bfloat16 or IEEE half values (`dtype`; all of a call's matrices alike),
+ * widened exactly when read. Every sum, softmax statistic and activation is held in fp32 and
+ * each output is rounded once, to nearest even. Conventions (streams, workspaces, errors,
+ * thread safety) are those above; pointers need their type's own alignment only, and 16-byte
+ * aligned matrices with leading dimensions that are multiples of 8 select the TMA path.
+ */
+typedef enum sgemm_dtype {
+    SGEMM_DTYPE_BF16 = 0,
+    SGEMM_DTYPE_F16 = 1
+} sgemm_dtype_t;
+
+/*
+ * A linear layer with its epilogue, for inference and the forward pass of training:
+ *
+ *     Z = X . op(W) + bias,   Y = act(Z) + R
+ *
+ *   X     M x K, ldx >= max(1, K).
+ *   W     SGEMM_OP_N: K x N, ldw >= max(1, N). SGEMM_OP_T: N x K, ldw >= max(1, K).
+ *   bias  N values or NULL.   R  residual, M x N, ldr >= max(1, N), or NULL.
+ *   Y     M x N, ldy >= max(1, N).
+ *   Z     the pre-activation that sgemm_linear_backward reads, M x N, ldz >= max(1, N), or
+ *         NULL. Y is computed from the unrounded Z.
+ * R may be Y itself (same pointer and leading dimension: the residual is updated in place);
+ * the outputs must not overlap an input or each other in any other way. M == 0 or N == 0 is a
+ * no-op; K == 0 gives act(bias) + R. X and W may be NULL only when K == 0.
+ */
+sgemm_status_t sgemm_linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                            int64_t K, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                            const void *bias, sgemm_activation_t act, const void *R, int64_t ldr,
+                            void *Y, int64_t ldy, void *Z, int64_t ldz, void *stream);
+
+/*
+ * The gradients of sgemm_linear, from dY = dLoss / dY:
+ *
+ *     dZ = dY * act'(Z),   dX = dZ . op(W)^T,   dW = X^T . dZ (in W's layout),
+ *     db[n] = sum over rows of dZ[., n]          (R's gradient is dY itself)
+ *
+ *   dY    M x N.   Z  the forward pass's pre-activation (may be NULL when act is none).
+ *   X, W  as in sgemm_linear; X is read only for dW, W only for dX (NULL otherwise).
+ *   dX    M x K, dW like W, both of the call's dtype; db N fp32 values. Each may be NULL (not
+ *         computed). With M == 0, dW and db are set to zero; with N == 0, dX is.
+ * act' of ReLU is 0 at z <= 0. db is summed in fp32 from unrounded dZ, in an order that does not
+ * depend on timing. The two products read dZ rounded to the call's dtype, as a separate
+ * activation layer would hand it over: the tensor cores multiply 16-bit values, and a second
+ * product for the rounded-off part would double the work for less than the outputs' own
+ * rounding. With an activation, dZ lives in a workspace of 2 * M * N' bytes (N' = N rounded up
+ * to a multiple of 8). Outputs must not overlap inputs or each other.
+ */
+sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                                     int64_t K, const void *dY, int64_t lddy, const void *Z,
+                                     int64_t ldz, sgemm_activation_t act, const void *X,
+                                     int64_t ldx, const void *W, int64_t ldw, void *dX,
+                                     int64_t lddx, void *dW, int64_t lddw, float *db,
+                                     void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (a decoding batch):
+ *
+ *     s = X . Wr^T,  p = softmax(s),  chosen: the topk experts of largest s, equal scores to
+ *     the lowest index;  w = p of the chosen, divided by their sum when renormalize != 0
+ *     h_e = act(x . Wgate_e^T) * (x . Wup_e^T),  or act(x . Wup_e^T) when Wgate is NULL
+ *     Y   = sum over the chosen of w_e * (h_e . Wdown_e^T) + R
+ *
+ *   T      tokens, 0 .. 64 (more: SGEMM_ERR_UNSUPPORTED).  E  experts, 1 .. 512.
+ *   topk   1 .. min(E, 16).   D  model width.   F  hidden width of one expert.
+ *   X      T x D, ldx >= max(1, D).   Wr  E x D, ldwr >= max(1, D).
+ *   Wgate, Wup   E matrices F x D, leading dimension ldu >= max(1, D), strideu >= F * ldu apart.
+ *   Wdown  E matrices D x F, leading dimension ldd >= max(1, F), strided >= D * ldd apart.
+ *   active T bytes or NULL: a token whose byte is 0 (an idle slot of the batch) chooses no
+ *          expert: its Y is R (or 0), its indices -1, its weights 0, and its X is not used.
+ *   R      T x D, ldr >= max(1, D), or NULL; it may be Y itself.   Y  T x D, ldy >= max(1, D).
+ *   topk_index (int32) and topk_weight (fp32): T x topk each, largest score first, or NULL.
+ * A NaN score counts as the largest and makes its token's weights NaN. Only the chosen experts'
+ * weights are read. The result does not depend on timing, and a token's does not depend on the
+ * values of the other tokens (an infinity or NaN stays in its own row).
+ */
+sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T, int64_t E,
+                         int64_t topk, int64_t D, int64_t F, const void *X, int64_t ldx,
+                         const void *Wr, int64_t ldwr, const void *Wgate, const void *Wup,
+                         int64_t ldu, int64_t strideu, const void *Wdown, int64_t ldd,
+                         int64_t strided, int renormalize, const uint8_t *active, const void *R,
+                         int64_t ldr, void *Y, int64_t ldy, int32_t *topk_index,
+                         float *topk_weight, void *stream);
+
 /* Static text for a status code (never NULL). */
 const char *sgemm_status_string(sgemm_status_t status);
 
@@ -283,8 +371,8 @@ sgemm_status_t sgemm_device_status(void *stream);
 sgemm_status_t sgemm_selftest_bounded_wait(int which, void *stream);
 
 /* Frees every workspace: stream-K and split-K partial sums, repacked and transposed operand
- * copies, TF32 split operands and the host-memory path's buffers (the next call that needs
- * one allocates it again). Synchronises the device first. */
+ * copies, TF32 split operands, the layer operators' buffers and the host-memory path's (the
+ * next call that needs one allocates it again). Synchronises the device first. */
 sgemm_status_t sgemm_release_workspace(void);
 
 /*
