@@ -51,4 +51,22 @@ struct Half16<__half> {
     }
 };
 
+// 8 values (of which the first `count`, 1 to 8, belong to the row) from any 2-byte aligned
+// address, through aligned 4-byte words: only words that hold a value of the row are read. The
+// values past `count` are arbitrary.
+__device__ __forceinline__ uint4 load8_any(const uint16_t *src, int count) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+    if ((a & 15u) == 0 && count == 8) return __ldg(reinterpret_cast<const uint4 *>(src));
+    const int shift = static_cast<int>(a & 2u) >> 1;  // the first word's low half precedes the row
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~static_cast<uintptr_t>(3));
+    uint32_t v[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = 2 * i - shift < count ? __ldg(w + i) : 0u;
+    if (shift) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
+    }
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 }  // namespace sg

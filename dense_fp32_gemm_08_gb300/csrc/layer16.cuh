@@ -29,6 +29,11 @@ struct Gemm16 {
     long long ldz = 0;
 };
 
+// True when TMA can address the matrix's rows: 16-byte aligned base and leading dimension.
+inline bool tma_rows(const void *p, long long ld) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
+}
+
 cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail);
 
 // The elementwise part of the linear layer's gradient: dz = dy * act'(z), M x N, and its
@@ -82,6 +87,7 @@ enum LayerScratch : int {
     kScratchDz = 0,    // the gradient's dz
     kScratchSums = 1,  // partial column sums
     kScratchMoe = 2,   // routing, hidden values and partial sums of the mixture of experts
+    kScratchPack = 3,  // aligned copies of operands TMA cannot address
     kScratchUses
 };
 cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, void **out,

@@ -3,70 +3,58 @@
 #include "epilogue.cuh"
 #include "half16.cuh"
 #include "layer16.cuh"
+#include "pair_gemm16.cuh"
 
 #include <algorithm>
 
 namespace sg {
 namespace {
 
-// ---- D = act(A . B + bias) + res ------------------------------------------------------------
-//
-// A 64 x 64 tile per CTA of 256 threads, 4 x 4 outputs per thread, fp32 FMAs over 16-wide
-// k-tiles in shared memory. Any size, stride and alignment: every load and store is one value.
-constexpr int kTile = 64, kTileK = 16;
-
+// ---- K == 0: D = act(bias) + res ----------------------------------------------------------------
 template <typename T>
-__global__ void __launch_bounds__(256) gemm16_simple_kernel(const Gemm16 g) {
+__global__ void __launch_bounds__(256) no_product_kernel(const Gemm16 g) {
     using H = Half16<T>;
-    __shared__ float As[kTileK][kTile + 1], Bs[kTileK][kTile + 1];
-    const int m0 = blockIdx.y * kTile;
-    const long long n0 = static_cast<long long>(blockIdx.x) * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long arow = g.a_mn ? 1 : g.lda, ak = g.a_mn ? g.lda : 1;
-    const long long bcol = g.b_mn ? 1 : g.ldb, bk = g.b_mn ? g.ldb : 1;
-    for (long long mb = m0; mb < g.M; mb += static_cast<long long>(gridDim.y) * kTile) {
-        float acc[4][4] = {};
-        for (long long k0 = 0; k0 < g.K; k0 += kTileK) {
-            for (int i = threadIdx.x; i < kTile * kTileK; i += 256) {
-                const int ar = g.a_mn ? i % kTile : i / kTileK, akk = g.a_mn ? i / kTile : i % kTileK;
-                const long long m = mb + ar, ka = k0 + akk;
-                As[akk][ar] = m < g.M && ka < g.K ? H::widen(g.A[m * arow + ka * ak]) : 0.0f;
-                const int bc = g.b_mn ? i % kTile : i / kTileK, bkk = g.b_mn ? i / kTile : i % kTileK;
-                const long long n = n0 + bc, kb = k0 + bkk;
-                Bs[bkk][bc] = n < g.N && kb < g.K ? H::widen(g.B[n * bcol + kb * bk]) : 0.0f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kTileK; ++k) {
-                float a[4], b[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a[i] = As[k][ty + 16 * i];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) b[j] = Bs[k][tx + 16 * j];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
-            }
-            __syncthreads();
+    for (long long m = blockIdx.y; m < g.M; m += gridDim.y)
+        for (long long n = blockIdx.x * 256LL + threadIdx.x; n < g.N; n += gridDim.x * 256LL) {
+            const float z = g.bias ? H::widen(g.bias[n]) : 0.0f;
+            if (g.pre) g.pre[m * g.ldz + n] = H::narrow(z);
+            float y = activate(z, g.act);
+            if (g.res) y += H::widen(g.res[m * g.ldr + n]);
+            g.D[m * g.ldd + n] = H::narrow(y);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const long long m = mb + ty + 16 * i;
-            if (m >= g.M) continue;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const long long n = n0 + tx + 16 * j;
-                if (n >= g.N) continue;
-                float z = acc[i][j];
-                if (g.bias) z += H::widen(g.bias[n]);
-                if (g.pre) g.pre[m * g.ldz + n] = H::narrow(z);
-                float y = activate(z, g.act);
-                if (g.res) y += H::widen(g.res[m * g.ldr + n]);
-                g.D[m * g.ldd + n] = H::narrow(y);
-            }
-        }
-    }
+}
+
+// ---- operands TMA cannot address ----------------------------------------------------------------
+//
+// A matrix whose base or leading dimension is not a multiple of 16 bytes is copied once into
+// scratch with an aligned leading dimension, at memory speed, and the product runs on the copy.
+// A thread writes 8 values from the aligned 4-byte words around them.
+struct PackJob {
+    const uint16_t *src;
+    long long ld;
+    uint16_t *dst;
+    long long ldd;
+    int rows, cols, gx, gy;
+};
+
+__global__ void __launch_bounds__(256) pack16_kernel(const PackJob j0, const PackJob j1) {
+    const int first = j0.gx * j0.gy;
+    const bool second = static_cast<int>(blockIdx.x) >= first;
+    const PackJob &j = second ? j1 : j0;
+    const int bid = static_cast<int>(blockIdx.x) - (second ? first : 0);
+    const int bx = bid % j.gx, by = bid / j.gx;
+    for (long long r = by; r < j.rows; r += j.gy)
+        for (long long c = 8 * (bx * 256LL + threadIdx.x); c < j.cols; c += 2048LL * j.gx)
+            *reinterpret_cast<uint4 *>(j.dst + r * j.ldd + c) =
+                load8_any(j.src + r * j.ld + c, static_cast<int>(min(8LL, j.cols - c)));
+}
+
+PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols, uint16_t *dst) {
+    PackJob j{src, ld, dst, (cols + 7LL) / 8 * 8, rows, cols, 0, 0};
+    // About 2,048 CTAs per matrix, each looping over several rows (as the fp32 repack does).
+    j.gx = static_cast<int>(std::min<long long>((cols + 2047LL) / 2048, 8));
+    j.gy = static_cast<int>(std::min<long long>(rows, 2048 / j.gx));
+    return j;
 }
 
 // ---- dz = dy * act'(z) and its column sums --------------------------------------------------
@@ -132,16 +120,50 @@ __global__ void column_sum_kernel(const float *part, int parts, int N, float *db
 }  // namespace
 
 cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    const long long gx = (g.N + static_cast<long long>(kTile) - 1) / kTile;
-    const long long gy = std::min<long long>((g.M + static_cast<long long>(kTile) - 1) / kTile, 65535);
-    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-    if (g.dtype == kBf16)
-        gemm16_simple_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g);
-    else
-        gemm16_simple_kernel<__half><<<grid, 256, 0, stream>>>(g);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
-    return err;
+    cudaError_t err = cudaSuccess;
+    if (g.K == 0) {
+        const dim3 grid(static_cast<unsigned>(std::min<long long>((g.N + 255LL) / 256, 64)),
+                        static_cast<unsigned>(std::min(g.M, 65535)));
+        if (g.dtype == kBf16)
+            no_product_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g);
+        else
+            no_product_kernel<__half><<<grid, 256, 0, stream>>>(g);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
+        return err;
+    }
+    Gemm16 q = g;
+    const bool pack_a = !tma_rows(g.A, g.lda), pack_b = !tma_rows(g.B, g.ldb);
+    if (pack_a || pack_b) {
+        const int ra = g.a_mn ? g.K : g.M, ca = g.a_mn ? g.M : g.K;
+        const int rb = g.b_mn ? g.K : g.N, cb = g.b_mn ? g.N : g.K;
+        const size_t na = pack_a ? static_cast<size_t>(ra) * ((ca + 7LL) / 8 * 8) : 0;
+        const size_t nb = pack_b ? static_cast<size_t>(rb) * ((cb + 7LL) / 8 * 8) : 0;
+        void *ptr = nullptr;
+        err = layer_scratch(kScratchPack, stream, (na + nb) * 2, &ptr, detail);
+        if (err != cudaSuccess) return err;
+        uint16_t *dst = static_cast<uint16_t *>(ptr);
+        PackJob jobs[2] = {};
+        int n = 0;
+        if (pack_a) {
+            jobs[n] = pack_job(g.A, g.lda, ra, ca, dst);
+            q.A = dst;
+            q.lda = jobs[n++].ldd;
+        }
+        if (pack_b) {
+            jobs[n] = pack_job(g.B, g.ldb, rb, cb, dst + na);
+            q.B = dst + na;
+            q.ldb = jobs[n++].ldd;
+        }
+        const int blocks = jobs[0].gx * jobs[0].gy + jobs[1].gx * jobs[1].gy;
+        pack16_kernel<<<blocks, 256, 0, stream>>>(jobs[0], jobs[1]);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) {
+            *detail = "repacking kernel launch failed";
+            return err;
+        }
+    }
+    return pair_gemm16_launch(q, stream, detail);
 }
 
 cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **detail) {

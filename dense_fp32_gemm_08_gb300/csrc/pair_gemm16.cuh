@@ -1,0 +1,19 @@
+// pair_gemm16.cuh: the CTA-pair tensor-core product and the tensor maps of 16-bit matrices.
+#pragma once
+
+#include <cuda.h>
+
+#include "layer16.cuh"
+
+namespace sg {
+
+// Tensor map of a rows x cols matrix of 16-bit values (cols contiguous, leading dimension ld),
+// or, with depth > 0, of `depth` such matrices `stride` values apart; values outside read as 0.
+bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,
+                   long long ld, int box_cols, int box_rows, int swizzle_bytes, long long depth = 0,
+                   long long stride = 0);
+
+// A and B must satisfy tma_rows; K > 0. The other matrices may have any alignment.
+cudaError_t pair_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail);
+
+}  // namespace sg

@@ -367,8 +367,10 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
     const uint16_t *dz = in16(dY);
     long long lddz = lddy;
     cudaError_t err = cudaSuccess;
-    const bool products = want_dx || want_dw;
-    if (N > 0 && (want_db || (reads && products && act != SGEMM_ACT_NONE))) {
+    // The products read dz: dY * act'(Z), or an aligned copy of a dY that TMA cannot address.
+    const bool make_dz = reads && (want_dx || want_dw) &&
+                         (act != SGEMM_ACT_NONE || !sg::tma_rows(dY, lddy));
+    if (want_db || make_dz) {
         sg::ActGrad a;
         a.dtype = dtype;
         a.M = static_cast<int>(M);
@@ -379,7 +381,7 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         a.ldz = ldz;
         a.act = act;
         a.db = db;
-        if (reads && products && act != SGEMM_ACT_NONE) {
+        if (make_dz) {
             lddz = (N + 7) / 8 * 8;
             void *p = nullptr;
             err = sg::layer_scratch(sg::kScratchDz, stream, static_cast<size_t>(M) * lddz * 2, &p, &detail);
