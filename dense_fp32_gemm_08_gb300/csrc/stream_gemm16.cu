@@ -1,0 +1,339 @@
+// stream_gemm16.cu: D = act(A . B + bias) + res on 16-bit values for few rows of A (tokens), bound
+// by streaming B (the weights) from memory once. The split of the work is in stream16.cuh. Roles
+// of a CTA's 8 warps:
+//   warp 0, lane 0: TMA producer (a 128 x 64 block of weights and the tokens' 64 k values per unit)
+//   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns
+//   warp 2:         TMEM allocation
+//   warps 4..7:     epilogue: lane = output feature, columns = tokens. Whole tiles go from TMEM to
+//                   the epilogue; pieces go to scratch in fp32, and the CTA that completes a tile's
+//                   last piece sums them in the order of k.
+#include "epilogue.cuh"
+#include "layer16.cuh"
+#include "pair_gemm16.cuh"
+#include "stream16.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace sg {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxDevices = 64;
+constexpr size_t kCounterBytes = 64 * 1024;  // one arrival counter per tile
+
+struct StreamParams {
+    int M, N;  // tokens, output features
+    int tiles, KB;
+    UnitSplit split;
+    uint32_t idesc;
+    const uint16_t *bias;
+    int act;
+    const uint16_t *res;
+    long long ldr;
+    uint16_t *D;
+    long long ldd;
+    uint16_t *pre;
+    long long ldz;
+    unsigned int *counters;  // [tiles], zero between calls
+    float *pieces;           // [2 * CTAs][NT][128]
+};
+
+template <int NT>
+struct StreamConfig {
+    static constexpr uint32_t A_BYTES = kStreamRows * kStreamK * 2;
+    static constexpr uint32_t B_BYTES = NT * kStreamK * 2;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int STAGES = static_cast<int>(220 * 1024 / STAGE_BYTES) < 12
+                                      ? static_cast<int>(220 * 1024 / STAGE_BYTES) : 12;
+    static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
+    static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
+};
+
+__device__ __forceinline__ void epilogue_barrier() {
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// 16 columns (tokens m0 .. m0 + 15) of output feature n.
+template <typename T>
+__device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, float (&v)[16]) {
+    using H = Half16<T>;
+    if (n >= p.N) return;
+    const float b = p.bias ? H::widen(p.bias[n]) : 0.0f;
+    const int rows = min(16, p.M - m0);
+    float r[16];
+    if (p.res) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            r[i] = i < rows ? H::widen(p.res[(m0 + i) * p.ldr + n]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if (i >= rows) break;
+        const float z = v[i] + b;
+        if (p.pre) p.pre[(m0 + i) * p.ldz + n] = H::narrow(z);
+        float y = activate(z, p.act);
+        if (p.res) y += r[i];
+        p.D[(m0 + i) * p.ldd + n] = H::narrow(y);
+    }
+}
+
+template <int NT, bool W_MN, typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
+                         const __grid_constant__ CUtensorMap map_x, const StreamParams p) {
+    using C = StreamConfig<NT>;
+    constexpr int STAGES = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES);
+    uint64_t *empty = full + STAGES;
+    uint64_t *acc_full = empty + STAGES;  // [2]
+    uint64_t *acc_free = acc_full + 2;    // [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
+    uint32_t *arrived = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int u0 = p.split.first(blockIdx.x), u1 = p.split.first(blockIdx.x + 1);
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_x);
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(&acc_full[j], 1);
+            mbar_init(&acc_free[j], 4);
+        }
+        mbar_init_fence();
+    }
+    if (warp == 2) tmem_alloc<1>(tmem_slot, C::TMEM_COLS);
+    tc_before_sync();
+    __syncthreads();
+    tc_after_sync();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            RingCursor<STAGES> ring;
+            int issued = 0;
+            int tile = u0 / p.KB, kb = u0 - tile * p.KB;
+            for (int u = u0; u < u1; ++u) {
+                if (issued >= STAGES && !mbar_wait(&empty[ring.stage], ring.parity ^ 1u)) break;
+                uint8_t *sw = smem + ring.stage * C::STAGE_BYTES, *sx = sw + C::A_BYTES;
+                uint64_t *bar = &full[ring.stage];
+                mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+                if (W_MN) {
+                    tma_load_2d(sw, &map_w, bar, tile * kStreamRows, kb * kStreamK);
+                    tma_load_2d(sw + 8192, &map_w, bar, tile * kStreamRows + 64, kb * kStreamK);
+                } else {
+                    tma_load_2d(sw, &map_w, bar, kb * kStreamK, tile * kStreamRows);
+                }
+                tma_load_2d(sx, &map_x, bar, kb * kStreamK, 0);
+                ring.next();
+                ++issued;
+                if (++kb == p.KB) {
+                    kb = 0;
+                    ++tile;
+                }
+            }
+            // Shared memory must outlive every copy: wait (bounded) for the last stages.
+            for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+                if (!mbar_wait(&full[j % STAGES], (j / STAGES) & 1)) break;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            RingCursor<STAGES> ring;
+            int j = -1, kb = u0 % p.KB;
+            bool ok = true;
+            uint32_t d = tmem;
+            for (int u = u0; u < u1 && ok; ++u) {
+                const bool first = u == u0 || kb == 0;
+                if (first) {
+                    ++j;
+                    if (j >= 2 && !mbar_wait(&acc_free[j & 1], ((j >> 1) - 1) & 1)) break;
+                    tc_after_sync();
+                    d = tmem + static_cast<uint32_t>((j & 1) * NT);
+                }
+                if (!mbar_wait(&full[ring.stage], ring.parity)) break;
+                tc_after_sync();
+                const uint32_t sw = smem_addr(smem + ring.stage * C::STAGE_BYTES), sx = sw + C::A_BYTES;
+                const uint64_t dw = W_MN ? desc_mn_major(sw, 8192) : desc_k_major(sw);
+                const uint64_t dx = desc_k_major(sx);
+#pragma unroll
+                for (int k = 0; k < kStreamK / 16; ++k)
+                    mma_16<1>(d, dw + static_cast<uint64_t>(k * (W_MN ? 128 : 2)),
+                              dx + static_cast<uint64_t>(k * 2), p.idesc, !first || k > 0);
+                mma_commit_16<1>(&empty[ring.stage]);
+                ring.next();
+                if (++kb == p.KB) kb = 0;
+                if (kb == 0 || u + 1 == u1) mma_commit_16<1>(&acc_full[j & 1]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int j = 0;
+        bool ok = true;  // after a wait that expired the loop runs on without waiting, so that
+                         // every warp still meets the others at the barriers below
+        for (int u = u0; u < u1; ++j) {
+            const int tile = u / p.KB, kb0 = u - tile * p.KB;
+            const int n_units = min(p.KB - kb0, u1 - u);
+            u += n_units;
+            ok = ok && mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+            tc_after_sync();
+            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * NT);
+            const int n = tile * kStreamRows + row;
+            const bool whole = n_units == p.KB;
+            float *mine = p.pieces + static_cast<size_t>(2 * blockIdx.x + (kb0 == 0 ? 1 : 0)) * NT * kStreamRows + row;
+#pragma unroll 1
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t r[16];
+                tmem_ld_x16(acc + static_cast<uint32_t>(c), r);
+                tmem_ld_wait();
+                if (c + 16 == NT) {
+                    tc_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_free[j & 1]);
+                }
+                if (c >= p.M) continue;
+                if (whole) {
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                    finish16<T>(p, n, c, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < p.M) __stcg(mine + (c + i) * kStreamRows, __uint_as_float(r[i]));
+                }
+            }
+            if (whole) continue;
+            // A piece: count it; whoever completes the tile sums the pieces.
+            const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
+            __threadfence();
+            epilogue_barrier();
+            if (threadIdx.x == 128) {
+                __threadfence();
+                *arrived = atomicAdd(&p.counters[tile], 1u);
+                if (*arrived == static_cast<unsigned>(c1 - c0)) p.counters[tile] = 0;
+            }
+            epilogue_barrier();
+            const bool last = *arrived == static_cast<unsigned>(c1 - c0);
+            if (last) {
+                __threadfence();
+#pragma unroll 1
+                for (int c = 0; c < p.M; c += 16) {
+                    float v[16] = {};
+                    for (int k = c0; k <= c1; ++k) {
+                        const float *piece = p.pieces + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * NT * kStreamRows + row;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < p.M) v[i] += __ldcg(piece + (c + i) * kStreamRows);
+                    }
+                    finish16<T>(p, n, c, v);
+                }
+            }
+            epilogue_barrier();  // `arrived` is read before the next piece overwrites it
+        }
+    }
+
+    __syncwarp();
+    tc_before_sync();
+    __syncthreads();
+    if (warp == 2) {
+        tc_after_sync();
+        tmem_dealloc<1>(tmem, C::TMEM_COLS);
+    }
+}
+
+template <int NT, bool W_MN, typename T>
+cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+    using C = StreamConfig<NT>;
+    auto kernel = stream_gemm16_kernel<NT, W_MN, T>;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        *detail = "cudaGetDevice failed";
+        return err != cudaSuccess ? err : cudaErrorInvalidDevice;
+    }
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t setup[kMaxDevices];
+    static int sms[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(C::SMEM));
+        if (setup[dev] == cudaSuccess)
+            setup[dev] = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+    });
+    if (setup[dev] != cudaSuccess) {
+        *detail = "linear layer kernel set-up failed";
+        return setup[dev];
+    }
+    StreamParams p;
+    p.M = g.M;
+    p.N = g.N;
+    p.tiles = static_cast<int>((g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows);
+    p.KB = static_cast<int>((g.K + static_cast<long long>(kStreamK) - 1) / kStreamK);
+    p.split.total = p.tiles * p.KB;
+    p.split.ctas = std::min(p.split.total, sms[dev]);
+    p.idesc = idesc_16(kStreamRows, NT, Half16<T>::kind, W_MN, false);
+    p.bias = g.bias;
+    p.act = g.act;
+    p.res = g.res;
+    p.ldr = g.ldr;
+    p.D = g.D;
+    p.ldd = g.ldd;
+    p.pre = g.pre;
+    p.ldz = g.ldz;
+    void *ws = nullptr;
+    err = layer_scratch(kScratchStream, stream,
+                        kCounterBytes + static_cast<size_t>(2) * sms[dev] * 256 * kStreamRows * 4, &ws, detail);
+    if (err != cudaSuccess) return err;
+    p.counters = static_cast<unsigned int *>(ws);
+    p.pieces = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
+    CUtensorMap mw, mx;
+    if (!(W_MN ? tensor_map_16(&mw, g.B, g.dtype, g.N, g.K, g.ldb, 64, kStreamK, 128)
+               : tensor_map_16(&mw, g.B, g.dtype, g.K, g.N, g.ldb, kStreamK, kStreamRows, 128)) ||
+        !tensor_map_16(&mx, g.A, g.dtype, g.K, g.M, g.lda, kStreamK, NT, 128)) {
+        *detail = "cuTensorMapEncodeTiled rejected a matrix";
+        return cudaErrorInvalidValue;
+    }
+    kernel<<<p.split.ctas, kThreads, C::SMEM, stream>>>(mw, mx, p);
+    err = cudaGetLastError();
+    if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
+    return err;
+}
+
+template <int NT, typename T>
+cudaError_t launch_major(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+    return g.b_mn ? launch<NT, true, T>(g, stream, detail) : launch<NT, false, T>(g, stream, detail);
+}
+
+template <typename T>
+cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+    if (g.M <= 16) return launch_major<16, T>(g, stream, detail);
+    if (g.M <= 32) return launch_major<32, T>(g, stream, detail);
+    if (g.M <= 64) return launch_major<64, T>(g, stream, detail);
+    if (g.M <= 128) return launch_major<128, T>(g, stream, detail);
+    return launch_major<256, T>(g, stream, detail);
+}
+
+}  // namespace
+
+bool stream_gemm16_supports(const Gemm16 &g) {
+    const long long tiles = (g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows;
+    const long long blocks = (g.K + static_cast<long long>(kStreamK) - 1) / kStreamK;
+    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 4) &&
+           tiles * blocks <= 0x7fffffffLL;
+}
+
+cudaError_t stream_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+    return g.dtype == kBf16 ? launch_width<__nv_bfloat16>(g, stream, detail)
+                            : launch_width<__half>(g, stream, detail);
+}
+
+}  // namespace sg
