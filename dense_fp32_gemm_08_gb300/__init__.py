@@ -332,17 +332,9 @@ def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, tensor_cores: bo
 
 
 # ---- layer operators on 16-bit values ------------------------------------------------------------
-
-def _ptr16(x, dtype):
-    """Address of a CUDA tensor of the call's 16-bit type (or an address, or None)."""
-    if x is None or isinstance(x, int):
-        return x
-    if not x.is_cuda:
-        raise TypeError("tensor arguments must live on a CUDA device")
-    if _DTYPES.get(str(x.dtype)) != dtype:
-        raise TypeError(f"expected every matrix of the call in one 16-bit type, got {x.dtype}")
-    return x.data_ptr()
-
+#
+# A call on a small layer costs the GPU a few microseconds, so these wrappers keep the host's share
+# small: each tensor is looked at once, and the stream is read without building a Stream object.
 
 def _dtype_code(dtype) -> int:
     return dtype if isinstance(dtype, int) else _DTYPES.get(str(dtype), -1)
@@ -350,27 +342,6 @@ def _dtype_code(dtype) -> int:
 
 def _act_code(act) -> int:
     return ACTIVATIONS[act] if isinstance(act, str) else int(act)
-
-
-def sgemm_linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z=None, ldz=0,
-                 stream=None) -> None:
-    """Z = X op(W) + bias, Y = act(Z) + R on bfloat16 or half matrices (asynchronous on
-    ``stream``); dtype is 'bf16' / 'f16', a torch dtype or the enum value. See
-    include/sgemm.h."""
-    dt = _dtype_code(dtype)
-    _check(lib().sgemm_linear(dt, _op(transw), M, N, K, _ptr16(X, dt), ldx, _ptr16(W, dt), ldw,
-                              _ptr16(bias, dt), _act_code(act), _ptr16(R, dt), ldr,
-                              _ptr16(Y, dt), ldy, _ptr16(Z, dt), ldz, _stream(stream)))
-
-
-def sgemm_linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx,
-                          dW, lddw, db, stream=None) -> None:
-    """The gradients of sgemm_linear (see include/sgemm.h); dX, dW and db may be None."""
-    dt = _dtype_code(dtype)
-    _check(lib().sgemm_linear_backward(dt, _op(transw), M, N, K, _ptr16(dY, dt), lddy,
-                                       _ptr16(Z, dt), ldz, _act_code(act), _ptr16(X, dt), ldx,
-                                       _ptr16(W, dt), ldw, _ptr16(dX, dt), lddx, _ptr16(dW, dt),
-                                       lddw, _ptr(db), _stream(stream)))
 
 
 def _ptr_as(x, names):
@@ -384,42 +355,99 @@ def _ptr_as(x, names):
     return x.data_ptr()
 
 
+_NAMES16 = {SGEMM_DTYPE_BF16: ("torch.bfloat16",), SGEMM_DTYPE_F16: ("torch.float16",)}
+
+
+def sgemm_linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z=None, ldz=0,
+                 stream=None) -> None:
+    """Z = X op(W) + bias, Y = act(Z) + R on bfloat16 or half matrices (asynchronous on
+    ``stream``); dtype is 'bf16' / 'f16', a torch dtype or the enum value. See
+    include/sgemm.h."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_linear(dt, _op(transw), M, N, K, _ptr_as(X, names), ldx, _ptr_as(W, names),
+                              ldw, _ptr_as(bias, names), _act_code(act), _ptr_as(R, names), ldr,
+                              _ptr_as(Y, names), ldy, _ptr_as(Z, names), ldz, _stream(stream)))
+
+
+def sgemm_linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx,
+                          dW, lddw, db, stream=None) -> None:
+    """The gradients of sgemm_linear (see include/sgemm.h); dX, dW and db may be None."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_linear_backward(dt, _op(transw), M, N, K, _ptr_as(dY, names), lddy,
+                                       _ptr_as(Z, names), ldz, _act_code(act), _ptr_as(X, names),
+                                       ldx, _ptr_as(W, names), ldw, _ptr_as(dX, names), lddx,
+                                       _ptr_as(dW, names), lddw, _ptr(db), _stream(stream)))
+
+
 def sgemm_moe(dtype, act, T, E, topk, D, F, X, ldx, Wr, ldwr, Wgate, Wup, ldu, strideu, Wdown, ldd,
               strided, renormalize, active, R, ldr, Y, ldy, topk_index=None, topk_weight=None,
               stream=None) -> None:
     """A whole mixture-of-experts layer for up to 64 tokens (see include/sgemm.h)."""
     dt = _dtype_code(dtype)
-    _check(lib().sgemm_moe(dt, _act_code(act), T, E, topk, D, F, _ptr16(X, dt), ldx,
-                           _ptr16(Wr, dt), ldwr, _ptr16(Wgate, dt), _ptr16(Wup, dt), ldu, strideu,
-                           _ptr16(Wdown, dt), ldd, strided, int(bool(renormalize)),
-                           _ptr_as(active, ("torch.bool", "torch.uint8")), _ptr16(R, dt), ldr,
-                           _ptr16(Y, dt), ldy, _ptr_as(topk_index, ("torch.int32",)),
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_moe(dt, _act_code(act), T, E, topk, D, F, _ptr_as(X, names), ldx,
+                           _ptr_as(Wr, names), ldwr, _ptr_as(Wgate, names), _ptr_as(Wup, names),
+                           ldu, strideu, _ptr_as(Wdown, names), ldd, strided,
+                           int(bool(renormalize)), _ptr_as(active, ("torch.bool", "torch.uint8")),
+                           _ptr_as(R, names), ldr, _ptr_as(Y, names), ldy,
+                           _ptr_as(topk_index, ("torch.int32",)),
                            _ptr_as(topk_weight, ("torch.float32",)), _stream(stream)))
 
 
-def _ld(t, what):
-    """Leading dimension of a 2-D tensor with contiguous rows."""
-    if t is None:
-        return 0
-    rows, cols = t.shape
-    if t.stride(1) != 1 and cols > 1:
-        raise ValueError(f"{what}: rows must be contiguous")
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols, 1)
+class _Call:
+    """The checks that the tensors of one layer call share: one 16-bit type, one device (the
+    calling thread's current one), contiguous rows."""
 
+    __slots__ = ("dtype", "device", "code")
 
-def _shape(t, shape, what):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{what} must have shape {shape}, got {tuple(t.shape)}")
+    def __init__(self, first):
+        import torch
+        self.dtype, self.device = first.dtype, first.device
+        self.code = SGEMM_DTYPE_BF16 if self.dtype is torch.bfloat16 else SGEMM_DTYPE_F16
+        if self.dtype is not torch.bfloat16 and self.dtype is not torch.float16:
+            raise TypeError(f"expected a bfloat16 or float16 tensor, got {self.dtype}")
 
+    def on_device(self):
+        import torch
+        if self.device.type != "cuda":
+            raise TypeError("tensor arguments must live on a CUDA device")
+        if self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {self.device}, which is not the current device")
 
-def _same_device(first, *rest):
-    """Tensors of one call live on one device, which is the calling thread's current one."""
-    import torch
-    for t in (first, *rest):
-        if t is not None and t.device != first.device:
+    def stream(self, stream):
+        import torch
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
+    def matrix(self, t, rows, cols, what):
+        """(address, leading dimension) of a rows x cols matrix, or (None, 0)."""
+        if t is None:
+            return None, 0
+        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+            raise ValueError(f"{what} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+        ld, inner = t.stride()
+        if inner != 1 and cols > 1:
+            raise ValueError(f"{what}: rows must be contiguous")
+        self.alike(t, what)
+        return t.data_ptr(), ld if rows > 1 else max(ld, cols, 1)
+
+    def vector(self, t, n, what):
+        if t is None:
+            return None
+        if t.dim() != 1 or t.shape[0] != n:
+            raise ValueError(f"{what} must have shape {(n,)}, got {tuple(t.shape)}")
+        if n > 1 and t.stride(0) != 1:
+            raise ValueError(f"{what} must be contiguous")
+        return t.data_ptr()
+
+    def alike(self, t, what):
+        if t.dtype is not self.dtype:
+            raise TypeError(f"{what} is {t.dtype}: every matrix of a call has one 16-bit type")
+        if t.device != self.device:
             raise ValueError("the tensors of a call must be on one device")
-    if first.is_cuda and first.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {first.device}, which is not the current device")
 
 
 def _weight_shape(weight, transw):
@@ -437,21 +465,22 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
     torch.nn.Linear keeps it), 'N' one stored in x out. Returns y, or (y, pre) with the
     pre-activation that ``linear_backward`` reads when ``save_pre``. ``out`` may be
     ``residual`` itself."""
-    import torch
+    call = _Call(x)
     N, K = _weight_shape(weight, transw)
-    if x.dim() != 2 or x.shape[1] != K:
-        raise ValueError(f"x must be 2-D with {K} columns")
     M = x.shape[0]
-    _shape(bias, (N,), "bias")
-    _shape(residual, (M, N), "residual")
-    _shape(out, (M, N), "out")
-    if bias is not None and N > 1 and bias.stride(0) != 1:
-        raise ValueError("bias must be contiguous")
-    _same_device(x, weight, bias, residual, out)
-    y = torch.empty((M, N), dtype=x.dtype, device=x.device) if out is None else out
-    z = torch.empty((M, N), dtype=x.dtype, device=x.device) if save_pre else None
-    sgemm_linear(x.dtype, transw, M, N, K, x, _ld(x, "x"), weight, _ld(weight, "weight"), bias, act,
-                 residual, _ld(residual, "residual"), y, _ld(y, "out"), z, _ld(z, "pre"), stream)
+    px, ldx = call.matrix(x, M, K, "x")
+    pw, ldw = call.matrix(weight, *weight.shape, "weight")
+    pr, ldr = call.matrix(residual, M, N, "residual")
+    pb = call.vector(bias, N, "bias")
+    if bias is not None:
+        call.alike(bias, "bias")
+    y = x.new_empty((M, N)) if out is None else out
+    py, ldy = call.matrix(y, M, N, "out")
+    z = x.new_empty((M, N)) if save_pre else None
+    call.on_device()
+    _check((_lib or lib()).sgemm_linear(
+        call.code, _op(transw), M, N, K, px, ldx, pw, ldw, pb, _act_code(act), pr, ldr, py, ldy,
+        None if z is None else z.data_ptr(), max(N, 1), call.stream(stream)))
     return (y, z) if save_pre else y
 
 
@@ -460,28 +489,35 @@ def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=Tru
     """torch convenience: (dx, dw, db) of ``linear`` from dy and the saved pre-activation
     (None for those not needed; db is float32). The residual's gradient is dy itself."""
     import torch
+    call = _Call(x)
     N, K = _weight_shape(weight, transw)
     M = x.shape[0]
-    _shape(x, (M, K), "x")
-    _shape(dy, (M, N), "dy")
-    _shape(pre, (M, N), "pre")
-    _same_device(x, weight, dy, pre)
-    dx = torch.empty((M, K), dtype=x.dtype, device=x.device) if need_dx else None
-    dw = torch.empty(tuple(weight.shape), dtype=x.dtype, device=x.device) if need_dw else None
-    db = torch.empty(N, dtype=torch.float32, device=x.device) if need_db else None
-    sgemm_linear_backward(x.dtype, transw, M, N, K, dy, _ld(dy, "dy"), pre, _ld(pre, "pre"), act, x,
-                          _ld(x, "x"), weight, _ld(weight, "weight"), dx, _ld(dx, "dx"), dw,
-                          _ld(dw, "dw"), db, stream)
+    px, ldx = call.matrix(x, M, K, "x")
+    pw, ldw = call.matrix(weight, *weight.shape, "weight")
+    pg, ldg = call.matrix(dy, M, N, "dy")
+    pz, ldz = call.matrix(pre, M, N, "pre")
+    dx = x.new_empty((M, K)) if need_dx else None
+    dw = x.new_empty(weight.shape) if need_dw else None
+    db = x.new_empty((N,), dtype=torch.float32) if need_db else None
+    call.on_device()
+    _check((_lib or lib()).sgemm_linear_backward(
+        call.code, _op(transw), M, N, K, pg, ldg, pz, ldz, _act_code(act), px, ldx, pw, ldw,
+        None if dx is None else dx.data_ptr(), max(K, 1),
+        None if dw is None else dw.data_ptr(), max(weight.shape[1], 1),
+        None if db is None else db.data_ptr(), call.stream(stream)))
     return dx, dw, db
 
 
-def _expert_ld(w, what):
-    """(leading dimension, expert stride) of an E x rows x cols tensor."""
-    E, rows, cols = w.shape
-    if w.stride(2) != 1 and cols > 1:
+def _experts(call, w, E, rows, cols, what):
+    """(address, leading dimension, expert stride) of an E x rows x cols tensor."""
+    if w.dim() != 3 or tuple(w.shape) != (E, rows, cols):
+        raise ValueError(f"{what} must have shape {(E, rows, cols)}, got {tuple(w.shape)}")
+    se, ld, inner = w.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{what}: rows must be contiguous")
-    ld = w.stride(1) if rows > 1 else max(w.stride(1), cols, 1)
-    return ld, w.stride(0) if E > 1 else max(w.stride(0), rows * ld)
+    call.alike(w, what)
+    ld = ld if rows > 1 else max(ld, cols, 1)
+    return w.data_ptr(), ld, se if E > 1 else max(se, rows * ld)
 
 
 def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, active=None,
@@ -491,28 +527,34 @@ def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, act
     Returns (y, index, weight) with the chosen experts (int32) and their weights (float32),
     T x topk each."""
     import torch
+    call = _Call(x)
     if w_up.dim() != 3:
         raise ValueError("w_up must be 3-D (experts x hidden x width)")
     E, F, D = w_up.shape
     T = x.shape[0]
-    _shape(x, (T, D), "x")
-    _shape(router, (E, D), "router")
-    _shape(w_gate, (E, F, D), "w_gate")
-    _shape(w_down, (E, D, F), "w_down")
-    _shape(residual, (T, D), "residual")
-    _shape(out, (T, D), "out")
-    _shape(active, (T,), "active")
-    if active is not None and T > 1 and active.stride(0) != 1:
-        raise ValueError("active must be contiguous")
-    _same_device(x, router, w_gate, w_up, w_down, residual, out, active)
-    ldu, su = _expert_ld(w_up, "w_up")
-    if w_gate is not None and _expert_ld(w_gate, "w_gate") != (ldu, su):
-        raise ValueError("w_gate and w_up must have the same strides")
-    ldd, sd = _expert_ld(w_down, "w_down")
-    y = torch.empty((T, D), dtype=x.dtype, device=x.device) if out is None else out
-    index = torch.empty((T, topk), dtype=torch.int32, device=x.device)
-    weight = torch.empty((T, topk), dtype=torch.float32, device=x.device)
-    sgemm_moe(x.dtype, act, T, E, topk, D, F, x, _ld(x, "x"), router, _ld(router, "router"), w_gate,
-              w_up, ldu, su, w_down, ldd, sd, renormalize, active, residual,
-              _ld(residual, "residual"), y, _ld(y, "out"), index, weight, stream)
+    px, ldx = call.matrix(x, T, D, "x")
+    pr, ldr = call.matrix(router, E, D, "router")
+    pu, ldu, su = _experts(call, w_up, E, F, D, "w_up")
+    pg = None
+    if w_gate is not None:
+        pg, ldg, sg = _experts(call, w_gate, E, F, D, "w_gate")
+        if (ldg, sg) != (ldu, su):
+            raise ValueError("w_gate and w_up must have the same strides")
+    pd, ldd, sd = _experts(call, w_down, E, D, F, "w_down")
+    ps, lds = call.matrix(residual, T, D, "residual")
+    pa = call.vector(active, T, "active")
+    if active is not None:
+        if active.dtype is not torch.bool and active.dtype is not torch.uint8:
+            raise TypeError("active must be bool or uint8")
+        if active.device != call.device:
+            raise ValueError("the tensors of a call must be on one device")
+    y = x.new_empty((T, D)) if out is None else out
+    py, ldy = call.matrix(y, T, D, "out")
+    index = x.new_empty((T, topk), dtype=torch.int32)
+    weight = x.new_empty((T, topk), dtype=torch.float32)
+    call.on_device()
+    _check((_lib or lib()).sgemm_moe(
+        call.code, _act_code(act), T, E, topk, D, F, px, ldx, pr, ldr, pg, pu, ldu, su, pd, ldd, sd,
+        int(bool(renormalize)), pa, ps, lds, py, ldy, index.data_ptr(), weight.data_ptr(),
+        call.stream(stream)))
     return y, index, weight

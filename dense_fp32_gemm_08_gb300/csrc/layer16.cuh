@@ -86,12 +86,17 @@ cudaError_t moe16_launch(const Moe16 &m, cudaStream_t stream, const char **detai
 enum LayerScratch : int {
     kScratchDz = 0,    // the gradient's dz
     kScratchSums = 1,  // partial column sums
-    kScratchMoe = 2,   // routing, hidden values and partial sums of the mixture of experts
+    kScratchMoe = 2,   // scores, hidden values and partial sums of the mixture of experts
     kScratchPack = 3,  // aligned copies of operands TMA cannot address
+    kScratchStream = 4,  // arrival counters and partial tiles of the weight-streaming product
+    kScratchMoeSync = 5,  // its barriers and arrival counters
     kScratchUses
 };
 cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, void **out,
                           const char **detail);
 cudaError_t release_layer_workspaces();
+// After a bounded wait expired: counters left by the kernel that gave up are cleared (in stream
+// order) before each scratch buffer's next use.
+void layer_scratch_distrust();
 
 }  // namespace sg

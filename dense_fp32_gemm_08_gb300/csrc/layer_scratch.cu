@@ -13,6 +13,7 @@ struct Entry {
     int use;
     void *ptr;
     size_t bytes;
+    bool distrusted = false;  // to be cleared before its next use
 };
 std::mutex g_mutex;
 std::vector<Entry> g_entries;
@@ -53,8 +54,21 @@ cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, v
             return err;
         }
     }
+    if (e->distrusted) {
+        err = cudaMemsetAsync(e->ptr, 0, e->bytes, stream);
+        if (err != cudaSuccess) {
+            *detail = "layer workspace reset failed";
+            return err;
+        }
+        e->distrusted = false;
+    }
     *out = e->ptr;
     return cudaSuccess;
+}
+
+void layer_scratch_distrust() {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    for (auto &w : g_entries) w.distrusted = w.ptr != nullptr;
 }
 
 cudaError_t release_layer_workspaces() {

@@ -163,7 +163,8 @@ cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **det
             return err;
         }
     }
-    return pair_gemm16_launch(q, stream, detail);
+    return stream_gemm16_supports(q) ? stream_gemm16_launch(q, stream, detail)
+                                     : pair_gemm16_launch(q, stream, detail);
 }
 
 cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **detail) {

@@ -6,20 +6,12 @@
 //   y   = sum_j w_j D_e h_j + residual
 #include "epilogue.cuh"
 #include "half16.cuh"
-#include "layer16.cuh"
+#include "moe16.cuh"
 
 #include <algorithm>
 
 namespace sg {
 namespace {
-
-// Order of the router's scores as unsigned integers, with the index below it so that equal
-// scores go to the lowest expert: NaN above everything, -0 equal to +0.
-__device__ __forceinline__ unsigned long long score_key(float s, int e) {
-    unsigned int u = __float_as_uint(s == 0.0f ? 0.0f : s);
-    u = s != s ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - static_cast<unsigned>(e));
-}
 
 // One CTA per token: the scores (a warp per expert in turn), then the k largest and their
 // weights by the first warp.
@@ -53,7 +45,7 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const Moe16 m, int *ind
     for (int j = 0; j < m.k; ++j) {
         unsigned long long best = 0;
         for (int e = lane; e < m.E; e += 32) {
-            const unsigned long long key = score_key(score[e], e);
+            const unsigned long long key = moe_score_key(score[e], e);
             if (key < below && key > best) best = key;
         }
         for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
@@ -141,7 +133,8 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
     moe_router_kernel<T><<<m.T, 256, 0, stream>>>(m, index, weight);
     if (m.F > 0)
         moe_up_kernel<T><<<dim3((m.F + 7) / 8, static_cast<unsigned>(pairs)), 256, 0, stream>>>(m, index, h);
-    moe_down_kernel<T><<<dim3((m.D + 7) / 8, m.T), 256, 0, stream>>>(m, index, weight, h);
+    if (m.D > 0)
+        moe_down_kernel<T><<<dim3((m.D + 7) / 8, m.T), 256, 0, stream>>>(m, index, weight, h);
     err = cudaGetLastError();
     if (err != cudaSuccess) *detail = "mixture-of-experts kernel launch failed";
     return err;
@@ -150,6 +143,7 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
 }  // namespace
 
 cudaError_t moe16_launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
+    if (moe_stream_supports(m)) return moe_stream_launch(m, stream, detail);
     return m.dtype == kBf16 ? launch<__nv_bfloat16>(m, stream, detail) : launch<__half>(m, stream, detail);
 }
 

@@ -1,0 +1,25 @@
+// moe16.cuh: parts shared by the mixture-of-experts kernels.
+#pragma once
+
+#include "layer16.cuh"
+
+namespace sg {
+
+// Order of the router's scores as unsigned integers, with the index below it so that equal
+// scores go to the lowest expert: NaN above everything, -0 equal to +0.
+__device__ __forceinline__ unsigned long long moe_score_key(float s, int e) {
+    unsigned int u = __float_as_uint(s == 0.0f ? 0.0f : s);
+    u = s != s ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - static_cast<unsigned>(e));
+}
+// The score of a key (NaN gives a NaN).
+__device__ __forceinline__ float moe_key_score(unsigned long long key) {
+    const unsigned int u = static_cast<unsigned int>(key >> 32);
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+
+// The fused kernel: needs operands TMA can address.
+bool moe_stream_supports(const Moe16 &m);
+cudaError_t moe_stream_launch(const Moe16 &m, cudaStream_t stream, const char **detail);
+
+}  // namespace sg

@@ -728,8 +728,10 @@ sgemm_status_t sgemm_device_status(void *stream_ptr) {
     cudaError_t err = cudaStreamSynchronize(stream);
     if (err != cudaSuccess) return fail_cuda("stream synchronize", err);
     const unsigned int word = sg::take_fault_words(stream);
-    if (word & sg::kFaultTimeout)
+    if (word & sg::kFaultTimeout) {
+        sg::layer_scratch_distrust();
         return fail(SGEMM_ERR_TIMEOUT, "a bounded wait inside a kernel expired");
+    }
     return SGEMM_OK;
 }
 
