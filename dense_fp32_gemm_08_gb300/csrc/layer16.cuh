@@ -90,6 +90,7 @@ enum LayerScratch : int {
     kScratchPack = 3,  // aligned copies of operands TMA cannot address
     kScratchStream = 4,  // arrival counters and partial tiles of the weight-streaming product
     kScratchMoeSync = 5,  // its barriers and arrival counters
+    kScratchSumSync = 6,  // arrival counters of the column sums
     kScratchUses
 };
 cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, void **out,

@@ -1,6 +1,6 @@
 // linear16.cu: the linear layer on 16-bit values, Y = act(X op(W) + b) + R, and the products
 // and reductions of its gradient.
-#include "epilogue.cuh"
+#include "activation16.cuh"
 #include "half16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
@@ -18,7 +18,8 @@ __global__ void __launch_bounds__(256) no_product_kernel(const Gemm16 g) {
         for (long long n = blockIdx.x * 256LL + threadIdx.x; n < g.N; n += gridDim.x * 256LL) {
             const float z = g.bias ? H::widen(g.bias[n]) : 0.0f;
             if (g.pre) g.pre[m * g.ldz + n] = H::narrow(z);
-            float y = activate(z, g.act);
+            float y = z;
+            with_activation(g.act, [&](auto act) { y = activate16<decltype(act)::value>(z); });
             if (g.res) y += H::widen(g.res[m * g.ldr + n]);
             g.D[m * g.ldd + n] = H::narrow(y);
         }
@@ -58,63 +59,102 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols, uint16_t
 }
 
 // ---- dz = dy * act'(z) and its column sums --------------------------------------------------
+//
+// Bound by memory (two matrices read, one written). A CTA covers 256 columns and `rows` rows: a
+// thread 8 columns (16 bytes) of every eighth row, four rows' loads in flight at once. Its 8 fp32
+// sums are added over the CTA's 8 threads of a column in a fixed order into part[row block][n], and
+// the CTA that completes a column block's last part (a count in memory; nothing waits) adds the
+// parts in ascending order, so that db does not depend on timing.
+constexpr int kGradCols = 256;
 
-// act'(z) * g. ReLU selects, so that an infinite gradient behind a closed gate gives zero.
-__device__ __forceinline__ float activate_grad(float z, float g, int act) {
-    switch (act) {
-        case kActRelu: return z <= 0.0f ? 0.0f : g;
-        case kActGelu:  // Phi(z) + z phi(z)
-            return g * (0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-                        z * 0.39894228040143268f * expf(-0.5f * z * z));
-        case kActGeluTanh: {
-            const float t = tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z));
-            const float du = 0.79788456080286536f * (1.0f + 0.134145f * z * z);
-            return g * (0.5f * (1.0f + t) + 0.5f * z * (1.0f - t * t) * du);
-        }
-        case kActSilu: {
-            const float s = 1.0f / (1.0f + expf(-z));
-            return g * s * (1.0f + z * (1.0f - s));
-        }
-        default: return g;
-    }
-}
-
-constexpr int kSumRows = 256;  // rows of one CTA's column sums
-
-// CTA (x, y): columns [32 x, 32 x + 32), rows [kSumRows y, ...). The CTA's sums go to
-// part[y][n]; column_sum_kernel adds them over y in ascending order, so that the result does
-// not depend on the order in which CTAs finish.
-template <typename T>
-__global__ void __launch_bounds__(256) act_grad_kernel(const ActGrad g, float *part) {
+template <typename T, int ACT>
+__device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, long long r1, int c,
+                                              int count, float (&sum)[8]) {
     using H = Half16<T>;
-    __shared__ float sums[8][33];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const long long n = static_cast<long long>(blockIdx.x) * 32 + lane;
-    const long long r0 = static_cast<long long>(blockIdx.y) * kSumRows;
-    const long long r1 = min(r0 + kSumRows, static_cast<long long>(g.M));
-    float sum = 0.0f;
-    if (n < g.N)
-        for (long long r = r0 + w; r < r1; r += 8) {
-            float v = H::widen(g.dy[r * g.lddy + n]);
-            if (g.act != kActNone) v = activate_grad(H::widen(g.z[r * g.ldz + n]), v, g.act);
-            if (g.dz) g.dz[r * g.lddz + n] = H::narrow(v);
-            sum = __fadd_rn(sum, v);  // never fused with v's last product: one result with and without dz
+    constexpr int UNROLL = 4;
+    for (long long r = r0; r < r1; r += 8 * UNROLL) {
+        uint4 dy[UNROLL], z[UNROLL];
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i)
+            if (r + 8 * i < r1) {
+                dy[i] = load8_any(g.dy + (r + 8 * i) * g.lddy + c, count);
+                if (ACT != kActNone) z[i] = load8_any(g.z + (r + 8 * i) * g.ldz + c, count);
+            }
+#pragma unroll
+        for (int i = 0; i < UNROLL; ++i) {
+            if (r + 8 * i >= r1) break;
+            const uint32_t d4[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w};
+            uint32_t out[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float2 v = H::widen2(d4[q]);
+                if (ACT != kActNone) {
+                    const uint32_t z4[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
+                    const float2 zv = H::widen2(z4[q]);
+                    v.x = activate16_grad<ACT>(zv.x, v.x);
+                    v.y = activate16_grad<ACT>(zv.y, v.y);
+                }
+                // Never fused with the products before them: the same sums with and without dz.
+                sum[2 * q] = __fadd_rn(sum[2 * q], v.x);
+                sum[2 * q + 1] = __fadd_rn(sum[2 * q + 1], v.y);
+                out[q] = H::narrow2(v.x, v.y);
+            }
+            // dz's rows are padded to 16 bytes: the values past N land in the padding.
+            if (g.dz)
+                *reinterpret_cast<uint4 *>(g.dz + (r + 8 * i) * g.lddz + c) =
+                    make_uint4(out[0], out[1], out[2], out[3]);
         }
-    if (!part) return;
-    sums[w][lane] = sum;
-    __syncthreads();
-    if (w == 0 && n < g.N) {
-        for (int i = 1; i < 8; ++i) sum += sums[i][lane];
-        part[static_cast<long long>(blockIdx.y) * g.N + n] = sum;
     }
 }
 
-__global__ void column_sum_kernel(const float *part, int parts, int N, float *db) {
-    const long long n = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (n >= N) return;
-    float s = 0.0f;
-    for (int i = 0; i < parts; ++i) s += part[static_cast<long long>(i) * N + n];
-    db[n] = s;
+template <typename T>
+__global__ void __launch_bounds__(256) act_grad_kernel(const ActGrad g, int rows, float *part,
+                                                       unsigned int *counters) {
+    __shared__ float sums[8][kGradCols];
+    __shared__ unsigned int arrived;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * kGradCols + lane * 8;
+    const int count = min(8, g.N - c);
+    const long long r0 = static_cast<long long>(blockIdx.y) * rows;
+    const long long r1 = min(r0 + rows, static_cast<long long>(g.M));
+    float sum[8] = {};
+    if (count > 0)
+        with_activation(g.act, [&](auto act) {
+            act_grad_rows<T, decltype(act)::value>(g, r0 + w, r1, c, count, sum);
+        });
+    if (!g.db) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[w][lane * 8 + i] = sum[i];
+    __syncthreads();
+    const int n = blockIdx.x * kGradCols + threadIdx.x;
+    float s = sums[0][threadIdx.x];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += sums[i][threadIdx.x];
+    const int parts = gridDim.y;
+    if (parts == 1) {
+        if (n < g.N) g.db[n] = s;
+        return;
+    }
+    if (n < g.N) __stcg(part + static_cast<long long>(blockIdx.y) * g.N + n, s);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        __threadfence();
+        arrived = atomicAdd(&counters[blockIdx.x], 1u);
+        if (arrived == static_cast<unsigned>(parts - 1)) counters[blockIdx.x] = 0;
+    }
+    __syncthreads();
+    if (arrived != static_cast<unsigned>(parts - 1) || n >= g.N) return;
+    __threadfence();
+    s = 0.0f;
+#pragma unroll 16
+    for (int i = 0; i < parts; ++i) s += __ldcg(part + static_cast<long long>(i) * g.N + n);
+    g.db[n] = s;
+}
+
+__global__ void zero_kernel(float *p, int n) {
+    const long long i = blockIdx.x * 256LL + threadIdx.x;
+    if (i < n) p[i] = 0.0f;
 }
 
 }  // namespace
@@ -168,30 +208,36 @@ cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **det
 }
 
 cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **detail) {
-    const int parts = static_cast<int>((g.M + static_cast<long long>(kSumRows) - 1) / kSumRows);
-    float *part = nullptr;
     cudaError_t err = cudaSuccess;
-    if (g.db && g.M > 0) {
-        void *p = nullptr;
-        err = layer_scratch(kScratchSums, stream,
-                            static_cast<size_t>(parts) * static_cast<size_t>(g.N) * 4, &p, detail);
-        if (err != cudaSuccess) return err;
-        part = static_cast<float *>(p);
-    }
-    if (g.M > 0) {
-        if (parts > 65535) {
-            *detail = "too many rows";
-            return cudaErrorInvalidValue;
+    if (g.M == 0) {
+        zero_kernel<<<static_cast<unsigned>((g.N + 255LL) / 256), 256, 0, stream>>>(g.db, g.N);
+    } else {
+        // Rows per CTA: about 8 CTAs of 256 threads per SM and three rounds of them, in 8 to 256
+        // rows (few enough parts to add; 16384 x 14336: 64 parts of 256 rows).
+        const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
+        const long long want = std::max<long long>(1, 3 * 8 * 152 / blocks);
+        long long rows = (g.M + want - 1) / want;
+        rows = std::min<long long>(256, (rows + 7) / 8 * 8);
+        rows = std::max(rows, (g.M + 65534LL) / 65535);
+        const int parts = static_cast<int>((g.M + rows - 1) / rows);
+        float *part = nullptr;
+        unsigned int *counters = nullptr;
+        if (g.db && parts > 1) {
+            void *p = nullptr, *q = nullptr;
+            err = layer_scratch(kScratchSums, stream,
+                                static_cast<size_t>(parts) * static_cast<size_t>(g.N) * 4, &p, detail);
+            if (err == cudaSuccess)
+                err = layer_scratch(kScratchSumSync, stream, static_cast<size_t>(blocks) * 4, &q, detail);
+            if (err != cudaSuccess) return err;
+            part = static_cast<float *>(p);
+            counters = static_cast<unsigned int *>(q);
         }
-        const dim3 grid(static_cast<unsigned>((g.N + 31LL) / 32), static_cast<unsigned>(parts));
+        const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
         if (g.dtype == kBf16)
-            act_grad_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g, part);
+            act_grad_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g, static_cast<int>(rows), part, counters);
         else
-            act_grad_kernel<__half><<<grid, 256, 0, stream>>>(g, part);
+            act_grad_kernel<__half><<<grid, 256, 0, stream>>>(g, static_cast<int>(rows), part, counters);
     }
-    if (g.db)
-        column_sum_kernel<<<static_cast<unsigned>((g.N + 255LL) / 256), 256, 0, stream>>>(
-            part, g.M > 0 ? parts : 0, g.N, g.db);
     err = cudaGetLastError();
     if (err != cudaSuccess) *detail = "gradient kernel launch failed";
     return err;

@@ -16,7 +16,7 @@
 //
 // h is rounded to the call's 16-bit type, as the tensor cores need it and as a layer computed in
 // separate products would hold it; every sum is in fp32, cut tiles are summed in the order of k.
-#include "epilogue.cuh"
+#include "activation16.cuh"
 #include "layer16.cuh"
 #include "moe16.cuh"
 #include "pair_gemm16.cuh"
@@ -430,12 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // h of expert e, hidden value f, tokens c .. c + 15
         auto emit = [&](int e, int f, int c, const float(&g)[16], const float(&v)[16]) {
             const unsigned long long mask = route.mask[e];
+            float x[16];
+            with_activation(m.act, [&](auto a) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[i] = GATED ? activate16<decltype(a)::value>(g[i]) * v[i]
+                                 : activate16<decltype(a)::value>(v[i]);
+            });
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 if (!((mask >> (c + i)) & 1ull) || f >= m.F) continue;
                 const int slot = route.offset[e] + __popcll(mask & ((1ull << (c + i)) - 1ull));
-                const float x = GATED ? activate(g[i], m.act) * v[i] : activate(v[i], m.act);
-                p.h[slot * p.ldh + f] = H::narrow(x);
+                p.h[slot * p.ldh + f] = H::narrow(x[i]);
             }
         };
         for (int u = up0; u < up1; ++j) {

@@ -23,7 +23,7 @@
 //
 // Every wait is bounded (ptx.cuh); a wait that expires ends the role, and the CTAs still meet at
 // the final cluster barrier and free their TMEM.
-#include "epilogue.cuh"
+#include "activation16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
 #include "raster.cuh"
@@ -98,19 +98,11 @@ __device__ __forceinline__ uint32_t store_chunk(int r, int c) {
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-template <int ACT>
-__device__ __forceinline__ void activate32(float (&v)[32]) {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = activate(v[i], ACT);
-}
 __device__ __forceinline__ void activate32(float (&v)[32], int act) {
-    switch (act) {
-        case kActRelu: activate32<kActRelu>(v); break;
-        case kActGelu: activate32<kActGelu>(v); break;
-        case kActGeluTanh: activate32<kActGeluTanh>(v); break;
-        case kActSilu: activate32<kActSilu>(v); break;
-        default: break;
-    }
+    with_activation(act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = activate16<decltype(a)::value>(v[i]);
+    });
 }
 
 // One warp's 32 x 32 block of an output at (row0, col0): v is lane r's row. `buf` is free (no

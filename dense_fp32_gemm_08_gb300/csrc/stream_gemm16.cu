@@ -7,7 +7,7 @@
 //   warps 4..7:     epilogue: lane = output feature, columns = tokens. Whole tiles go from TMEM to
 //                   the epilogue; pieces go to scratch in fp32, and the CTA that completes a tile's
 //                   last piece sums them in the order of k.
-#include "epilogue.cuh"
+#include "activation16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
 #include "stream16.cuh"
@@ -69,13 +69,16 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        if (i >= rows) break;
-        const float z = v[i] + b;
-        if (p.pre) p.pre[(m0 + i) * p.ldz + n] = H::narrow(z);
-        float y = activate(z, p.act);
-        if (p.res) y += r[i];
-        p.D[(m0 + i) * p.ldd + n] = H::narrow(y);
+        v[i] += b;
+        if (p.pre && i < rows) p.pre[(m0 + i) * p.ldz + n] = H::narrow(v[i]);
     }
+    with_activation(p.act, [&](auto a) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = activate16<decltype(a)::value>(v[i]);
+    });
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < rows) p.D[(m0 + i) * p.ldd + n] = H::narrow(p.res ? v[i] + r[i] : v[i]);
 }
 
 template <int NT, bool W_MN, typename T>
