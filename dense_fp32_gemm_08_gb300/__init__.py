@@ -396,66 +396,72 @@ def sgemm_moe(dtype, act, T, E, topk, D, F, X, ldx, Wr, ldwr, Wgate, Wup, ldu, s
                            _ptr_as(topk_weight, ("torch.float32",)), _stream(stream)))
 
 
-class _Call:
-    """The checks that the tensors of one layer call share: one 16-bit type, one device (the
-    calling thread's current one), contiguous rows."""
+_torch = None
+_CODES: dict = {}
 
-    __slots__ = ("dtype", "device", "code")
 
-    def __init__(self, first):
-        import torch
-        self.dtype, self.device = first.dtype, first.device
-        self.code = SGEMM_DTYPE_BF16 if self.dtype is torch.bfloat16 else SGEMM_DTYPE_F16
-        if self.dtype is not torch.bfloat16 and self.dtype is not torch.float16:
-            raise TypeError(f"expected a bfloat16 or float16 tensor, got {self.dtype}")
+def _setup():
+    """torch, imported on first use (the C ABI's wrappers above work without it)."""
+    global _torch
+    import torch
+    _CODES[torch.bfloat16] = SGEMM_DTYPE_BF16
+    _CODES[torch.float16] = SGEMM_DTYPE_F16
+    _torch = torch
+    return torch
 
-    def on_device(self):
-        import torch
-        if self.device.type != "cuda":
-            raise TypeError("tensor arguments must live on a CUDA device")
-        if self.device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {self.device}, which is not the current device")
 
-    def stream(self, stream):
-        import torch
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self.device.index)
-        return stream if isinstance(stream, int) else stream.cuda_stream
+def _begin(x):
+    """(torch, dtype, device, dtype code) of a call, from its first tensor."""
+    torch = _torch or _setup()
+    code = _CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"expected a bfloat16 or float16 tensor, got {x.dtype}")
+    return torch, x.dtype, x.device, code
 
-    def matrix(self, t, rows, cols, what):
-        """(address, leading dimension) of a rows x cols matrix, or (None, 0)."""
-        if t is None:
-            return None, 0
-        if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-            raise ValueError(f"{what} must have shape {(rows, cols)}, got {tuple(t.shape)}")
-        ld, inner = t.stride()
-        if inner != 1 and cols > 1:
-            raise ValueError(f"{what}: rows must be contiguous")
-        self.alike(t, what)
-        return t.data_ptr(), ld if rows > 1 else max(ld, cols, 1)
 
-    def vector(self, t, n, what):
-        if t is None:
-            return None
-        if t.dim() != 1 or t.shape[0] != n:
-            raise ValueError(f"{what} must have shape {(n,)}, got {tuple(t.shape)}")
-        if n > 1 and t.stride(0) != 1:
-            raise ValueError(f"{what} must be contiguous")
-        return t.data_ptr()
+def _queue(torch, device, stream):
+    """The stream's address; the tensors must be on the calling thread's current device."""
+    index = device.index
+    if device.type != "cuda":
+        raise TypeError("tensor arguments must live on a CUDA device")
+    if index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {device}, which is not the current device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
-    def alike(self, t, what):
-        if t.dtype is not self.dtype:
-            raise TypeError(f"{what} is {t.dtype}: every matrix of a call has one 16-bit type")
-        if t.device != self.device:
-            raise ValueError("the tensors of a call must be on one device")
+
+def _matrix(t, rows, cols, dtype, device, what):
+    """(address, leading dimension) of a rows x cols matrix of the call's type and device."""
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} is {t.dtype}: every matrix of a call has one 16-bit type")
+    if t.device != device:
+        raise ValueError("the tensors of a call must be on one device")
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    return t.data_ptr(), (ld if rows > 1 else max(ld, cols, 1))
+
+
+def _vector(t, n, device, what):
+    if t.shape != (n,):
+        raise ValueError(f"{what} must have shape {(n,)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError("the tensors of a call must be on one device")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def _weight_shape(weight, transw):
-    """(N, K) of a weight stored N x K ('T') or K x N ('N')."""
+    """(N, K, transw code) of a weight stored N x K ('T') or K x N ('N')."""
     if weight.dim() != 2:
         raise ValueError("weight must be 2-D")
     a, b = weight.shape
-    return (a, b) if _op(transw) == SGEMM_OP_T else (b, a)
+    op = SGEMM_OP_T if transw == "T" else _op(transw)
+    return (a, b, op) if op == SGEMM_OP_T else (b, a, op)
 
 
 def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre=False, out=None,
@@ -465,59 +471,78 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
     torch.nn.Linear keeps it), 'N' one stored in x out. Returns y, or (y, pre) with the
     pre-activation that ``linear_backward`` reads when ``save_pre``. ``out`` may be
     ``residual`` itself."""
-    call = _Call(x)
-    N, K = _weight_shape(weight, transw)
+    torch, dtype, device, code = _begin(x)
+    N, K, op = _weight_shape(weight, transw)
     M = x.shape[0]
-    px, ldx = call.matrix(x, M, K, "x")
-    pw, ldw = call.matrix(weight, *weight.shape, "weight")
-    pr, ldr = call.matrix(residual, M, N, "residual")
-    pb = call.vector(bias, N, "bias")
+    px, ldx = _matrix(x, M, K, dtype, device, "x")
+    pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
+    pb = pr = pz = None
+    ldr = 0
     if bias is not None:
-        call.alike(bias, "bias")
-    y = x.new_empty((M, N)) if out is None else out
-    py, ldy = call.matrix(y, M, N, "out")
-    z = x.new_empty((M, N)) if save_pre else None
-    call.on_device()
-    _check((_lib or lib()).sgemm_linear(
-        call.code, _op(transw), M, N, K, px, ldx, pw, ldw, pb, _act_code(act), pr, ldr, py, ldy,
-        None if z is None else z.data_ptr(), max(N, 1), call.stream(stream)))
-    return (y, z) if save_pre else y
+        if bias.dtype is not dtype:
+            raise TypeError(f"bias is {bias.dtype}: every matrix of a call has one 16-bit type")
+        pb = _vector(bias, N, device, "bias")
+    if residual is not None:
+        pr, ldr = _matrix(residual, M, N, dtype, device, "residual")
+    if out is None:
+        out, ldy = torch.empty((M, N), dtype=dtype, device=device), max(N, 1)
+        py = out.data_ptr()
+    else:
+        py, ldy = _matrix(out, M, N, dtype, device, "out")
+    if save_pre:
+        pre = torch.empty((M, N), dtype=dtype, device=device)
+        pz = pre.data_ptr()
+    status = (_lib or lib()).sgemm_linear(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act), pr,
+                                          ldr, py, ldy, pz, max(N, 1), _queue(torch, device, stream))
+    if status:
+        _check(status)
+    return (out, pre) if save_pre else out
 
 
 def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=True, need_dw=True,
                     need_db=True, stream=None):
     """torch convenience: (dx, dw, db) of ``linear`` from dy and the saved pre-activation
     (None for those not needed; db is float32). The residual's gradient is dy itself."""
-    import torch
-    call = _Call(x)
-    N, K = _weight_shape(weight, transw)
+    torch, dtype, device, code = _begin(x)
+    N, K, op = _weight_shape(weight, transw)
     M = x.shape[0]
-    px, ldx = call.matrix(x, M, K, "x")
-    pw, ldw = call.matrix(weight, *weight.shape, "weight")
-    pg, ldg = call.matrix(dy, M, N, "dy")
-    pz, ldz = call.matrix(pre, M, N, "pre")
-    dx = x.new_empty((M, K)) if need_dx else None
-    dw = x.new_empty(weight.shape) if need_dw else None
-    db = x.new_empty((N,), dtype=torch.float32) if need_db else None
-    call.on_device()
-    _check((_lib or lib()).sgemm_linear_backward(
-        call.code, _op(transw), M, N, K, pg, ldg, pz, ldz, _act_code(act), px, ldx, pw, ldw,
-        None if dx is None else dx.data_ptr(), max(K, 1),
-        None if dw is None else dw.data_ptr(), max(weight.shape[1], 1),
-        None if db is None else db.data_ptr(), call.stream(stream)))
+    px, ldx = _matrix(x, M, K, dtype, device, "x")
+    pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
+    pg, ldg = _matrix(dy, M, N, dtype, device, "dy")
+    pz, ldz = (None, 0) if pre is None else _matrix(pre, M, N, dtype, device, "pre")
+    queue = _queue(torch, device, stream)
+    dx = dw = db = px_out = pw_out = pb_out = None
+    if need_dx:
+        dx = torch.empty((M, K), dtype=dtype, device=device)
+        px_out = dx.data_ptr()
+    if need_dw:
+        dw = torch.empty(weight.shape, dtype=dtype, device=device)
+        pw_out = dw.data_ptr()
+    if need_db:
+        db = torch.empty(N, dtype=torch.float32, device=device)
+        pb_out = db.data_ptr()
+    status = (_lib or lib()).sgemm_linear_backward(code, op, M, N, K, pg, ldg, pz, ldz, _act_code(act), px,
+                                                   ldx, pw, ldw, px_out, max(K, 1), pw_out,
+                                                   max(weight.shape[1], 1), pb_out, queue)
+    if status:
+        _check(status)
     return dx, dw, db
 
 
-def _experts(call, w, E, rows, cols, what):
+def _experts(w, E, rows, cols, dtype, device, what):
     """(address, leading dimension, expert stride) of an E x rows x cols tensor."""
-    if w.dim() != 3 or tuple(w.shape) != (E, rows, cols):
+    if w.shape != (E, rows, cols):
         raise ValueError(f"{what} must have shape {(E, rows, cols)}, got {tuple(w.shape)}")
+    if w.dtype is not dtype:
+        raise TypeError(f"{what} is {w.dtype}: every matrix of a call has one 16-bit type")
+    if w.device != device:
+        raise ValueError("the tensors of a call must be on one device")
     se, ld, inner = w.stride()
     if inner != 1 and cols > 1:
         raise ValueError(f"{what}: rows must be contiguous")
-    call.alike(w, what)
-    ld = ld if rows > 1 else max(ld, cols, 1)
-    return w.data_ptr(), ld, se if E > 1 else max(se, rows * ld)
+    if rows <= 1:
+        ld = max(ld, cols, 1)
+    return w.data_ptr(), ld, (se if E > 1 else max(se, rows * ld))
 
 
 def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, active=None,
@@ -526,35 +551,38 @@ def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, act
     E x D, w_gate (or None) and w_up E x F x D, w_down E x D x F, active T booleans or None.
     Returns (y, index, weight) with the chosen experts (int32) and their weights (float32),
     T x topk each."""
-    import torch
-    call = _Call(x)
+    torch, dtype, device, code = _begin(x)
     if w_up.dim() != 3:
         raise ValueError("w_up must be 3-D (experts x hidden x width)")
     E, F, D = w_up.shape
     T = x.shape[0]
-    px, ldx = call.matrix(x, T, D, "x")
-    pr, ldr = call.matrix(router, E, D, "router")
-    pu, ldu, su = _experts(call, w_up, E, F, D, "w_up")
-    pg = None
+    px, ldx = _matrix(x, T, D, dtype, device, "x")
+    pr, ldr = _matrix(router, E, D, dtype, device, "router")
+    pu, ldu, su = _experts(w_up, E, F, D, dtype, device, "w_up")
+    pg = pa = ps = None
+    lds = 0
     if w_gate is not None:
-        pg, ldg, sg = _experts(call, w_gate, E, F, D, "w_gate")
-        if (ldg, sg) != (ldu, su):
+        pg, *strides = _experts(w_gate, E, F, D, dtype, device, "w_gate")
+        if strides != [ldu, su]:
             raise ValueError("w_gate and w_up must have the same strides")
-    pd, ldd, sd = _experts(call, w_down, E, D, F, "w_down")
-    ps, lds = call.matrix(residual, T, D, "residual")
-    pa = call.vector(active, T, "active")
+    pd, ldd, sd = _experts(w_down, E, D, F, dtype, device, "w_down")
+    if residual is not None:
+        ps, lds = _matrix(residual, T, D, dtype, device, "residual")
     if active is not None:
         if active.dtype is not torch.bool and active.dtype is not torch.uint8:
             raise TypeError("active must be bool or uint8")
-        if active.device != call.device:
-            raise ValueError("the tensors of a call must be on one device")
-    y = x.new_empty((T, D)) if out is None else out
-    py, ldy = call.matrix(y, T, D, "out")
-    index = x.new_empty((T, topk), dtype=torch.int32)
-    weight = x.new_empty((T, topk), dtype=torch.float32)
-    call.on_device()
-    _check((_lib or lib()).sgemm_moe(
-        call.code, _act_code(act), T, E, topk, D, F, px, ldx, pr, ldr, pg, pu, ldu, su, pd, ldd, sd,
-        int(bool(renormalize)), pa, ps, lds, py, ldy, index.data_ptr(), weight.data_ptr(),
-        call.stream(stream)))
-    return y, index, weight
+        pa = _vector(active, T, device, "active")
+    queue = _queue(torch, device, stream)
+    if out is None:
+        out, ldy = torch.empty((T, D), dtype=dtype, device=device), max(D, 1)
+        py = out.data_ptr()
+    else:
+        py, ldy = _matrix(out, T, D, dtype, device, "out")
+    index = torch.empty((T, topk), dtype=torch.int32, device=device)
+    weight = torch.empty((T, topk), dtype=torch.float32, device=device)
+    status = (_lib or lib()).sgemm_moe(code, _act_code(act), T, E, topk, D, F, px, ldx, pr, ldr, pg, pu, ldu,
+                                       su, pd, ldd, sd, 1 if renormalize else 0, pa, ps, lds, py, ldy,
+                                       index.data_ptr(), weight.data_ptr(), queue)
+    if status:
+        _check(status)
+    return out, index, weight

@@ -51,22 +51,29 @@ struct Half16<__half> {
     }
 };
 
-// 8 values (of which the first `count`, 1 to 8, belong to the row) from any 2-byte aligned
-// address, through aligned 4-byte words: only words that hold a value of the row are read. The
-// values past `count` are arbitrary.
-__device__ __forceinline__ uint4 load8_any(const uint16_t *src, int count) {
+// 8 values of a row at any 2-byte aligned address, of which the first `count` (up to 8) belong to
+// the row: first the aligned 4-byte words that hold one of them (load8_words, so that several
+// loads can be under way), then the values from the words (align8; past `count` arbitrary).
+__device__ __forceinline__ void load8_words(uint32_t (&v)[5], const uint16_t *src, int count) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(src);
-    if ((a & 15u) == 0 && count == 8) return __ldg(reinterpret_cast<const uint4 *>(src));
     const int shift = static_cast<int>(a & 2u) >> 1;  // the first word's low half precedes the row
     const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~static_cast<uintptr_t>(3));
-    uint32_t v[5];
 #pragma unroll
-    for (int i = 0; i < 5; ++i) v[i] = 2 * i - shift < count ? __ldg(w + i) : 0u;
-    if (shift) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __funnelshift_r(v[i], v[i + 1], 16);
-    }
+    for (int i = 0; i < 5; ++i)
+        if (2 * i - shift < count) v[i] = __ldg(w + i);
+}
+__device__ __forceinline__ uint4 align8(const uint32_t (&v)[5], const uint16_t *src) {
+    if (reinterpret_cast<uintptr_t>(src) & 2u)
+        return make_uint4(__funnelshift_r(v[0], v[1], 16), __funnelshift_r(v[1], v[2], 16),
+                          __funnelshift_r(v[2], v[3], 16), __funnelshift_r(v[3], v[4], 16));
     return make_uint4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ uint4 load8_any(const uint16_t *src, int count) {
+    if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0 && count == 8)
+        return __ldg(reinterpret_cast<const uint4 *>(src));
+    uint32_t v[5] = {};
+    load8_words(v, src, count);
+    return align8(v, src);
 }
 
 }  // namespace sg

@@ -34,7 +34,37 @@ inline bool tma_rows(const void *p, long long ld) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0;
 }
 
-cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail);
+// Programmatic dependent launch: each kernel of the layer operators lets the stream's next one
+// start its prologue early (grid_dependents) and touches global memory only after the kernels
+// before it have completed (grid_dependency); set_early_start() asks for it at launch.
+__device__ __forceinline__ void grid_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+inline void set_early_start(cudaLaunchAttribute &attr) {
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+}
+template <typename... Params, typename... Args>
+cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem,
+                         cudaStream_t stream, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    set_early_start(attr[0]);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// One or two independent products; the larger kernels run them as one grid.
+constexpr int kMaxProducts = 2;
+cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail);
 
 // The elementwise part of the linear layer's gradient: dz = dy * act'(z), M x N, and its
 // column sums db (fp32), either of them optional. dz == nullptr: only the sums.

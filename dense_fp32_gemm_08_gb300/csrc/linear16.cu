@@ -14,6 +14,8 @@ namespace {
 template <typename T>
 __global__ void __launch_bounds__(256) no_product_kernel(const Gemm16 g) {
     using H = Half16<T>;
+    grid_dependents();
+    grid_dependency();
     for (long long m = blockIdx.y; m < g.M; m += gridDim.y)
         for (long long n = blockIdx.x * 256LL + threadIdx.x; n < g.N; n += gridDim.x * 256LL) {
             const float z = g.bias ? H::widen(g.bias[n]) : 0.0f;
@@ -39,19 +41,31 @@ struct PackJob {
 };
 
 __global__ void __launch_bounds__(256) pack16_kernel(const PackJob j0, const PackJob j1) {
+    grid_dependents();
+    grid_dependency();
     const int first = j0.gx * j0.gy;
     const bool second = static_cast<int>(blockIdx.x) >= first;
     const PackJob &j = second ? j1 : j0;
     const int bid = static_cast<int>(blockIdx.x) - (second ? first : 0);
     const int bx = bid % j.gx, by = bid / j.gx;
-    for (long long r = by; r < j.rows; r += j.gy)
-        for (long long c = 8 * (bx * 256LL + threadIdx.x); c < j.cols; c += 2048LL * j.gx)
-            *reinterpret_cast<uint4 *>(j.dst + r * j.ldd + c) =
-                load8_any(j.src + r * j.ld + c, static_cast<int>(min(8LL, j.cols - c)));
+    // Two rows at a time, so that twice the loads are under way.
+    for (int c = 8 * (bx * 256 + static_cast<int>(threadIdx.x)); c < j.cols; c += 2048 * j.gx) {
+        const int count = min(8, j.cols - c);
+        for (int r = by; r < j.rows; r += 2 * j.gy) {
+            const bool two = r + j.gy < j.rows;
+            const uint16_t *s0 = j.src + r * j.ld + c, *s1 = s0 + j.gy * j.ld;
+            uint32_t v0[5] = {}, v1[5] = {};
+            load8_words(v0, s0, count);
+            if (two) load8_words(v1, s1, count);
+            uint16_t *d = j.dst + r * j.ldd + c;
+            *reinterpret_cast<uint4 *>(d) = align8(v0, s0);
+            if (two) *reinterpret_cast<uint4 *>(d + j.gy * j.ldd) = align8(v1, s1);
+        }
+    }
 }
 
-PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols, uint16_t *dst) {
-    PackJob j{src, ld, dst, (cols + 7LL) / 8 * 8, rows, cols, 0, 0};
+PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols) {
+    PackJob j{src, ld, nullptr, (cols + 7LL) / 8 * 8, rows, cols, 0, 0};
     // About 2,048 CTAs per matrix, each looping over several rows (as the fp32 repack does).
     j.gx = static_cast<int>(std::min<long long>((cols + 2047LL) / 2048, 8));
     j.gy = static_cast<int>(std::min<long long>(rows, 2048 / j.gx));
@@ -67,29 +81,57 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols, uint16_t
 // parts in ascending order, so that db does not depend on timing.
 constexpr int kGradCols = 256;
 
-template <typename T, int ACT>
+template <bool VEC, int W>
+__device__ __forceinline__ void load8_row(uint32_t (&v)[W], const uint16_t *src, int count) {
+    if constexpr (VEC) {
+        const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src));
+        v[0] = q.x;
+        v[1] = q.y;
+        v[2] = q.z;
+        v[3] = q.w;
+    } else {
+        load8_words(v, src, count);
+    }
+}
+template <bool VEC, int W>
+__device__ __forceinline__ void align8_row(uint32_t (&out)[4], const uint32_t (&v)[W], const uint16_t *src) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) out[i] = v[i];
+    } else {
+        const uint4 q = align8(v, src);
+        out[0] = q.x;
+        out[1] = q.y;
+        out[2] = q.z;
+        out[3] = q.w;
+    }
+}
+
+template <typename T, int ACT, bool VEC>
 __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, long long r1, int c,
                                               int count, float (&sum)[8]) {
     using H = Half16<T>;
-    constexpr int UNROLL = 4;
+    constexpr int UNROLL = VEC ? 4 : 2;
     for (long long r = r0; r < r1; r += 8 * UNROLL) {
-        uint4 dy[UNROLL], z[UNROLL];
+        constexpr int W = VEC ? 4 : 5;
+        uint32_t dy[UNROLL][W], z[UNROLL][W];
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i)
             if (r + 8 * i < r1) {
-                dy[i] = load8_any(g.dy + (r + 8 * i) * g.lddy + c, count);
-                if (ACT != kActNone) z[i] = load8_any(g.z + (r + 8 * i) * g.ldz + c, count);
+                load8_row<VEC>(dy[i], g.dy + (r + 8 * i) * g.lddy + c, count);
+                if (ACT != kActNone) load8_row<VEC>(z[i], g.z + (r + 8 * i) * g.ldz + c, count);
             }
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
             if (r + 8 * i >= r1) break;
-            const uint32_t d4[4] = {dy[i].x, dy[i].y, dy[i].z, dy[i].w};
+            uint32_t d4[4], z4[4] = {};
+            align8_row<VEC>(d4, dy[i], g.dy + (r + 8 * i) * g.lddy + c);
+            if (ACT != kActNone) align8_row<VEC>(z4, z[i], g.z + (r + 8 * i) * g.ldz + c);
             uint32_t out[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float2 v = H::widen2(d4[q]);
                 if (ACT != kActNone) {
-                    const uint32_t z4[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
                     const float2 zv = H::widen2(z4[q]);
                     v.x = activate16_grad<ACT>(zv.x, v.x);
                     v.y = activate16_grad<ACT>(zv.y, v.y);
@@ -107,11 +149,14 @@ __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, lo
     }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) act_grad_kernel(const ActGrad g, int rows, float *part,
+// VEC: dy and z allow 16-byte loads (and N is a multiple of 8).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int rows, float *part,
                                                        unsigned int *counters) {
     __shared__ float sums[8][kGradCols];
     __shared__ unsigned int arrived;
+    grid_dependents();
+    grid_dependency();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int c = blockIdx.x * kGradCols + lane * 8;
     const int count = min(8, g.N - c);
@@ -120,7 +165,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGrad g, int rows
     float sum[8] = {};
     if (count > 0)
         with_activation(g.act, [&](auto act) {
-            act_grad_rows<T, decltype(act)::value>(g, r0 + w, r1, c, count, sum);
+            act_grad_rows<T, decltype(act)::value, VEC>(g, r0 + w, r1, c, count, sum);
         });
     if (!g.db) return;
 #pragma unroll
@@ -153,64 +198,85 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGrad g, int rows
 }
 
 __global__ void zero_kernel(float *p, int n) {
+    grid_dependents();
+    grid_dependency();
     const long long i = blockIdx.x * 256LL + threadIdx.x;
     if (i < n) p[i] = 0.0f;
 }
 
 }  // namespace
 
-cudaError_t gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
     cudaError_t err = cudaSuccess;
-    if (g.K == 0) {
+    Gemm16 q[kMaxProducts];
+    int products = 0;
+    for (int i = 0; i < n; ++i) {
+        const Gemm16 &g = list[i];
+        if (g.K > 0) {
+            q[products++] = g;
+            continue;
+        }
         const dim3 grid(static_cast<unsigned>(std::min<long long>((g.N + 255LL) / 256, 64)),
                         static_cast<unsigned>(std::min(g.M, 65535)));
-        if (g.dtype == kBf16)
-            no_product_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g);
-        else
-            no_product_kernel<__half><<<grid, 256, 0, stream>>>(g);
-        err = cudaGetLastError();
-        if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
-        return err;
-    }
-    Gemm16 q = g;
-    const bool pack_a = !tma_rows(g.A, g.lda), pack_b = !tma_rows(g.B, g.ldb);
-    if (pack_a || pack_b) {
-        const int ra = g.a_mn ? g.K : g.M, ca = g.a_mn ? g.M : g.K;
-        const int rb = g.b_mn ? g.K : g.N, cb = g.b_mn ? g.N : g.K;
-        const size_t na = pack_a ? static_cast<size_t>(ra) * ((ca + 7LL) / 8 * 8) : 0;
-        const size_t nb = pack_b ? static_cast<size_t>(rb) * ((cb + 7LL) / 8 * 8) : 0;
-        void *ptr = nullptr;
-        err = layer_scratch(kScratchPack, stream, (na + nb) * 2, &ptr, detail);
-        if (err != cudaSuccess) return err;
-        uint16_t *dst = static_cast<uint16_t *>(ptr);
-        PackJob jobs[2] = {};
-        int n = 0;
-        if (pack_a) {
-            jobs[n] = pack_job(g.A, g.lda, ra, ca, dst);
-            q.A = dst;
-            q.lda = jobs[n++].ldd;
-        }
-        if (pack_b) {
-            jobs[n] = pack_job(g.B, g.ldb, rb, cb, dst + na);
-            q.B = dst + na;
-            q.ldb = jobs[n++].ldd;
-        }
-        const int blocks = jobs[0].gx * jobs[0].gy + jobs[1].gx * jobs[1].gy;
-        pack16_kernel<<<blocks, 256, 0, stream>>>(jobs[0], jobs[1]);
-        err = cudaGetLastError();
+        err = launch_early(g.dtype == kBf16 ? no_product_kernel<__nv_bfloat16> : no_product_kernel<__half>,
+                           grid, 256, 0, stream, g);
         if (err != cudaSuccess) {
-            *detail = "repacking kernel launch failed";
+            *detail = "linear layer kernel launch failed";
             return err;
         }
     }
-    return stream_gemm16_supports(q) ? stream_gemm16_launch(q, stream, detail)
-                                     : pair_gemm16_launch(q, stream, detail);
+    // Aligned copies of the operands TMA cannot address, in one launch.
+    PackJob jobs[2 * kMaxProducts] = {};
+    const uint16_t **base[2 * kMaxProducts];
+    size_t at[2 * kMaxProducts], elems = 0;
+    int n_jobs = 0;
+    auto pack = [&](const uint16_t *&ptr, long long &ld, int rows, int cols) {
+        if (tma_rows(ptr, ld)) return;
+        jobs[n_jobs] = pack_job(ptr, ld, rows, cols);
+        base[n_jobs] = &ptr;
+        at[n_jobs++] = elems;
+        ld = (cols + 7LL) / 8 * 8;
+        elems += static_cast<size_t>(rows) * ld;
+    };
+    for (int i = 0; i < products; ++i) {
+        pack(q[i].A, q[i].lda, q[i].a_mn ? q[i].K : q[i].M, q[i].a_mn ? q[i].M : q[i].K);
+        pack(q[i].B, q[i].ldb, q[i].b_mn ? q[i].K : q[i].N, q[i].b_mn ? q[i].N : q[i].K);
+    }
+    if (n_jobs > 0) {
+        void *ptr = nullptr;
+        err = layer_scratch(kScratchPack, stream, elems * 2, &ptr, detail);
+        if (err != cudaSuccess) return err;
+        for (int i = 0; i < n_jobs; ++i) {
+            jobs[i].dst = static_cast<uint16_t *>(ptr) + at[i];
+            *base[i] = jobs[i].dst;
+        }
+        for (int i = 0; i < n_jobs; i += 2) {
+            const int blocks = jobs[i].gx * jobs[i].gy + jobs[i + 1].gx * jobs[i + 1].gy;
+            err = launch_early(pack16_kernel, dim3(blocks), 256, 0, stream, jobs[i], jobs[i + 1]);
+            if (err != cudaSuccess) {
+                *detail = "repacking kernel launch failed";
+                return err;
+            }
+        }
+    }
+    // Products that stream weights for a few rows go alone; the others share one launch.
+    int together = 0;
+    for (int i = 0; i < products; ++i) {
+        if (stream_gemm16_supports(q[i])) {
+            err = stream_gemm16_launch(q[i], stream, detail);
+            if (err != cudaSuccess) return err;
+        } else {
+            q[together++] = q[i];
+        }
+    }
+    return together > 0 ? pair_gemm16_launch(q, together, stream, detail) : cudaSuccess;
 }
 
 cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **detail) {
     cudaError_t err = cudaSuccess;
     if (g.M == 0) {
-        zero_kernel<<<static_cast<unsigned>((g.N + 255LL) / 256), 256, 0, stream>>>(g.db, g.N);
+        err = launch_early(zero_kernel, dim3(static_cast<unsigned>((g.N + 255LL) / 256)), 256, 0, stream, g.db,
+                           g.N);
     } else {
         // Rows per CTA: about 8 CTAs of 256 threads per SM and three rounds of them, in 8 to 256
         // rows (few enough parts to add; 16384 x 14336: 64 parts of 256 rows).
@@ -233,12 +299,12 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
             counters = static_cast<unsigned int *>(q);
         }
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
-        if (g.dtype == kBf16)
-            act_grad_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(g, static_cast<int>(rows), part, counters);
-        else
-            act_grad_kernel<__half><<<grid, 256, 0, stream>>>(g, static_cast<int>(rows), part, counters);
+        const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) && (g.act == kActNone || tma_rows(g.z, g.ldz));
+        auto kernel = g.dtype == kBf16
+                          ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
+                          : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);
+        err = launch_early(kernel, grid, 256, 0, stream, g, static_cast<int>(rows), part, counters);
     }
-    err = cudaGetLastError();
     if (err != cudaSuccess) *detail = "gradient kernel launch failed";
     return err;
 }

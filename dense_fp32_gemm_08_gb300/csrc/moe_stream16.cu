@@ -665,11 +665,11 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
 
     const long long su = m.E > 1 ? m.su : m.F * m.ldu, sd = m.E > 1 ? m.sd : m.D * m.ldd;
     CUtensorMap mx, mg, mu, md, mh;
-    if (!tensor_map_16(&mx, m.X, m.dtype, m.D, m.T, m.ldx, kStreamK, NT, 128) ||
-        (GATED && !tensor_map_16(&mg, m.Wg, m.dtype, m.D, m.F, m.ldu, kStreamK, kStreamRows, 128, m.E, su)) ||
-        !tensor_map_16(&mu, m.Wu, m.dtype, m.D, m.F, m.ldu, kStreamK, kStreamRows, 128, m.E, su) ||
-        !tensor_map_16(&md, m.Wd, m.dtype, m.F, m.D, m.ldd, kStreamK, kStreamRows, 128, m.E, sd) ||
-        !tensor_map_16(&mh, p.h, m.dtype, m.F, static_cast<long long>(pairs), p.ldh, kStreamK, NT, 128)) {
+    if (!tensor_map_16(&mx, m.X, m.dtype, m.D, m.T, m.ldx, kStreamK, NT) ||
+        (GATED && !tensor_map_16(&mg, m.Wg, m.dtype, m.D, m.F, m.ldu, kStreamK, kStreamRows, false, m.E, su)) ||
+        !tensor_map_16(&mu, m.Wu, m.dtype, m.D, m.F, m.ldu, kStreamK, kStreamRows, false, m.E, su) ||
+        !tensor_map_16(&md, m.Wd, m.dtype, m.F, m.D, m.ldd, kStreamK, kStreamRows, false, m.E, sd) ||
+        !tensor_map_16(&mh, p.h, m.dtype, m.F, static_cast<long long>(pairs), p.ldh, kStreamK, NT)) {
         *detail = "cuTensorMapEncodeTiled rejected a matrix";
         return cudaErrorInvalidValue;
     }

@@ -1,22 +1,26 @@
 // pair_gemm16.cu: D = act(A . B + bias) + res on 16-bit values with tcgen05 MMAs over pairs of
-// CTAs (cta_group::2): one MMA multiplies 256 rows by BN columns, each CTA of the pair holding
+// CTAs (cta_group::2): one MMA multiplies 256 rows by 256 columns, each CTA of the pair holding
 // half of A's rows and half of B's columns in its own shared memory, so each SM stages half the
-// operand bytes per multiply-add of a one-CTA tile.
+// operand bytes per multiply-add of a one-CTA tile. (Narrower tiles, 128 and 192 columns, took as
+// long per k-block as 256, 0.29 us: the operands' way from L2 bounds them.)
 //
-// A persistent grid of pairs walks the 256 x BN output tiles in grouped-raster order. Roles of a
-// CTA's 12 warps:
-//   warp 0, lane 0: TMA producer: this CTA's 128 rows of A and BN / 2 columns of B per 64-wide
-//                   k-block into a ring of STAGES stages; both CTAs' copies complete on the
-//                   leader's "full" barrier.
+// A persistent grid of pairs walks the output tiles of one product, or of the two of a gradient
+// one after the other (the idle part of a last round is then paid once), in grouped-raster order.
+// Roles of a CTA's 20 warps:
+//   warp 0, lane 0: TMA producer: this CTA's 128 rows of A and 128 columns of B per 64-wide
+//                   k-block into a ring of 5 stages; both CTAs' copies complete on the leader's
+//                   "full" barrier.
 //   warp 1, lane 0: (leader CTA) issues the MMAs, four k-steps of 16 per block, into one of two
-//                   TMEM accumulators of BN columns; commits free the stage in both CTAs and,
+//                   TMEM accumulators of 256 columns; commits free the stage in both CTAs and,
 //                   at a tile's end, hand the accumulator to both CTAs' epilogues.
 //   warp 2:         allocates and frees the pair's TMEM.
-//   warps 4..11:    epilogue of this CTA's 128 rows while the next tile multiplies: warp w reads
-//                   TMEM lanes 32 (w % 4) .. + 31 and one half of the columns, 32 at a time;
-//                   bias, pre-activation, activation and residual in fp32, one rounding, through
-//                   shared memory to TMA stores (or, for outputs TMA cannot address, to stores
-//                   of 64 consecutive bytes per row).
+//   warps 4..19:    epilogue of this CTA's 128 rows while the next tile multiplies: warp w reads
+//                   TMEM lanes 32 (w % 4) .. + 31 and 64 of the columns, 32 at a time; bias,
+//                   pre-activation, activation and residual in fp32, one rounding, through shared
+//                   memory to TMA stores (or, for outputs TMA cannot address, to stores of 64
+//                   consecutive bytes per row). Four warps per scheduler hide one another's waits:
+//                   with two, a tile's epilogue took 11 us against 20 us of MMAs at K = 4096 (bias,
+//                   GELU, residual and pre-activation; 256 x 256).
 // Either operand may be stored with k or with its other dimension contiguous: TMA boxes and the
 // MMA descriptors differ, the arithmetic does not, so the three products of a linear layer and
 // its gradient need no transposed copies.
@@ -37,36 +41,61 @@ namespace {
 
 constexpr int kBM = 128;  // rows per CTA (256 per pair)
 constexpr int kBK = 64;   // k values per 128-byte swizzled row
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 128 + 32 * kEpiWarps;
 
-struct PairParams {
-    int M, N, K;
-    int tiles_m, tiles_n, group_m, total_tiles;
+constexpr int kBN = 256;
+constexpr int kEpiWarps = 16;  // 4 row quarters x 4 groups of 64 columns
+constexpr int kThreads = 128 + 32 * kEpiWarps;
+constexpr uint32_t kPartBytes = kBM * kBK * 2;  // A's or B's share of a stage
+constexpr uint32_t kStageBytes = 2 * kPartBytes;
+constexpr int kStages = 5;
+constexpr uint32_t kStoreBytes = 2048;  // 32 rows x 32 values
+constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * 2 * kStoreBytes + (2 * kStages + 4) * 8 + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "ring and store buffers fit in shared memory");
+
+struct PairProduct {
+    int M, N, KB;  // KB: k-blocks
+    int tiles_m, tiles_n, tiles;
+    int a_mn, b_mn;
     uint32_t idesc;
+    uint16_t *D;
+    long long ldd;
+    int d_tma;  // the output's rows are addressable by TMA
+};
+struct PairParams {
+    PairProduct g[kMaxProducts];
+    int total_tiles;
+    // The epilogue's matrices, of a launch with one product.
     const uint16_t *bias;
     int act;
     const uint16_t *res;
     long long ldr;
-    uint16_t *D;
-    long long ldd;
+    int res_vec;  // the residual's rows allow 16-byte loads of 8 values each
     uint16_t *pre;
     long long ldz;
-    int d_tma, z_tma;  // the output's rows are addressable by TMA
-    int res_vec;       // the residual's rows allow 16-byte loads
+    int z_tma;
 };
+struct PairMaps {
+    CUtensorMap a[kMaxProducts], b[kMaxProducts], d[kMaxProducts], z;
+};
+constexpr int kGroupM = 8;  // tile rows of the raster's groups
 
-template <int BN>
-struct PairConfig {
-    static constexpr uint32_t A_BYTES = kBM * kBK * 2;
-    static constexpr uint32_t B_BYTES = (BN / 2) * kBK * 2;
-    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 6 : 8;
-    static constexpr uint32_t STORE_BYTES = 2048;  // 32 rows x 32 values
-    static constexpr uint32_t TMEM_COLS = 2 * BN;
-    static constexpr size_t SMEM = STAGES * STAGE_BYTES + kEpiWarps * 2 * STORE_BYTES +
-                                   (2 * STAGES + 4) * 8 + 16 + 1024;
-};
+// Tile t of the launch: its product and place.
+__device__ __forceinline__ int locate(const PairParams &p, int t, int &tm, int &tn) {
+    const int i = t >= p.g[0].tiles ? 1 : 0;
+    tile_coords(i ? t - p.g[0].tiles : t, p.g[i].tiles_m, p.g[i].tiles_n, kGroupM, tm, tn);
+    return i;
+}
+
+// Calls body with the operands' layouts as compile-time constants.
+template <typename Body>
+__device__ __forceinline__ void with_layout(const PairProduct &g, Body body) {
+    if (g.a_mn)
+        body(std::true_type(), std::true_type());
+    else if (g.b_mn)
+        body(std::false_type(), std::true_type());
+    else
+        body(std::false_type(), std::false_type());
+}
 
 // A wait whose arrivals may come from the other CTA of the pair.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -92,8 +121,8 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// 16-byte chunk c (0..3) of row r (0..31) of a warp's 32 x 32 store tile: the 64-byte TMA swizzle,
-// with which eight lanes' 16-byte accesses touch all banks once.
+// 16-byte chunk c (0..3) of row r (0..31) of a warp's 32 x 32 buffer: the 64-byte TMA
+// swizzle, with which eight lanes' 16-byte accesses touch all banks once.
 __device__ __forceinline__ uint32_t store_chunk(int r, int c) {
     return static_cast<uint32_t>(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
@@ -105,13 +134,15 @@ __device__ __forceinline__ void activate32(float (&v)[32], int act) {
     });
 }
 
-// One warp's 32 x 32 block of an output at (row0, col0): v is lane r's row. `buf` is free (no
-// copy reads it) on entry for every lane.
+// One warp's 32 x 32 block of an output at (row0, col0): v is lane r's row. It goes through `buf`
+// (which no earlier copy still reads) to a TMA store or, for rows TMA cannot address, to stores of
+// one row per instruction. (Stores of 16 bytes per lane from the same buffer, in place of the TMA
+// stores, cost 3 to 6% on the large products; 4-byte stores of two rows per instruction, in place
+// of 2-byte ones of one row, 40% on the ragged one.)
 template <typename T>
-__device__ __forceinline__ void store_block(const float (&v)[32], uint8_t *buf,
-                                            const CUtensorMap *map, int tma, uint16_t *out,
-                                            long long ld, int M, int N, int row0, int col0,
-                                            int lane) {
+__device__ __forceinline__ void store_block(const float (&v)[32], uint8_t *buf, const CUtensorMap *map,
+                                            int tma, uint16_t *out, long long ld, int M, int N, int row0,
+                                            int col0, int lane) {
     using H = Half16<T>;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -129,96 +160,100 @@ __device__ __forceinline__ void store_block(const float (&v)[32], uint8_t *buf,
             tma_store_2d(map, buf, col0, row0);
             bulk_commit();
         }
-    } else {
-        __syncwarp();
-        const int rows = min(32, M - row0);
-        uint16_t *p = out + static_cast<long long>(row0) * ld + col0 + lane;
-        if (col0 + lane < N) {
-#pragma unroll 8
-            for (int r = 0; r < rows; ++r)
-                p[r * ld] = *reinterpret_cast<const uint16_t *>(buf + store_chunk(r, lane >> 3) + (lane & 7) * 2);
-        }
-        __syncwarp();
-    }
-}
-
-// The residual's 32 values of lane r's row, added to v. Rows that allow it are read 16 bytes at a
-// time by their own lane; otherwise the warp reads 64 consecutive bytes of one row after another
-// and hands them over through `buf`.
-template <typename T>
-__device__ __forceinline__ void add_residual(float (&v)[32], uint8_t *buf, const PairParams &p,
-                                             int row0, int col0, int lane) {
-    using H = Half16<T>;
-    if (p.res_vec && col0 + 32 <= p.N) {
-        if (row0 + lane < p.M) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.res + static_cast<long long>(row0 + lane) * p.ldr + col0);
-            uint4 q[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) q[c] = src[c];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t w[4] = {q[c].x, q[c].y, q[c].z, q[c].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = H::widen2(w[i]);
-                    v[8 * c + 2 * i] += f.x;
-                    v[8 * c + 2 * i + 1] += f.y;
-                }
-            }
-        }
         return;
     }
-    const uint16_t *src = p.res + static_cast<long long>(row0) * p.ldr + col0 + lane;
-    const int rows = min(32, p.M - row0);
-    uint16_t t[32];
+    __syncwarp();
+    const int rows = min(32, M - row0);
+    if (col0 + lane < N) {
+        uint16_t *p = out + static_cast<long long>(row0) * ld + col0 + lane;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r)
+            p[r * ld] = *reinterpret_cast<const uint16_t *>(buf + store_chunk(r, lane >> 3) + (lane & 7) * 2);
+    }
+    __syncwarp();
+}
+
+// The residual of a 32 x 32 block is fetched ahead of the arithmetic before it, four lanes to a row
+// (whole 32-byte sectors, eight rows per instruction), and turned around through `buf` so that
+// each lane gets its own row. Rows without 16-byte alignment are read as the aligned 4-byte words
+// around them. raw[5 i ..]: row 8 i + lane / 4, values 8 (lane % 4) .. + 7.
+__device__ __forceinline__ void fetch_residual(uint32_t (&raw)[20], const PairParams &p, int row0,
+                                               int col0, int lane) {
+    const int col = col0 + (lane & 3) * 8, count = min(8, p.g[0].N - col);
 #pragma unroll
-    for (int r = 0; r < 32; ++r) t[r] = r < rows && col0 + lane < p.N ? src[r * p.ldr] : uint16_t(0);
+    for (int i = 0; i < 4; ++i) {
+        const int row = row0 + 8 * i + (lane >> 2);
+        if (row >= p.g[0].M || count <= 0) continue;
+        const uint16_t *src = p.res + static_cast<long long>(row) * p.ldr + col;
+        if (p.res_vec) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(src);
+            raw[5 * i] = q.x;
+            raw[5 * i + 1] = q.y;
+            raw[5 * i + 2] = q.z;
+            raw[5 * i + 3] = q.w;
+        } else {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(src);
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(a & ~static_cast<uintptr_t>(3));
+            const int shift = static_cast<int>(a & 2u) >> 1;  // only words with a value of the row
 #pragma unroll
-    for (int r = 0; r < 32; ++r)
-        *reinterpret_cast<uint16_t *>(buf + store_chunk(r, lane >> 3) + (lane & 7) * 2) = t[r];
+            for (int k = 0; k < 5; ++k)
+                if (2 * k - shift < count) raw[5 * i + k] = w[k];
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void add_residual(float (&v)[32], uint32_t (&raw)[20], uint8_t *buf,
+                                             const PairParams &p, int row0, int col0, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        if (!p.res_vec) {
+            const uint16_t *src = p.res + static_cast<long long>(row0 + r) * p.ldr + col0;
+            if (reinterpret_cast<uintptr_t>(src) & 2u) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    raw[5 * i + k] = __funnelshift_r(raw[5 * i + k], raw[5 * i + k + 1], 16);
+            }
+        }
+        *reinterpret_cast<uint4 *>(buf + store_chunk(r, lane & 3)) =
+            make_uint4(raw[5 * i], raw[5 * i + 1], raw[5 * i + 2], raw[5 * i + 3]);
+    }
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const uint4 q = *reinterpret_cast<const uint4 *>(buf + store_chunk(lane, c));
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = H::widen2(w[i]);
-            v[8 * c + 2 * i] += f.x;
-            v[8 * c + 2 * i + 1] += f.y;
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = Half16<T>::widen2(w[k]);
+            v[8 * c + 2 * k] += f.x;
+            v[8 * c + 2 * k + 1] += f.y;
         }
     }
     __syncwarp();
 }
 
-template <int BN, bool A_MN, bool B_MN, typename T>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
-    pair_gemm16_kernel(const __grid_constant__ CUtensorMap map_a,
-                       const __grid_constant__ CUtensorMap map_b,
-                       const __grid_constant__ CUtensorMap map_d,
-                       const __grid_constant__ CUtensorMap map_z, const PairParams p) {
-    using C = PairConfig<BN>;
-    constexpr int STAGES = C::STAGES;
+    pair_gemm16_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
-    uint8_t *store_bufs = smem + STAGES * C::STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(store_bufs + kEpiWarps * 2 * C::STORE_BYTES);
-    uint64_t *empty = full + STAGES;
-    uint64_t *acc_full = empty + STAGES;  // [2]
-    uint64_t *acc_free = acc_full + 2;    // [2], the leader's are used
+    uint8_t *store_bufs = smem + kStages * kStageBytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(store_bufs + kEpiWarps * 2 * kStoreBytes);
+    uint64_t *empty = full + kStages;
+    uint64_t *acc_full = empty + kStages;  // [2]
+    uint64_t *acc_free = acc_full + 2;     // [2], the leader's are used
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const int KB = (p.K + kBK - 1) / kBK;
 
     if (threadIdx.x == 0) {
-        tma_prefetch_desc(&map_a);
-        tma_prefetch_desc(&map_b);
-        for (int s = 0; s < STAGES; ++s) {
+        tma_prefetch_desc(&maps.a[0]);
+        tma_prefetch_desc(&maps.b[0]);
+        for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -228,12 +263,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         mbar_init_fence();
     }
-    if (warp == 2) tmem_alloc<2>(tmem_slot, C::TMEM_COLS);
+    if (warp == 2) tmem_alloc<2>(tmem_slot, 2 * kBN);
     tc_before_sync();
-    __syncthreads();
     cluster_sync();  // the pair's barriers exist before either CTA's copies complete on them
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
+    grid_dependents();  // after the TMEM allocation: a later kernel's CTA cannot take it first
+    grid_dependency();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -241,130 +277,145 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             bool ok = true;
             for (int t = pair; t < p.total_tiles && ok; t += pairs) {
                 int tm, tn;
-                tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
+                const int i = locate(p, t, tm, tn);
+                const CUtensorMap *ma = &maps.a[i], *mb = &maps.b[i];
                 const int m0 = tm * 256 + static_cast<int>(rank) * kBM;
-                const int n0 = tn * BN + static_cast<int>(rank) * (BN / 2);
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (it >= STAGES && !mbar_wait_cluster(&empty[s], ((it / STAGES) - 1) & 1)) {
-                        ok = false;
-                        break;
+                const int n0 = tn * kBN + static_cast<int>(rank) * (kBN / 2);
+                const int KB = p.g[i].KB;
+                auto blocks = [&](auto a_layout, auto b_layout) {
+                    constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+                    for (int k0 = 0; k0 < KB * kBK; k0 += kBK, ++it) {
+                        const int s = it % kStages;
+                        if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *sa = smem + s * kStageBytes, *sb = sa + kPartBytes;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+                        const uint32_t bar = map_to_rank(&full[s], 0);
+                        if (a_mn) {
+                            tma_load_2d_pair(sa, ma, bar, m0, k0);
+                            tma_load_2d_pair(sa + 8192, ma, bar, m0 + 64, k0);
+                        } else {
+                            tma_load_2d_pair(sa, ma, bar, k0, m0);
+                        }
+                        if (b_mn) {
+                            tma_load_2d_pair(sb, mb, bar, n0, k0);
+                            tma_load_2d_pair(sb + 8192, mb, bar, n0 + 64, k0);
+                        } else {
+                            tma_load_2d_pair(sb, mb, bar, k0, n0);
+                        }
                     }
-                    uint8_t *sa = smem + s * C::STAGE_BYTES, *sb = sa + C::A_BYTES;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::STAGE_BYTES);
-                    const uint32_t bar = map_to_rank(&full[s], 0);
-                    const int k0 = kb * kBK;
-                    if (A_MN) {
-#pragma unroll
-                        for (int i = 0; i < kBM / 64; ++i)
-                            tma_load_2d_pair(sa + i * 8192, &map_a, bar, m0 + 64 * i, k0);
-                    } else {
-                        tma_load_2d_pair(sa, &map_a, bar, k0, m0);
-                    }
-                    if (B_MN) {
-#pragma unroll
-                        for (int i = 0; i < BN / 128; ++i)
-                            tma_load_2d_pair(sb + i * 8192, &map_b, bar, n0 + 64 * i, k0);
-                    } else {
-                        tma_load_2d_pair(sb, &map_b, bar, k0, n0);
-                    }
-                }
+                };
+                with_layout(p.g[i], blocks);
             }
             // Shared memory must outlive every copy: the leader waits (bounded) for the last
             // stages of both CTAs; the final cluster barrier holds the other CTA until then.
             if (rank == 0)
-                for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-                    if (!mbar_wait_cluster(&full[j % STAGES], (j / STAGES) & 1)) break;
+                for (int j = it > kStages ? it - kStages : 0; j < it; ++j)
+                    if (!mbar_wait_cluster(&full[j % kStages], (j / kStages) & 1)) break;
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             int it = 0, j = 0;
             bool ok = true;
             for (int t = pair; t < p.total_tiles && ok; t += pairs, ++j) {
+                const int i = t >= p.g[0].tiles ? 1 : 0;
                 const int set = j & 1;
                 if (j >= 2 && !mbar_wait_cluster(&acc_free[set], ((j >> 1) - 1) & 1)) break;
                 tc_after_sync();
-                const uint32_t d = tmem + static_cast<uint32_t>(set * BN);
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait_cluster(&full[s], (it / STAGES) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_after_sync();
-                    const uint32_t sa = smem_addr(smem + s * C::STAGE_BYTES), sb = sa + C::A_BYTES;
-                    const uint64_t da = A_MN ? desc_mn_major(sa, 8192) : desc_k_major(sa);
-                    const uint64_t db = B_MN ? desc_mn_major(sb, 8192) : desc_k_major(sb);
+                const uint32_t d = tmem + static_cast<uint32_t>(set * kBN);
+                const int KB = p.g[i].KB;
+                const uint32_t idesc = p.g[i].idesc;
+                auto blocks = [&](auto a_layout, auto b_layout) {
+                    constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+                    for (int kb = 0; kb < KB; ++kb, ++it) {
+                        const int s = it % kStages;
+                        if (!mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_after_sync();
+                        const uint32_t sa = smem_addr(smem + s * kStageBytes), sb = sa + kPartBytes;
+                        const uint64_t da = a_mn ? desc_mn_major(sa, 8192) : desc_k_major(sa);
+                        const uint64_t db = b_mn ? desc_mn_major(sb, 8192) : desc_k_major(sb);
 #pragma unroll
-                    for (int k = 0; k < kBK / 16; ++k)  // start addresses count 16 bytes
-                        mma_16<2>(d, da + static_cast<uint64_t>(k * (A_MN ? 128 : 2)),
-                                  db + static_cast<uint64_t>(k * (B_MN ? 128 : 2)), p.idesc,
-                                  kb > 0 || k > 0);
-                    mma_commit_16<2>(&empty[s]);
-                }
+                        for (int k = 0; k < kBK / 16; ++k)  // start addresses count 16 bytes: a
+                            mma_16<2>(d, da + static_cast<uint64_t>(k * (a_mn ? 128 : 2)),  // k-step is
+                                      db + static_cast<uint64_t>(k * (b_mn ? 128 : 2)),     // 32 bytes
+                                      idesc, kb > 0 || k > 0);  // of a row or 16 rows
+                        mma_commit_16<2>(&empty[s]);
+                    }
+                };
+                with_layout(p.g[i], blocks);
                 if (ok) mma_commit_16<2>(&acc_full[set]);
             }
         }
     } else if (warp >= 4) {
-        const int w = warp - 4, quarter = warp & 3, half = w >> 2;
+        const int w = warp - 4, quarter = warp & 3, group = w >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        uint8_t *bufs = store_bufs + w * 2 * C::STORE_BYTES;
+        uint8_t *bufs = store_bufs + w * 2 * kStoreBytes;
         const uint32_t free0 = map_to_rank(&acc_free[0], 0), free1 = map_to_rank(&acc_free[1], 0);
+        const int cfirst = group * 64, cend = cfirst + 64;
         int j = 0, nbuf = 0;
+        uint32_t raw[20];  // the next block's residual
+        float bias = 0.0f;  // and bias, of column col0 + lane
+        auto fetch = [&](int row0, int col0) {
+            if (p.res) fetch_residual(raw, p, row0, col0, lane);
+            if (p.bias) bias = col0 + lane < p.g[0].N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
+        };
         for (int t = pair; t < p.total_tiles; t += pairs, ++j) {
             const int set = j & 1;
+            int tm, tn;
+            const int i = locate(p, t, tm, tn);
+            const PairProduct g = p.g[i];
+            const int row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
+            if (row0 < g.M && tn * kBN + cfirst < g.N) fetch(row0, tn * kBN + cfirst);
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
             tc_after_sync();
-            int tm, tn;
-            tile_coords(t, p.tiles_m, p.tiles_n, p.group_m, tm, tn);
-            const int row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
-            const uint32_t tset = tmem + lane_base + static_cast<uint32_t>(set * BN);
+            const uint32_t tset = tmem + lane_base + static_cast<uint32_t>(set * kBN);
 #pragma unroll 1
-            for (int c0 = half * (BN / 2); c0 < (half + 1) * (BN / 2); c0 += 32) {
-                uint32_t r[32];
-                tmem_ld_x32(tset + static_cast<uint32_t>(c0), r);
+            for (int c0 = cfirst; c0 < cend; c0 += 32) {
+                float v[32];
+                tmem_ld_x32(tset + static_cast<uint32_t>(c0), reinterpret_cast<uint32_t(&)[32]>(v));
                 tmem_ld_wait();
-                if (c0 + 32 == (half + 1) * (BN / 2)) {  // the warp's last read of this accumulator
+                if (c0 + 32 == cend) {  // the warp's last read of this accumulator
                     tc_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_at(set ? free1 : free0);
                 }
-                const int col0 = tn * BN + c0;
-                if (row0 >= p.M || col0 >= p.N) continue;
-                float v[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+                const int col0 = tn * kBN + c0;
+                if (row0 >= g.M || col0 >= g.N) continue;
                 if (p.bias) {
-                    const float b = col0 + lane < p.N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, b, i);
+                    for (int k = 0; k < 32; ++k) v[k] += __shfl_sync(0xFFFFFFFFu, bias, k);
                 }
                 if (p.pre) {
                     if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
-                    store_block<T>(v, bufs + nbuf * C::STORE_BYTES, &map_z, p.z_tma, p.pre, p.ldz, p.M,
-                                   p.N, row0, col0, lane);
+                    store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.z, p.z_tma, p.pre, p.ldz, g.M, g.N,
+                                   row0, col0, lane);
                     nbuf ^= 1;
                 }
                 activate32(v, p.act);
                 if (lane == 0) bulk_wait_read<1>();
                 __syncwarp();
-                if (p.res) add_residual<T>(v, bufs + nbuf * C::STORE_BYTES, p, row0, col0, lane);
-                store_block<T>(v, bufs + nbuf * C::STORE_BYTES, &map_d, p.d_tma, p.D, p.ldd, p.M, p.N,
-                               row0, col0, lane);
+                if (p.res) add_residual<T>(v, raw, bufs + nbuf * kStoreBytes, p, row0, col0, lane);
+                if (c0 + 32 < cend && col0 + 32 < g.N) fetch(row0, col0 + 32);
+                store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.d[i], g.d_tma, g.D, g.ldd, g.M, g.N, row0,
+                               col0, lane);
                 nbuf ^= 1;
             }
         }
-        if (lane == 0) bulk_wait<0>();
+        if (lane == 0) bulk_wait_read<0>();
     }
 
     __syncwarp();
     tc_before_sync();
-    __syncthreads();
     cluster_sync();  // neither CTA's shared or tensor memory is used by the other any more
     if (warp == 2) {
         tc_after_sync();
-        tmem_dealloc<2>(tmem, C::TMEM_COLS);
+        tmem_dealloc<2>(tmem, 2 * kBN);
     }
 }
 
@@ -372,107 +423,113 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 
 constexpr int kMaxDevices = 64;
 
-template <int BN, bool A_MN, bool B_MN, typename T>
-cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    using C = PairConfig<BN>;
-    auto kernel = pair_gemm16_kernel<BN, A_MN, B_MN, T>;
-    int dev = 0;
+// Pairs that can run at once (an odd SM of a cluster group stays idle), found once per device.
+template <typename T>
+cudaError_t prepare(int dev, int *pairs) {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t setup[kMaxDevices];
+    static int max_pairs[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        auto kernel = pair_gemm16_kernel<T>;
+        setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          static_cast<int>(kSmem));
+        if (setup[dev] != cudaSuccess) return;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(kThreads, 1, 1);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        setup[dev] = cudaOccupancyMaxActiveClusters(&max_pairs[dev], kernel, &cfg);
+        if (setup[dev] == cudaSuccess && max_pairs[dev] < 1) setup[dev] = cudaErrorInvalidConfiguration;
+    });
+    *pairs = max_pairs[dev];
+    return setup[dev];
+}
+
+template <typename T>
+cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
+    int dev = 0, max_pairs = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         *detail = "cudaGetDevice failed";
         return err != cudaSuccess ? err : cudaErrorInvalidDevice;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    // Pairs that can run at once (an odd SM of a cluster group stays idle), queried once.
-    static std::once_flag once[kMaxDevices];
-    static cudaError_t setup[kMaxDevices];
-    static int max_pairs[kMaxDevices];
-    std::call_once(once[dev], [&] {
-        setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(C::SMEM));
-        if (setup[dev] != cudaSuccess) return;
-        cudaLaunchConfig_t q = cfg;
-        q.gridDim = dim3(2, 1, 1);
-        q.attrs = attr;
-        q.numAttrs = 1;
-        setup[dev] = cudaOccupancyMaxActiveClusters(&max_pairs[dev], kernel, &q);
-        if (setup[dev] == cudaSuccess && max_pairs[dev] < 1) setup[dev] = cudaErrorInvalidConfiguration;
-    });
-    if (setup[dev] != cudaSuccess) {
+    err = prepare<T>(dev, &max_pairs);
+    if (err != cudaSuccess) {
         *detail = "linear layer kernel set-up failed";
-        return setup[dev];
+        return err;
     }
-
-    PairParams p;
-    p.M = g.M;
-    p.N = g.N;
-    p.K = g.K;
-    p.tiles_m = static_cast<int>((g.M + 255LL) / 256);
-    p.tiles_n = static_cast<int>((g.N + static_cast<long long>(BN) - 1) / BN);
-    p.group_m = 8;
-    const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    if (tiles > 0x3fffffffLL) {
-        *detail = "too many output tiles";
-        return cudaErrorInvalidValue;
+    PairParams p = {};
+    PairMaps maps;
+    // Tiles with the longer k first: the shorter ones fill the last round.
+    const int order[2] = {n == 2 && list[1].K > list[0].K ? 1 : 0, n == 2 && list[1].K > list[0].K ? 0 : 1};
+    long long total = 0;
+    for (int i = 0; i < n; ++i) {
+        const Gemm16 &g = list[order[i]];
+        PairProduct &q = p.g[i];
+        q.M = g.M;
+        q.N = g.N;
+        q.KB = static_cast<int>((g.K + static_cast<long long>(kBK) - 1) / kBK);
+        q.tiles_m = static_cast<int>((g.M + 255LL) / 256);
+        q.tiles_n = static_cast<int>((g.N + static_cast<long long>(kBN) - 1) / kBN);
+        const long long tiles = static_cast<long long>(q.tiles_m) * q.tiles_n;
+        total += tiles;
+        if (total > 0x3fffffffLL) {
+            *detail = "too many output tiles";
+            return cudaErrorInvalidValue;
+        }
+        q.tiles = static_cast<int>(tiles);
+        q.a_mn = g.a_mn;
+        q.b_mn = g.b_mn;
+        q.idesc = idesc_16(256, kBN, Half16<T>::kind, g.a_mn, g.b_mn);
+        q.D = g.D;
+        q.ldd = g.ldd;
+        // A TMA store also writes zeros into the rest of a row's last 16 bytes, which may belong to
+        // the caller's wider matrix: only rows that end on that boundary are stored so.
+        q.d_tma = tma_rows(g.D, g.ldd) && g.N % 8 == 0;
+        if (!(g.a_mn ? tensor_map_16(&maps.a[i], g.A, g.dtype, g.M, g.K, g.lda, 64, kBK)
+                     : tensor_map_16(&maps.a[i], g.A, g.dtype, g.K, g.M, g.lda, kBK, kBM)) ||
+            !(g.b_mn ? tensor_map_16(&maps.b[i], g.B, g.dtype, g.N, g.K, g.ldb, 64, kBK)
+                     : tensor_map_16(&maps.b[i], g.B, g.dtype, g.K, g.N, g.ldb, kBK, kBN / 2)) ||
+            (q.d_tma && !tensor_map_16(&maps.d[i], g.D, g.dtype, g.N, g.M, g.ldd, 32, 32, true))) {
+            *detail = "cuTensorMapEncodeTiled rejected a matrix";
+            return cudaErrorInvalidValue;
+        }
     }
-    p.total_tiles = static_cast<int>(tiles);
-    p.idesc = idesc_16(256, BN, Half16<T>::kind, A_MN, B_MN);
-    p.bias = g.bias;
-    p.act = g.act;
-    p.res = g.res;
-    p.ldr = g.ldr;
-    p.D = g.D;
-    p.ldd = g.ldd;
-    p.pre = g.pre;
-    p.ldz = g.ldz;
-    // A TMA store also writes zeros into the rest of a row's last 16 bytes, which may belong to
-    // the caller's wider matrix: only rows that end on that boundary are stored so.
-    p.d_tma = tma_rows(g.D, g.ldd) && g.N % 8 == 0;
-    p.z_tma = g.pre && tma_rows(g.pre, g.ldz) && g.N % 8 == 0;
-    p.res_vec = g.res && tma_rows(g.res, g.ldr);
-
-    CUtensorMap ma, mb, md, mz;
-    const bool ok =
-        (A_MN ? tensor_map_16(&ma, g.A, g.dtype, g.M, g.K, g.lda, 64, kBK, 128)
-              : tensor_map_16(&ma, g.A, g.dtype, g.K, g.M, g.lda, kBK, kBM, 128)) &&
-        (B_MN ? tensor_map_16(&mb, g.B, g.dtype, g.N, g.K, g.ldb, 64, kBK, 128)
-              : tensor_map_16(&mb, g.B, g.dtype, g.K, g.N, g.ldb, kBK, BN / 2, 128)) &&
-        (!p.d_tma || tensor_map_16(&md, g.D, g.dtype, g.N, g.M, g.ldd, 32, 32, 64)) &&
-        (!p.z_tma || tensor_map_16(&mz, g.pre, g.dtype, g.N, g.M, g.ldz, 32, 32, 64));
-    if (!ok) {
-        *detail = "cuTensorMapEncodeTiled rejected a matrix";
-        return cudaErrorInvalidValue;
+    p.total_tiles = static_cast<int>(total);
+    if (n == 1) {
+        const Gemm16 &g = list[0];
+        p.bias = g.bias;
+        p.act = g.act;
+        p.res = g.res;
+        p.ldr = g.ldr;
+        p.res_vec = g.res && tma_rows(g.res, g.ldr) && g.N % 8 == 0;
+        p.pre = g.pre;
+        p.ldz = g.ldz;
+        p.z_tma = g.pre && tma_rows(g.pre, g.ldz) && g.N % 8 == 0;
+        if (p.z_tma && !tensor_map_16(&maps.z, g.pre, g.dtype, g.N, g.M, g.ldz, 32, 32, true)) {
+            *detail = "cuTensorMapEncodeTiled rejected a matrix";
+            return cudaErrorInvalidValue;
+        }
     }
-    if (!p.d_tma) md = ma;
-    if (!p.z_tma) mz = ma;
-    const int pairs = static_cast<int>(std::min<long long>(tiles, max_pairs[dev]));
-    cfg.gridDim = dim3(2u * static_cast<unsigned>(pairs), 1, 1);
-    err = cudaLaunchKernelEx(&cfg, kernel, ma, mb, md, mz, p);
-    if (err == cudaSuccess) err = cudaGetLastError();
+    const int pairs = std::min(p.total_tiles, max_pairs);
+    err = launch_early(pair_gemm16_kernel<T>, dim3(2u * static_cast<unsigned>(pairs)), kThreads, kSmem,
+                       stream, maps, p);
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
     return err;
 }
 
-template <int BN, typename T>
-cudaError_t launch_major(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    if (g.a_mn) return launch<BN, true, true, T>(g, stream, detail);
-    return g.b_mn ? launch<BN, false, true, T>(g, stream, detail)
-                  : launch<BN, false, false, T>(g, stream, detail);
-}
-
 }  // namespace
 
-cudaError_t pair_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    return g.dtype == kBf16 ? launch_major<256, __nv_bfloat16>(g, stream, detail)
-                            : launch_major<256, __half>(g, stream, detail);
+cudaError_t pair_gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
+    return list[0].dtype == kBf16 ? launch<__nv_bfloat16>(list, n, stream, detail)
+                                  : launch<__half>(list, n, stream, detail);
 }
 
 // ---- tensor maps ------------------------------------------------------------------------------------
@@ -497,7 +554,7 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,
-                   long long ld, int box_cols, int box_rows, int swizzle_bytes, long long depth,
+                   long long ld, int box_cols, int box_rows, bool narrow, long long depth,
                    long long stride) {
     const EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
@@ -509,8 +566,7 @@ bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols
     return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                depth > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+               narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace sg

@@ -328,7 +328,7 @@ sgemm_status_t linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t
     g.pre = out16(Z);
     g.ldz = ldz;
     const char *detail = "";
-    const cudaError_t err = sg::gemm16_launch(g, stream, &detail);
+    const cudaError_t err = sg::gemm16_launch(&g, 1, stream, &detail);
     return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
 }
 
@@ -393,9 +393,11 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         err = sg::act_grad_launch(a, stream, &detail);
         if (err != cudaSuccess) return fail_cuda(detail, err);
     }
-    sg::Gemm16 g;
-    g.dtype = dtype;
+    sg::Gemm16 list[2];
+    int n = 0;
     if (want_dx) {  // dX = dZ . op(W)^T: K of this product is N, op(W)^T is N x K
+        sg::Gemm16 &g = list[n++];
+        g.dtype = dtype;
         g.M = static_cast<int>(M);
         g.N = static_cast<int>(K);
         g.K = static_cast<int>(N);
@@ -407,10 +409,10 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         g.b_mn = t;  // W stored N x K: rows run along this product's K
         g.D = out16(dX);
         g.ldd = lddx;
-        err = sg::gemm16_launch(g, stream, &detail);
-        if (err != cudaSuccess) return fail_cuda(detail, err);
     }
     if (want_dw) {  // dW = dZ^T . X (N x K) or X^T . dZ (K x N): K of this product is M
+        sg::Gemm16 &g = list[n++];
+        g.dtype = dtype;
         g.M = static_cast<int>(t ? N : K);
         g.N = static_cast<int>(t ? K : N);
         g.K = static_cast<int>(M);
@@ -422,7 +424,9 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         g.b_mn = true;
         g.D = out16(dW);
         g.ldd = lddw;
-        err = sg::gemm16_launch(g, stream, &detail);
+    }
+    if (n > 0) {
+        err = sg::gemm16_launch(list, n, stream, &detail);
         if (err != cudaSuccess) return fail_cuda(detail, err);
     }
     return SGEMM_OK;

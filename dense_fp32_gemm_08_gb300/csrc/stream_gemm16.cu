@@ -118,6 +118,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
+    grid_dependents();  // after the TMEM allocation: a later kernel's CTA cannot take it first
+    grid_dependency();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -299,14 +301,13 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     p.counters = static_cast<unsigned int *>(ws);
     p.pieces = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
     CUtensorMap mw, mx;
-    if (!(W_MN ? tensor_map_16(&mw, g.B, g.dtype, g.N, g.K, g.ldb, 64, kStreamK, 128)
-               : tensor_map_16(&mw, g.B, g.dtype, g.K, g.N, g.ldb, kStreamK, kStreamRows, 128)) ||
-        !tensor_map_16(&mx, g.A, g.dtype, g.K, g.M, g.lda, kStreamK, NT, 128)) {
+    if (!(W_MN ? tensor_map_16(&mw, g.B, g.dtype, g.N, g.K, g.ldb, 64, kStreamK)
+               : tensor_map_16(&mw, g.B, g.dtype, g.K, g.N, g.ldb, kStreamK, kStreamRows)) ||
+        !tensor_map_16(&mx, g.A, g.dtype, g.K, g.M, g.lda, kStreamK, NT)) {
         *detail = "cuTensorMapEncodeTiled rejected a matrix";
         return cudaErrorInvalidValue;
     }
-    kernel<<<p.split.ctas, kThreads, C::SMEM, stream>>>(mw, mx, p);
-    err = cudaGetLastError();
+    err = launch_early(kernel, dim3(p.split.ctas), kThreads, C::SMEM, stream, mw, mx, p);
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
     return err;
 }
