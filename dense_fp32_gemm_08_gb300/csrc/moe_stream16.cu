@@ -45,13 +45,13 @@ struct MoeParams {
     int tiles_d, kb_down;  // step 4: tiles of D, k-blocks of F
     uint32_t idesc;
     MoeSync *sync;
-    unsigned int *counters;  // [active experts * tiles_f]: units of a step-3 tile that arrived
+    unsigned int *counters;  // [active experts * tiles_f][4 warps]: units of step 3 that arrived
     float *score;            // [T][E]
     uint16_t *h;             // [T * k][ldh]
     long long ldh;
     float *out;              // [T * k][tiles_d * 128]: an expert's output for one token
-    float *up_pieces;        // [2 * CTAs][accumulators][NT][128]
-    float *down_pieces;      // [2 * CTAs][NT][128]
+    float *up_pieces;        // [2 * CTAs][accumulators][NT / 4][128][4]
+    float *down_pieces;      // [2 * CTAs][NT / 4][128][4]
 };
 
 // What every CTA knows of the routing.
@@ -119,14 +119,15 @@ __device__ __forceinline__ void moe_scores(const MoeParams &p, float *part) {
     const int slices = m.T >= 8 ? 1 : m.T >= 4 ? 2 : m.T >= 2 ? 4 : 8;
     const int slice = warp & (slices - 1), t_step = 8 / slices;
     const int chunks = (m.D + 7) / 8;
-    for (int e = blockIdx.x; e < m.E; e += gridDim.x) {
+    const int groups = (m.T + t_step - 1) / t_step;
+    for (int item = blockIdx.x; item < m.E * groups; item += gridDim.x) {
+        const int e = item / groups, t = (item - e * groups) * t_step + warp / slices;
         const uint16_t *w = m.Wr + e * m.ldr;
-        for (int t0 = 0; t0 < m.T; t0 += t_step) {
-            const int t = t0 + warp / slices;
+        {
             float s = 0.0f;
             if (t < m.T && !(m.active && !m.active[t])) {
                 const uint16_t *x = m.X + t * m.ldx;
-#pragma unroll 4
+#pragma unroll 8
                 for (int c = slice * 32 + lane; c < chunks; c += slices * 32) {
                     const int count = min(8, m.D - 8 * c);
                     const uint4 a = load8_any(x + 8 * c, count), b = load8_any(w + 8 * c, count);
@@ -153,61 +154,60 @@ __device__ __forceinline__ void moe_scores(const MoeParams &p, float *part) {
 }
 
 // ---- step 2: routing ----------------------------------------------------------------------------------
-__device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r) {
+__device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r, unsigned long long *scratch) {
     const Moe16 &m = p.m;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int e = threadIdx.x; e < m.E; e += kThreads) r.mask[e] = 0;
     __syncthreads();
+    // A warp per token. An expert's rank is the number of experts before it in the order of
+    // moe_score_key; every lane counts for its own experts against all of them in shared memory,
+    // which takes one pass over the scores instead of one reduction per chosen expert.
     for (int t = warp; t < m.T; t += kThreads / 32) {
         const bool on = !(m.active && !m.active[t]);
-        float s[kMoeMaxExperts / 32];
-        unsigned long long below = ~0ull;
-        float top = 0.0f;
-        if (on) {
-#pragma unroll
-            for (int i = 0; i < kMoeMaxExperts / 32; ++i)
-                s[i] = i * 32 + lane < m.E ? __ldcg(p.score + t * m.E + i * 32 + lane) : 0.0f;
-        }
-#pragma unroll 1
-        for (int j = 0; j < m.k; ++j) {
-            int e = -1;
-            if (on) {
-                unsigned long long best = 0;
-#pragma unroll
-                for (int i = 0; i < kMoeMaxExperts / 32; ++i) {
-                    if (i * 32 >= m.E) break;
-                    const unsigned long long key = moe_score_key(s[i], i * 32 + lane);
-                    if (i * 32 + lane < m.E && key < below && key > best) best = key;
-                }
-                for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-                below = best;
-                e = static_cast<int>(0xFFFFFFFFu - static_cast<unsigned>(best));
-                const float se = moe_key_score(best);
-                if (j == 0) top = se;
-                r.weight[t * m.k + j] = expf(se - top);
-                if (lane == 0) atomicOr(&r.mask[e], 1ull << t);
+        if (!on) {
+            if (lane < m.k) {
+                r.expert[t * m.k + lane] = kNone;
+                r.weight[t * m.k + lane] = 0.0f;
+                if (blockIdx.x == 0 && m.index) m.index[t * m.k + lane] = -1;
+                if (blockIdx.x == 0 && m.weight) m.weight[t * m.k + lane] = 0.0f;
             }
-            if (lane == 0) {
-                r.expert[t * m.k + j] = on ? static_cast<uint16_t>(e) : kNone;
-                if (blockIdx.x == 0 && m.index) m.index[t * m.k + j] = e;
-            }
+            continue;
         }
+        unsigned long long *keys = scratch + warp * kMoeMaxExperts;
+        unsigned long long best = 0;
+        for (int e = lane; e < m.E; e += 32) {
+            const unsigned long long key = moe_score_key(__ldcg(p.score + t * m.E + e), e);
+            keys[e] = key;
+            best = max(best, key);
+        }
+        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
+        const float top = moe_key_score(best);
         __syncwarp();
-        float sum = 0.0f;
-        if (on && m.renormalize) {
-            for (int j = 0; j < m.k; ++j) sum += r.weight[t * m.k + j];
-        } else if (on) {
-#pragma unroll
-            for (int i = 0; i < kMoeMaxExperts / 32; ++i)
-                if (i * 32 + lane < m.E) sum += expf(s[i] - top);
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        float sum = 0.0f;  // of every expert's exp(s - top), or of the chosen ones'
+        for (int e0 = 0; e0 < m.E; e0 += 32) {
+            const int e = e0 + lane;
+            const unsigned long long key = e < m.E ? keys[e] : 0ull;
+            int before = 0;
+#pragma unroll 8
+            for (int i = 0; i < m.E; ++i) before += keys[i] > key ? 1 : 0;
+            const bool chosen = e < m.E && before < m.k;
+            const float w = e < m.E ? expf(moe_key_score(key) - top) : 0.0f;
+            if (chosen || !m.renormalize) sum += w;
+            if (chosen) {
+                r.expert[t * m.k + before] = static_cast<uint16_t>(e);
+                r.weight[t * m.k + before] = w;
+                atomicOr(&r.mask[e], 1ull << t);
+                if (blockIdx.x == 0 && m.index) m.index[t * m.k + before] = e;
+            }
         }
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
         __syncwarp();
         if (lane < m.k) {
-            const float w = on ? r.weight[t * m.k + lane] / sum : 0.0f;
+            const float w = r.weight[t * m.k + lane] / sum;
             r.weight[t * m.k + lane] = w;
             if (blockIdx.x == 0 && m.weight) m.weight[t * m.k + lane] = w;
         }
+        __syncwarp();
     }
     __syncthreads();
     if (warp == 0) {
@@ -254,7 +254,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *acc_full = empty + STAGES;  // [2]
     uint64_t *acc_free = acc_full + 2;    // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
-    uint32_t *arrived = tmem_slot + 1;
     float *part = reinterpret_cast<float *>(tmem_slot + 2);  // [8]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,14 +287,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         grid_wait(&p.sync->gen, gen0 + 1);
     }
     __syncthreads();
-    moe_route(p, route);
+    moe_route(p, route, reinterpret_cast<unsigned long long *>(smem));  // the ring is still unused
 
+    // The ring's memory held the keys: order those accesses before the copies into it.
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
     const int n_active = route.n_active;
     UnitSplit up, down;
     up.total = n_active * p.tiles_f * p.kb_up;
-    up.ctas = min(up.total, static_cast<int>(ctas));
+    up.ctas = min(static_cast<int>(ctas), max(up.total / min_run(NT), min(n_active * p.tiles_f, static_cast<int>(ctas))));
     down.total = n_active * p.tiles_d * p.kb_down;
-    down.ctas = min(down.total, static_cast<int>(ctas));
+    down.ctas = min(static_cast<int>(ctas), max(down.total / min_run(NT), min(n_active * p.tiles_d, static_cast<int>(ctas))));
     const int cta = blockIdx.x;
     const int up0 = cta < up.ctas ? up.first(cta) : 0, up1 = cta < up.ctas ? up.first(cta + 1) : 0;
     const int dn0 = cta < down.ctas ? down.first(cta) : 0, dn1 = cta < down.ctas ? down.first(cta + 1) : 0;
@@ -423,10 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        constexpr size_t PIECE = static_cast<size_t>(NT) * kStreamRows;
         int j = 0;
         bool ok = true;  // after a wait that expired the loops run on without waiting, so that
-                         // every warp still meets the others at the barriers below
+                         // every warp still meets the others at the barrier below
         // h of expert e, hidden value f, tokens c .. c + 15
         auto emit = [&](int e, int f, int c, const float(&g)[16], const float(&v)[16]) {
             const unsigned long long mask = route.mask[e];
@@ -454,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int e = route.active[tile / p.tiles_f], f = tile % p.tiles_f * kStreamRows + row;
             const unsigned long long mask = route.mask[e];
             const bool whole = n_units == p.kb_up;
-            float *mine = p.up_pieces + (2 * cta + (kb0 == 0 ? 1 : 0)) * ACCS * PIECE + row;
+            const int slot = (2 * cta + (kb0 == 0 ? 1 : 0)) * ACCS;
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[ACCS][16];
@@ -477,42 +478,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     emit(e, f, c, g, v);
                 } else {
 #pragma unroll
-                    for (int a = 0; a < ACCS; ++a)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if ((mask >> (c + i)) & 1ull)
-                                __stcg(mine + a * PIECE + (c + i) * kStreamRows, __uint_as_float(r[a][i]));
+                    for (int a = 0; a < ACCS; ++a) put_piece<NT>(p.up_pieces, slot + a, c, row, m.T, r[a]);
                 }
             }
-            if (whole) continue;
-            __threadfence();
-            epilogue_barrier();
-            if (threadIdx.x == 128) {
-                __threadfence();
-                *arrived = atomicAdd(&p.counters[tile], static_cast<unsigned>(n_units)) + n_units;
-                if (*arrived == static_cast<unsigned>(p.kb_up)) p.counters[tile] = 0;
-            }
-            epilogue_barrier();
-            if (*arrived == static_cast<unsigned>(p.kb_up)) {
-                __threadfence();
-                const int c0 = up.owner(tile * p.kb_up), c1 = up.owner(tile * p.kb_up + p.kb_up - 1);
+            if (whole || !piece_arrived(p.counters + tile * 4 + (warp & 3), n_units, p.kb_up, lane)) continue;
+            const int c0 = up.owner(tile * p.kb_up), c1 = up.owner(tile * p.kb_up + p.kb_up - 1);
 #pragma unroll 1
-                for (int c = 0; c < NT; c += 16) {
-                    if (!((mask >> c) & 0xFFFFull)) continue;
-                    float g[16] = {}, v[16] = {};
-                    for (int k = c0; k <= c1; ++k) {
-                        const float *piece = p.up_pieces + (2 * k + (k == c0 ? 1 : 0)) * ACCS * PIECE + row;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if ((mask >> (c + i)) & 1ull) {
-                                v[i] += __ldcg(piece + (ACCS - 1) * PIECE + (c + i) * kStreamRows);
-                                if (GATED) g[i] += __ldcg(piece + (c + i) * kStreamRows);
-                            }
-                    }
-                    emit(e, f, c, g, v);
-                }
+            for (int c = 0; c < NT; c += 16) {
+                if (!((mask >> c) & 0xFFFFull)) continue;
+                float g[16], v[16];
+                sum_pieces<NT>(p.up_pieces, c0, c1, ACCS, ACCS - 1, c, row, m.T, v);
+                if (GATED)
+                    sum_pieces<NT>(p.up_pieces, c0, c1, ACCS, 0, c, row, m.T, g);
+                emit(e, f, c, g, v);
             }
-            epilogue_barrier();  // `arrived` is read before the next piece overwrites it
         }
         // This CTA's part of h is written: step 4 may read it through the async proxy.
         asm volatile("fence.proxy.async;" ::: "memory");
@@ -528,10 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_after_sync();
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * ACCS * NT);
             const int e = route.active[tile / p.tiles_d], rows = __popcll(route.mask[e]);
-            float *dst = n_units == p.kb_down
-                             ? p.out + route.offset[e] * ldo + tile % p.tiles_d * kStreamRows + row
-                             : p.down_pieces + (2 * cta + (kb0 == 0 ? 1 : 0)) * PIECE + row;
-            const long long step = n_units == p.kb_down ? ldo : kStreamRows;
+            const bool whole = n_units == p.kb_down;
+            float *dst = p.out + route.offset[e] * ldo + tile % p.tiles_d * kStreamRows + row;
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
@@ -542,9 +519,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_free[j & 1]);
                 }
+                if (whole) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (c + i < rows) __stcg(dst + (c + i) * step, __uint_as_float(r[i]));
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < rows) __stcg(dst + (c + i) * ldo, __uint_as_float(r[i]));
+                } else {
+                    put_piece<NT>(p.down_pieces, 2 * cta + (kb0 == 0 ? 1 : 0), c, row, rows, r);
+                }
             }
         }
     }
@@ -563,47 +544,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_after_sync();
         tmem_dealloc<1>(tmem, C::TMEM_COLS);
     }
-    constexpr size_t PIECE = static_cast<size_t>(NT) * kStreamRows;
     const long long ldo = static_cast<long long>(p.tiles_d) * kStreamRows;
-    const int quads = (m.D + 3) / 4;
-    for (long long i = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
-         i < static_cast<long long>(m.T) * quads; i += static_cast<long long>(ctas) * kThreads) {
-        const int t = static_cast<int>(i / quads), d = static_cast<int>(i - static_cast<long long>(t) * quads) * 4;
-        float y[4] = {};
+    // A warp's 32 lanes take 32 features of one token.
+    const int blocks = (m.D + 31) / 32;
+    const long long items = static_cast<long long>(m.T) * blocks;
+    for (long long i = blockIdx.x * (kThreads / 32) + warp; i < items; i += ctas * (kThreads / 32)) {
+        const int t = static_cast<int>(i / blocks);
+        const int d = static_cast<int>(i - static_cast<long long>(t) * blocks) * 32 + lane, row = d % kStreamRows;
+        if (d >= m.D) continue;
+        float y = 0.0f;
+        const float res = m.R ? H::widen(m.R[t * m.ldres + d]) : 0.0f;
+#pragma unroll 4
         for (int j = 0; j < m.k; ++j) {
-            const int pr = t * m.k + j;
-            if (route.expert[pr] == kNone) break;
-            const int e = route.expert[pr];
+            const int e = route.expert[t * m.k + j];
+            if (e == kNone) break;
             const int col = __popcll(route.mask[e] & ((1ull << t) - 1ull));
             const int tile = route.rank[e] * p.tiles_d + d / kStreamRows;
             const int c0 = down.owner(tile * p.kb_down), c1 = down.owner(tile * p.kb_down + p.kb_down - 1);
-            float4 s;
+            float s = 0.0f;
             if (c0 == c1) {
-                s = __ldcg(reinterpret_cast<const float4 *>(p.out + (route.offset[e] + col) * ldo + d));
+                s = __ldcg(p.out + (route.offset[e] + col) * ldo + d);
             } else {
-                s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int k = c0; k <= c1; ++k) {
-                    const float4 q = __ldcg(reinterpret_cast<const float4 *>(
-                        p.down_pieces + (2 * k + (k == c0 ? 1 : 0)) * PIECE + col * kStreamRows +
-                        d % kStreamRows));
-                    s.x += q.x;
-                    s.y += q.y;
-                    s.z += q.z;
-                    s.w += q.w;
-                }
+                for (int k = c0; k <= c1; ++k)
+                    s += __ldcg(reinterpret_cast<const float *>(
+                                    piece_at<NT>(p.down_pieces, 2 * k + (k == c0 ? 1 : 0), col / 4, row)) +
+                                col % 4);
             }
-            const float w = route.weight[pr];
-            y[0] = fmaf(w, s.x, y[0]);
-            y[1] = fmaf(w, s.y, y[1]);
-            y[2] = fmaf(w, s.z, y[2]);
-            y[3] = fmaf(w, s.w, y[3]);
+            y = fmaf(route.weight[t * m.k + j], s, y);
         }
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-            if (d + v < m.D) {
-                if (m.R) y[v] += H::widen(m.R[t * m.ldres + d + v]);
-                m.Y[t * m.ldy + d + v] = H::narrow(y[v]);
-            }
+        m.Y[t * m.ldy + d] = H::narrow(y + res);
     }
 }
 
@@ -645,7 +614,7 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
     const size_t pairs = static_cast<size_t>(m.T) * m.k, G = static_cast<size_t>(sms[dev]);
     const size_t experts = std::min<size_t>(m.E, pairs);
     void *sync = nullptr, *data = nullptr;
-    err = layer_scratch(kScratchMoeSync, stream, kSyncBytes + experts * p.tiles_f * 4, &sync, detail);
+    err = layer_scratch(kScratchMoeSync, stream, kSyncBytes + experts * p.tiles_f * 16, &sync, detail);
     if (err != cudaSuccess) return err;
     p.sync = static_cast<MoeSync *>(sync);
     p.counters = reinterpret_cast<unsigned int *>(static_cast<char *>(sync) + kSyncBytes);

@@ -5,8 +5,8 @@
 //   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns
 //   warp 2:         TMEM allocation
 //   warps 4..7:     epilogue: lane = output feature, columns = tokens. Whole tiles go from TMEM to
-//                   the epilogue; pieces go to scratch in fp32, and the CTA that completes a tile's
-//                   last piece sums them in the order of k.
+//                   the epilogue; pieces go to scratch in fp32, and the warp that completes its
+//                   32 rows of a tile sums them in the order of k.
 #include "activation16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
@@ -20,7 +20,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxDevices = 64;
-constexpr size_t kCounterBytes = 64 * 1024;  // one arrival counter per tile
+constexpr size_t kCounterBytes = 256 * 1024;  // arrival counters, four per tile
 
 struct StreamParams {
     int M, N;  // tokens, output features
@@ -35,8 +35,8 @@ struct StreamParams {
     long long ldd;
     uint16_t *pre;
     long long ldz;
-    unsigned int *counters;  // [tiles], zero between calls
-    float *pieces;           // [2 * CTAs][NT][128]
+    unsigned int *counters;  // [tiles][4 warps], zero between calls
+    float *pieces;           // [2 * CTAs][NT / 4][128][4]
 };
 
 template <int NT>
@@ -50,16 +50,11 @@ struct StreamConfig {
     static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
 };
 
-__device__ __forceinline__ void epilogue_barrier() {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
 // 16 columns (tokens m0 .. m0 + 15) of output feature n.
 template <typename T>
-__device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, float (&v)[16]) {
+__device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, float b, float (&v)[16]) {
     using H = Half16<T>;
     if (n >= p.N) return;
-    const float b = p.bias ? H::widen(p.bias[n]) : 0.0f;
     const int rows = min(16, p.M - m0);
     float r[16];
     if (p.res) {
@@ -95,7 +90,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *acc_full = empty + STAGES;  // [2]
     uint64_t *acc_free = acc_full + 2;    // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
-    uint32_t *arrived = tmem_slot + 1;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u0 = p.split.first(blockIdx.x), u1 = p.split.first(blockIdx.x + 1);
@@ -182,18 +176,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int j = 0;
-        bool ok = true;  // after a wait that expired the loop runs on without waiting, so that
-                         // every warp still meets the others at the barriers below
         for (int u = u0; u < u1; ++j) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
             const int n_units = min(p.KB - kb0, u1 - u);
             u += n_units;
-            ok = ok && mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+            const int n = tile * kStreamRows + row;
+            const float b = p.bias && n < p.N ? Half16<T>::widen(p.bias[n]) : 0.0f;
+            if (!mbar_wait(&acc_full[j & 1], (j >> 1) & 1)) break;
             tc_after_sync();
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * NT);
-            const int n = tile * kStreamRows + row;
             const bool whole = n_units == p.KB;
-            float *mine = p.pieces + static_cast<size_t>(2 * blockIdx.x + (kb0 == 0 ? 1 : 0)) * NT * kStreamRows + row;
 #pragma unroll 1
             for (int c = 0; c < NT; c += 16) {
                 uint32_t r[16];
@@ -209,40 +201,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T>(p, n, c, v);
+                    finish16<T>(p, n, c, b, v);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c + i < p.M) __stcg(mine + (c + i) * kStreamRows, __uint_as_float(r[i]));
+                    put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, p.M, r);
                 }
             }
-            if (whole) continue;
-            // A piece: count it; whoever completes the tile sums the pieces.
+            if (whole || !piece_arrived(p.counters + tile * 4 + (warp & 3), n_units, p.KB, lane)) continue;
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
-            __threadfence();
-            epilogue_barrier();
-            if (threadIdx.x == 128) {
-                __threadfence();
-                *arrived = atomicAdd(&p.counters[tile], 1u);
-                if (*arrived == static_cast<unsigned>(c1 - c0)) p.counters[tile] = 0;
-            }
-            epilogue_barrier();
-            const bool last = *arrived == static_cast<unsigned>(c1 - c0);
-            if (last) {
-                __threadfence();
 #pragma unroll 1
-                for (int c = 0; c < p.M; c += 16) {
-                    float v[16] = {};
-                    for (int k = c0; k <= c1; ++k) {
-                        const float *piece = p.pieces + static_cast<size_t>(2 * k + (k == c0 ? 1 : 0)) * NT * kStreamRows + row;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < p.M) v[i] += __ldcg(piece + (c + i) * kStreamRows);
-                    }
-                    finish16<T>(p, n, c, v);
-                }
+            for (int c = 0; c < p.M; c += 16) {
+                float v[16];
+                sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, p.M, v);
+                finish16<T>(p, n, c, b, v);
             }
-            epilogue_barrier();  // `arrived` is read before the next piece overwrites it
         }
     }
 
@@ -284,7 +255,7 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     p.tiles = static_cast<int>((g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows);
     p.KB = static_cast<int>((g.K + static_cast<long long>(kStreamK) - 1) / kStreamK);
     p.split.total = p.tiles * p.KB;
-    p.split.ctas = std::min(p.split.total, sms[dev]);
+    p.split.ctas = std::min(sms[dev], std::max({1, p.split.total / min_run(NT), std::min(p.tiles, sms[dev])}));
     p.idesc = idesc_16(kStreamRows, NT, Half16<T>::kind, W_MN, false);
     p.bias = g.bias;
     p.act = g.act;
@@ -331,7 +302,7 @@ cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **deta
 bool stream_gemm16_supports(const Gemm16 &g) {
     const long long tiles = (g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows;
     const long long blocks = (g.K + static_cast<long long>(kStreamK) - 1) / kStreamK;
-    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 4) &&
+    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 16) &&
            tiles * blocks <= 0x7fffffffLL;
 }
 
