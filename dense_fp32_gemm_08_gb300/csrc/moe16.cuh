@@ -5,17 +5,18 @@
 
 namespace sg {
 
-// Order of the router's scores as unsigned integers, with the index below it so that equal
-// scores go to the lowest expert: NaN above everything, -0 equal to +0.
-__device__ __forceinline__ unsigned long long moe_score_key(float s, int e) {
-    unsigned int u = __float_as_uint(s == 0.0f ? 0.0f : s);
-    u = s != s ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return (static_cast<unsigned long long>(u) << 32) | (0xFFFFFFFFu - static_cast<unsigned>(e));
+// The router's scores as unsigned integers of the same order: NaN above everything, -0 equal to +0.
+__device__ __forceinline__ unsigned int moe_score_order(float s) {
+    const unsigned int u = __float_as_uint(s == 0.0f ? 0.0f : s);
+    return s != s ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-// The score of a key (NaN gives a NaN).
-__device__ __forceinline__ float moe_key_score(unsigned long long key) {
-    const unsigned int u = static_cast<unsigned int>(key >> 32);
+// The score of such an integer (NaN gives a NaN).
+__device__ __forceinline__ float moe_order_score(unsigned int u) {
     return __uint_as_float((u & 0x80000000u) ? (u & 0x7FFFFFFFu) : ~u);
+}
+// With the index below it, so that equal scores go to the lowest expert.
+__device__ __forceinline__ unsigned long long moe_score_key(float s, int e) {
+    return (static_cast<unsigned long long>(moe_score_order(s)) << 32) | (0xFFFFFFFFu - static_cast<unsigned>(e));
 }
 
 // The fused kernel: needs operands TMA can address.

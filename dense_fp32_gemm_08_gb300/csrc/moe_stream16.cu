@@ -28,7 +28,6 @@
 namespace sg {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxDevices = 64;
 constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopk;
 
@@ -45,13 +44,13 @@ struct MoeParams {
     int tiles_d, kb_down;  // step 4: tiles of D, k-blocks of F
     uint32_t idesc;
     MoeSync *sync;
-    unsigned int *counters;  // [active experts * tiles_f][4 warps]: units of step 3 that arrived
+    unsigned int *counters;  // [active experts * tiles_f][epilogue warps]: units of step 3 that arrived
     float *score;            // [T][E]
     uint16_t *h;             // [T * k][ldh]
     long long ldh;
     float *out;              // [T * k][tiles_d * 128]: an expert's output for one token
     float *up_pieces;        // [2 * CTAs][accumulators][NT / 4][128][4]
-    float *down_pieces;      // [2 * CTAs][NT / 4][128][4]
+    float *down_pieces;      // [2 * CTAs][NT][128]
 };
 
 // What every CTA knows of the routing.
@@ -69,6 +68,8 @@ constexpr uint16_t kNone = 0xFFFF;
 template <int NT, bool GATED>
 struct MoeConfig {
     static constexpr int ACCS = GATED ? 2 : 1;
+    static constexpr int GROUPS = epilogue_groups(NT);
+    static constexpr int THREADS = 128 + 128 * GROUPS;
     static constexpr uint32_t W_BYTES = kStreamRows * kStreamK * 2;
     static constexpr uint32_t A_BYTES = ACCS * W_BYTES;
     static constexpr uint32_t X_BYTES = NT * kStreamK * 2;
@@ -104,67 +105,103 @@ __device__ __forceinline__ bool grid_wait(const unsigned int *gen, unsigned int 
         }
     }
 }
-__device__ __forceinline__ void epilogue_barrier() {
-    asm volatile("bar.sync 1, 128;" ::: "memory");
-}
 
 // ---- step 1: scores ---------------------------------------------------------------------------------
-// A warp per token (for fewer than 8 tokens, several warps share one token's D and their sums are
-// added in a fixed order).
+// This lane's share of a dot product: chunks of 8 values first, first + step, ...; eight chunks of
+// each row are under way at once where 16-byte loads are possible.
 template <typename T>
-__device__ __forceinline__ void moe_scores(const MoeParams &p, float *part) {
+__device__ __forceinline__ float dot_share(const uint16_t *x, const uint16_t *w, int D, int first, int step) {
     using H = Half16<T>;
+    const int chunks = (D + 7) / 8;
+    float s = 0.0f;
+    auto add = [&](const uint4 &a, const uint4 &b, int count) {
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 fa = H::widen2(av[i]), fb = H::widen2(bv[i]);
+            if (2 * i < count) s = fmaf(fa.x, fb.x, s);
+            if (2 * i + 1 < count) s = fmaf(fa.y, fb.y, s);
+        }
+    };
+    if (D % 8 == 0 && ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w)) & 15u) == 0) {
+        const uint4 *xv = reinterpret_cast<const uint4 *>(x), *wv = reinterpret_cast<const uint4 *>(w);
+        for (int c = first; c < chunks; c += 8 * step) {
+            uint4 a[8], b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i * step < chunks) {
+                    a[i] = __ldg(xv + c + i * step);
+                    b[i] = __ldg(wv + c + i * step);
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i * step < chunks) add(a[i], b[i], 8);
+        }
+    } else {
+        for (int c = first; c < chunks; c += step) {
+            const int count = min(8, D - 8 * c);
+            add(load8_any(x + 8 * c, count), load8_any(w + 8 * c, count), count);
+        }
+    }
+    return s;
+}
+
+// Every CTA for itself when there is a score per warp at most (`local`): the grid barrier that
+// would collect them costs about as much as they do. Otherwise an expert and 8 tokens per CTA, a
+// warp per token (for fewer than 8 tokens, several warps share one token's D and their sums are
+// added in a fixed order).
+__host__ __device__ inline bool scores_local(const Moe16 &m) { return m.T * m.E <= 8; }
+
+template <typename T, int THREADS>
+__device__ __forceinline__ void moe_scores(const MoeParams &p, float *part, float *local) {
     const Moe16 &m = p.m;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (warp >= 8 && scores_local(m)) return;
+    if (scores_local(m)) {
+        if (warp < m.T * m.E) {
+            const int t = warp / m.E, e = warp - t * m.E;
+            float s = 0.0f;
+            if (!(m.active && !m.active[t]))
+                s = dot_share<T>(m.X + t * m.ldx, m.Wr + e * m.ldr, m.D, lane, 32);
+            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (lane == 0) local[warp] = s;
+        }
+        return;
+    }
     const int slices = m.T >= 8 ? 1 : m.T >= 4 ? 2 : m.T >= 2 ? 4 : 8;
     const int slice = warp & (slices - 1), t_step = 8 / slices;
-    const int chunks = (m.D + 7) / 8;
     const int groups = (m.T + t_step - 1) / t_step;
     for (int item = blockIdx.x; item < m.E * groups; item += gridDim.x) {
         const int e = item / groups, t = (item - e * groups) * t_step + warp / slices;
-        const uint16_t *w = m.Wr + e * m.ldr;
-        {
-            float s = 0.0f;
-            if (t < m.T && !(m.active && !m.active[t])) {
-                const uint16_t *x = m.X + t * m.ldx;
-#pragma unroll 8
-                for (int c = slice * 32 + lane; c < chunks; c += slices * 32) {
-                    const int count = min(8, m.D - 8 * c);
-                    const uint4 a = load8_any(x + 8 * c, count), b = load8_any(w + 8 * c, count);
-                    const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 fa = H::widen2(av[i]), fb = H::widen2(bv[i]);
-                        if (2 * i < count) s = fmaf(fa.x, fb.x, s);
-                        if (2 * i + 1 < count) s = fmaf(fa.y, fb.y, s);
-                    }
-                }
-            }
-            for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (slices > 1) {
-                if (lane == 0) part[warp] = s;
-                __syncthreads();
-                s = 0.0f;
+        float s = 0.0f;
+        const bool mine = warp < 8 && t < m.T;
+        if (mine && !(m.active && !m.active[t]))
+            s = dot_share<T>(m.X + t * m.ldx, m.Wr + e * m.ldr, m.D, slice * 32 + lane, slices * 32);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        if (slices > 1) {
+            if (lane == 0 && warp < 8) part[warp] = s;
+            __syncthreads();
+            s = 0.0f;
+            if (mine)
                 for (int i = 0; i < slices; ++i) s += part[(warp & ~(slices - 1)) + i];
-                __syncthreads();
-            }
-            if (lane == 0 && slice == 0 && t < m.T) __stcg(p.score + t * m.E + e, s);
+            __syncthreads();
         }
+        if (lane == 0 && slice == 0 && mine) __stcg(p.score + t * m.E + e, s);
     }
 }
 
 // ---- step 2: routing ----------------------------------------------------------------------------------
-__device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r, unsigned long long *scratch) {
+// A warp per token, an expert's score in the registers of lane e % 32. Each chosen expert takes one
+// warp-wide maximum of the scores and one minimum of the indices that have it.
+template <int THREADS>
+__device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r, const float *local) {
     const Moe16 &m = p.m;
+    constexpr int REGS = kMoeMaxExperts / 32;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int e = threadIdx.x; e < m.E; e += kThreads) r.mask[e] = 0;
+    for (int e = threadIdx.x; e < m.E; e += THREADS) r.mask[e] = 0;
     __syncthreads();
-    // A warp per token. An expert's rank is the number of experts before it in the order of
-    // moe_score_key; every lane counts for its own experts against all of them in shared memory,
-    // which takes one pass over the scores instead of one reduction per chosen expert.
-    for (int t = warp; t < m.T; t += kThreads / 32) {
-        const bool on = !(m.active && !m.active[t]);
-        if (!on) {
+    for (int t = warp; t < m.T; t += THREADS / 32) {
+        if (m.active && !m.active[t]) {
             if (lane < m.k) {
                 r.expert[t * m.k + lane] = kNone;
                 r.weight[t * m.k + lane] = 0.0f;
@@ -173,41 +210,57 @@ __device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r, unsign
             }
             continue;
         }
-        unsigned long long *keys = scratch + warp * kMoeMaxExperts;
-        unsigned long long best = 0;
-        for (int e = lane; e < m.E; e += 32) {
-            const unsigned long long key = moe_score_key(__ldcg(p.score + t * m.E + e), e);
-            keys[e] = key;
-            best = max(best, key);
+        unsigned int key[REGS];  // 0, below every score, where there is no expert or none any more
+        unsigned int best = 0;
+#pragma unroll
+        for (int i = 0; i < REGS; ++i) {
+            const int e = i * 32 + lane;
+            key[i] = 0u;
+            if (i * 32 < m.E && e < m.E)
+                key[i] = moe_score_order(local ? local[t * m.E + e] : __ldcg(p.score + t * m.E + e));
         }
-        for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, o));
-        const float top = moe_key_score(best);
-        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < REGS; ++i) best = max(best, key[i]);
+        const float top = moe_order_score(__reduce_max_sync(0xFFFFFFFFu, best));
         float sum = 0.0f;  // of every expert's exp(s - top), or of the chosen ones'
-        for (int e0 = 0; e0 < m.E; e0 += 32) {
-            const int e = e0 + lane;
-            const unsigned long long key = e < m.E ? keys[e] : 0ull;
-            int before = 0;
-#pragma unroll 8
-            for (int i = 0; i < m.E; ++i) before += keys[i] > key ? 1 : 0;
-            const bool chosen = e < m.E && before < m.k;
-            const float w = e < m.E ? expf(moe_key_score(key) - top) : 0.0f;
-            if (chosen || !m.renormalize) sum += w;
-            if (chosen) {
-                r.expert[t * m.k + before] = static_cast<uint16_t>(e);
-                r.weight[t * m.k + before] = w;
-                atomicOr(&r.mask[e], 1ull << t);
-                if (blockIdx.x == 0 && m.index) m.index[t * m.k + before] = e;
+        if (!m.renormalize) {
+#pragma unroll
+            for (int i = 0; i < REGS; ++i)
+                if (i * 32 + lane < m.E) sum += expf(moe_order_score(key[i]) - top);
+        }
+        int chosen = -1;  // lane j keeps the j-th
+        float w = 0.0f;
+        for (int j = 0; j < m.k; ++j) {
+            unsigned int high = 0;
+            int at = 0x7FFFFFFF;
+#pragma unroll
+            for (int i = 0; i < REGS; ++i)
+                if (key[i] > high) {
+                    high = key[i];
+                    at = i * 32 + lane;
+                }
+            const unsigned int win = __reduce_max_sync(0xFFFFFFFFu, high);
+            const int e = __reduce_min_sync(0xFFFFFFFFu, high == win ? at : 0x7FFFFFFF);
+            if (lane == j) {
+                chosen = e;
+                w = expf(moe_order_score(win) - top);
+            }
+            if (lane == (e & 31)) {
+#pragma unroll
+                for (int i = 0; i < REGS; ++i)
+                    if (i == e >> 5) key[i] = 0u;
             }
         }
+        if (m.renormalize) sum = w;
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        __syncwarp();
         if (lane < m.k) {
-            const float w = r.weight[t * m.k + lane] / sum;
+            w = w / sum;
+            r.expert[t * m.k + lane] = static_cast<uint16_t>(chosen);
             r.weight[t * m.k + lane] = w;
+            atomicOr(reinterpret_cast<unsigned int *>(&r.mask[chosen]) + (t >> 5), 1u << (t & 31));
+            if (blockIdx.x == 0 && m.index) m.index[t * m.k + lane] = chosen;
             if (blockIdx.x == 0 && m.weight) m.weight[t * m.k + lane] = w;
         }
-        __syncwarp();
     }
     __syncthreads();
     if (warp == 0) {
@@ -236,7 +289,7 @@ __device__ __forceinline__ void moe_route(const MoeParams &p, Routing &r, unsign
 }
 
 template <int NT, bool GATED, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
     moe_stream_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_g,
                       const __grid_constant__ CUtensorMap map_u, const __grid_constant__ CUtensorMap map_d,
                       const __grid_constant__ CUtensorMap map_h, const MoeParams p) {
@@ -255,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *acc_free = acc_full + 2;    // [2]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
     float *part = reinterpret_cast<float *>(tmem_slot + 2);  // [8]
+    const bool local = scores_local(m);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const unsigned int ctas = gridDim.x;
@@ -272,26 +326,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < 2; ++j) {
             mbar_init(&acc_full[j], 1);
-            mbar_init(&acc_free[j], 4);
+            mbar_init(&acc_free[j], 4 * C::GROUPS);
         }
         mbar_init_fence();
     }
     if (warp == 2) tmem_alloc<1>(tmem_slot, C::TMEM_COLS);
-    moe_scores<T>(p, part);
+    moe_scores<T, C::THREADS>(p, part, part);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
-    if (threadIdx.x == 0) {
-        grid_arrive(&p.sync->count[0], &p.sync->gen, ctas);
-        grid_wait(&p.sync->gen, gen0 + 1);
+    if (!local) {
+        if (threadIdx.x == 0) {
+            grid_arrive(&p.sync->count[0], &p.sync->gen, ctas);
+            grid_wait(&p.sync->gen, ++gen0);
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    moe_route(p, route, reinterpret_cast<unsigned long long *>(smem));  // the ring is still unused
-
-    // The ring's memory held the keys: order those accesses before the copies into it.
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncthreads();
+    moe_route<C::THREADS>(p, route, local ? part : nullptr);
     const int n_active = route.n_active;
     UnitSplit up, down;
     up.total = n_active * p.tiles_f * p.kb_up;
@@ -345,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             auto open_gate = [&]() {
-                ok = grid_wait(&p.sync->gen, gen0 + 2) && ok;
+                ok = grid_wait(&p.sync->gen, gen0 + 1) && ok;
                 asm volatile("fence.proxy.async;" ::: "memory");  // h was written by plain stores
                 open = true;
                 for (; waiting > 0; --waiting) load_rows();
@@ -425,6 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        constexpr int COLS = NT / C::GROUPS;
+        const int first_col = (warp - 4) / 4 * COLS, end_col = first_col + COLS;
         int j = 0;
         bool ok = true;  // after a wait that expired the loops run on without waiting, so that
                          // every warp still meets the others at the barrier below
@@ -457,12 +511,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = n_units == p.kb_up;
             const int slot = (2 * cta + (kb0 == 0 ? 1 : 0)) * ACCS;
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = first_col; c < end_col; c += 16) {
                 uint32_t r[ACCS][16];
 #pragma unroll
                 for (int a = 0; a < ACCS; ++a) tmem_ld_x16(acc + static_cast<uint32_t>(a * NT + c), r[a]);
                 tmem_ld_wait();
-                if (c + 16 == NT) {
+                if (c + 16 == end_col) {
                     tc_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_free[j & 1]);
@@ -481,10 +535,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int a = 0; a < ACCS; ++a) put_piece<NT>(p.up_pieces, slot + a, c, row, m.T, r[a]);
                 }
             }
-            if (whole || !piece_arrived(p.counters + tile * 4 + (warp & 3), n_units, p.kb_up, lane)) continue;
+            if (whole || !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.kb_up, lane))
+                continue;
             const int c0 = up.owner(tile * p.kb_up), c1 = up.owner(tile * p.kb_up + p.kb_up - 1);
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = first_col; c < end_col; c += 16) {
                 if (!((mask >> c) & 0xFFFFull)) continue;
                 float g[16], v[16];
                 sum_pieces<NT>(p.up_pieces, c0, c1, ACCS, ACCS - 1, c, row, m.T, v);
@@ -496,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // This CTA's part of h is written: step 4 may read it through the async proxy.
         asm volatile("fence.proxy.async;" ::: "memory");
         __threadfence();
-        epilogue_barrier();
+        asm volatile("bar.sync 1, %0;" ::"n"(128 * C::GROUPS) : "memory");  // the epilogue's warps
         if (threadIdx.x == 128) grid_arrive(&p.sync->count[1], &p.sync->gen, ctas);
         const long long ldo = static_cast<long long>(p.tiles_d) * kStreamRows;
         for (int u = dn0; u < dn1; ++j) {
@@ -510,11 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool whole = n_units == p.kb_down;
             float *dst = p.out + route.offset[e] * ldo + tile % p.tiles_d * kStreamRows + row;
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = first_col; c < end_col; c += 16) {
                 uint32_t r[16];
                 tmem_ld_x16(acc + static_cast<uint32_t>(c), r);
                 tmem_ld_wait();
-                if (c + 16 == NT) {
+                if (c + 16 == end_col) {
                     tc_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_free[j & 1]);
@@ -524,7 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i)
                         if (c + i < rows) __stcg(dst + (c + i) * ldo, __uint_as_float(r[i]));
                 } else {
-                    put_piece<NT>(p.down_pieces, 2 * cta + (kb0 == 0 ? 1 : 0), c, row, rows, r);
+                    float *piece = p.down_pieces +
+                                   static_cast<size_t>(2 * cta + (kb0 == 0 ? 1 : 0)) * NT * kStreamRows + row;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c + i < rows) __stcg(piece + (c + i) * kStreamRows, __uint_as_float(r[i]));
                 }
             }
         }
@@ -537,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (threadIdx.x == 0) {
         grid_arrive(&p.sync->count[2], &p.sync->gen, ctas);
-        grid_wait(&p.sync->gen, gen0 + 3);
+        grid_wait(&p.sync->gen, gen0 + 2);
     }
     __syncthreads();
     if (warp == 2) {
@@ -545,34 +604,67 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc<1>(tmem, C::TMEM_COLS);
     }
     const long long ldo = static_cast<long long>(p.tiles_d) * kStreamRows;
-    // A warp's 32 lanes take 32 features of one token.
-    const int blocks = (m.D + 31) / 32;
-    const long long items = static_cast<long long>(m.T) * blocks;
-    for (long long i = blockIdx.x * (kThreads / 32) + warp; i < items; i += ctas * (kThreads / 32)) {
-        const int t = static_cast<int>(i / blocks);
-        const int d = static_cast<int>(i - static_cast<long long>(t) * blocks) * 32 + lane, row = d % kStreamRows;
-        if (d >= m.D) continue;
-        float y = 0.0f;
-        const float res = m.R ? H::widen(m.R[t * m.ldres + d]) : 0.0f;
-#pragma unroll 4
-        for (int j = 0; j < m.k; ++j) {
-            const int e = route.expert[t * m.k + j];
-            if (e == kNone) break;
-            const int col = __popcll(route.mask[e] & ((1ull << t) - 1ull));
-            const int tile = route.rank[e] * p.tiles_d + d / kStreamRows;
-            const int c0 = down.owner(tile * p.kb_down), c1 = down.owner(tile * p.kb_down + p.kb_down - 1);
-            float s = 0.0f;
-            if (c0 == c1) {
-                s = __ldcg(p.out + (route.offset[e] + col) * ldo + d);
-            } else {
-                for (int k = c0; k <= c1; ++k)
-                    s += __ldcg(reinterpret_cast<const float *>(
-                                    piece_at<NT>(p.down_pieces, 2 * k + (k == c0 ? 1 : 0), col / 4, row)) +
-                                col % 4);
-            }
-            y = fmaf(route.weight[t * m.k + j], s, y);
+    // A warp takes 128 features of one token, four per lane; lane j finds where its j-th expert's
+    // output lies (a whole tile's in `out`, a cut one's in pieces first .. last).
+    constexpr int WARPS = C::THREADS / 32;
+    const long long items = static_cast<long long>(m.T) * p.tiles_d;
+    for (long long i = blockIdx.x * WARPS + warp; i < items; i += ctas * WARPS) {
+        const int t = static_cast<int>(i / p.tiles_d), tile_d = static_cast<int>(i - static_cast<long long>(t) * p.tiles_d);
+        const int d = tile_d * kStreamRows + 4 * lane, count = min(4, m.D - d);
+        float y[4] = {}, res[4] = {};
+        if (m.R)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (v < count) res[v] = H::widen(m.R[t * m.ldres + d + v]);
+        int col = 0, first = -1, last = -1, out_row = 0;
+        const int e = lane < m.k ? route.expert[t * m.k + lane] : kNone;
+        if (e != kNone) {
+            col = __popcll(route.mask[e] & ((1ull << t) - 1ull));
+            out_row = route.offset[e] + col;
+            const int unit = (route.rank[e] * p.tiles_d + tile_d) * p.kb_down;
+            first = down.owner(unit);
+            last = down.owner(unit + p.kb_down - 1);
         }
-        m.Y[t * m.ldy + d] = H::narrow(y + res);
+        auto piece = [&](int slot, int c) {
+            return __ldcg(reinterpret_cast<const float4 *>(
+                p.down_pieces + (static_cast<size_t>(slot) * NT + c) * kStreamRows + 4 * lane));
+        };
+        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        // Four experts' values under way at once, in up to two pieces each; more pieces are rare.
+        for (int j0 = 0; j0 < m.k; j0 += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // m.k is at most 16: a lane of its own for each
+                const int c0 = __shfl_sync(0xFFFFFFFFu, first, j0 + q), c1 = __shfl_sync(0xFFFFFFFFu, last, j0 + q);
+                const int cj = __shfl_sync(0xFFFFFFFFu, col, j0 + q), rj = __shfl_sync(0xFFFFFFFFu, out_row, j0 + q);
+                a[q] = c0 < 0 ? zero
+                       : c0 == c1 ? __ldcg(reinterpret_cast<const float4 *>(p.out + rj * ldo + d))
+                                  : piece(2 * c0 + 1, cj);
+                b[q] = c0 < c1 ? piece(2 * (c0 + 1), cj) : zero;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int c0 = __shfl_sync(0xFFFFFFFFu, first, j0 + q), c1 = __shfl_sync(0xFFFFFFFFu, last, j0 + q);
+                const int cj = __shfl_sync(0xFFFFFFFFu, col, j0 + q);
+                if (c0 < 0) continue;
+                float4 s = make_float4(a[q].x + b[q].x, a[q].y + b[q].y, a[q].z + b[q].z, a[q].w + b[q].w);
+                for (int k = c0 + 2; k <= c1; ++k) {
+                    const float4 x = piece(2 * k, cj);
+                    s.x += x.x;
+                    s.y += x.y;
+                    s.z += x.z;
+                    s.w += x.w;
+                }
+                const float w = route.weight[t * m.k + j0 + q];
+                y[0] = fmaf(w, s.x, y[0]);
+                y[1] = fmaf(w, s.y, y[1]);
+                y[2] = fmaf(w, s.z, y[2]);
+                y[3] = fmaf(w, s.w, y[3]);
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (v < count) m.Y[t * m.ldy + d + v] = H::narrow(y[v] + res[v]);
     }
 }
 
@@ -614,7 +706,7 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
     const size_t pairs = static_cast<size_t>(m.T) * m.k, G = static_cast<size_t>(sms[dev]);
     const size_t experts = std::min<size_t>(m.E, pairs);
     void *sync = nullptr, *data = nullptr;
-    err = layer_scratch(kScratchMoeSync, stream, kSyncBytes + experts * p.tiles_f * 16, &sync, detail);
+    err = layer_scratch(kScratchMoeSync, stream, kSyncBytes + experts * p.tiles_f * 16 * C::GROUPS, &sync, detail);
     if (err != cudaSuccess) return err;
     p.sync = static_cast<MoeSync *>(sync);
     p.counters = reinterpret_cast<unsigned int *>(static_cast<char *>(sync) + kSyncBytes);
@@ -645,7 +737,7 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
     if (!GATED) mg = mu;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(G), 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

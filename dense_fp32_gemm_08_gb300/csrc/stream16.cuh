@@ -23,7 +23,9 @@ struct UnitSplit {
         return static_cast<int>(static_cast<long long>(c) * total / ctas);
     }
     __device__ __forceinline__ int owner(int unit) const {
-        return static_cast<int>(((unit + 1LL) * ctas - 1) / total);
+        const unsigned long long x = (unit + 1ull) * ctas - 1;
+        if (x >> 32) return static_cast<int>(x / total);
+        return static_cast<int>(static_cast<unsigned>(x) / static_cast<unsigned>(total));
     }
 };
 
@@ -80,6 +82,10 @@ __device__ __forceinline__ bool piece_arrived(unsigned int *counter, int units, 
     __threadfence();
     return true;
 }
+// Epilogue warps: 4 (one per 32 rows) for up to 32 columns, 8 for 64 and so on: half the columns
+// each, so that their round trips to memory overlap.
+__host__ __device__ constexpr int epilogue_groups(int nt) { return nt <= 32 ? 1 : nt / 32; }
+
 // Runs of fewer units would cut a tile into more pieces than summing them in turn is worth (a
 // unit streams in about 0.1 us, a piece of 16 columns is summed in 0.2 us, of 64 in 0.8 us).
 __host__ __device__ constexpr int min_run(int nt) { return 8 + nt / 8; }

@@ -1,6 +1,6 @@
 // stream_gemm16.cu: D = act(A . B + bias) + res on 16-bit values for few rows of A (tokens), bound
 // by streaming B (the weights) from memory once. The split of the work is in stream16.cuh. Roles
-// of a CTA's 8 warps:
+// of a CTA's warps:
 //   warp 0, lane 0: TMA producer (a 128 x 64 block of weights and the tokens' 64 k values per unit)
 //   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns
 //   warp 2:         TMEM allocation
@@ -18,9 +18,8 @@
 namespace sg {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxDevices = 64;
-constexpr size_t kCounterBytes = 256 * 1024;  // arrival counters, four per tile
+constexpr size_t kCounterBytes = 256 * 1024;  // arrival counters, up to 8 per tile
 
 struct StreamParams {
     int M, N;  // tokens, output features
@@ -35,7 +34,7 @@ struct StreamParams {
     long long ldd;
     uint16_t *pre;
     long long ldz;
-    unsigned int *counters;  // [tiles][4 warps], zero between calls
+    unsigned int *counters;  // [tiles][epilogue warps], zero between calls
     float *pieces;           // [2 * CTAs][NT / 4][128][4]
 };
 
@@ -44,8 +43,12 @@ struct StreamConfig {
     static constexpr uint32_t A_BYTES = kStreamRows * kStreamK * 2;
     static constexpr uint32_t B_BYTES = NT * kStreamK * 2;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int STAGES = static_cast<int>(220 * 1024 / STAGE_BYTES) < 12
-                                      ? static_cast<int>(220 * 1024 / STAGE_BYTES) : 12;
+    static constexpr int GROUPS = epilogue_groups(NT);
+    static constexpr int THREADS = 128 + 128 * GROUPS;
+    // About 100 KiB of ring: enough in flight for the memory's full rate, and two CTAs fit on an SM,
+    // so that the stream's next such kernel is resident, and its first weights on their way to L2,
+    // while this one finishes.
+    static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;
     static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
     static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
 };
@@ -77,7 +80,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
 }
 
 template <int NT, bool W_MN, typename T>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const StreamParams p) {
     using C = StreamConfig<NT>;
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int j = 0; j < 2; ++j) {
             mbar_init(&acc_full[j], 1);
-            mbar_init(&acc_free[j], 4);
+            mbar_init(&acc_free[j], 4 * C::GROUPS);
         }
         mbar_init_fence();
     }
@@ -112,7 +115,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_after_sync();
     const uint32_t tmem = *tmem_slot;
-    grid_dependents();  // after the TMEM allocation: a later kernel's CTA cannot take it first
+    // The weights of the first stages go to L2 while the kernels before this one finish. (They are
+    // read only after those have: L2 sees any write in between.)
+    auto load_weights = [&](uint8_t *dst, uint64_t *bar, int tile, int kb) {
+        if (W_MN) {
+            tma_load_2d(dst, &map_w, bar, tile * kStreamRows, kb * kStreamK);
+            tma_load_2d(dst + 8192, &map_w, bar, tile * kStreamRows + 64, kb * kStreamK);
+        } else {
+            tma_load_2d(dst, &map_w, bar, kb * kStreamK, tile * kStreamRows);
+        }
+    };
+    if (threadIdx.x == 0) {
+        for (int u = u0; u < min(u1, u0 + STAGES); ++u) {
+            const int tile = u / p.KB, kb = u - tile * p.KB;
+            if (W_MN) {
+                tma_prefetch_2d(&map_w, tile * kStreamRows, kb * kStreamK);
+                tma_prefetch_2d(&map_w, tile * kStreamRows + 64, kb * kStreamK);
+            } else {
+                tma_prefetch_2d(&map_w, kb * kStreamK, tile * kStreamRows);
+            }
+        }
+    }
     grid_dependency();
 
     if (warp == 0) {
@@ -125,12 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *sw = smem + ring.stage * C::STAGE_BYTES, *sx = sw + C::A_BYTES;
                 uint64_t *bar = &full[ring.stage];
                 mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-                if (W_MN) {
-                    tma_load_2d(sw, &map_w, bar, tile * kStreamRows, kb * kStreamK);
-                    tma_load_2d(sw + 8192, &map_w, bar, tile * kStreamRows + 64, kb * kStreamK);
-                } else {
-                    tma_load_2d(sw, &map_w, bar, kb * kStreamK, tile * kStreamRows);
-                }
+                load_weights(sw, bar, tile, kb);
                 tma_load_2d(sx, &map_x, bar, kb * kStreamK, 0);
                 ring.next();
                 ++issued;
@@ -139,6 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++tile;
                 }
             }
+            grid_dependents();  // every copy is on its way: the next kernel may start its prologue
             // Shared memory must outlive every copy: wait (bounded) for the last stages.
             for (int j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
                 if (!mbar_wait(&full[j % STAGES], (j / STAGES) & 1)) break;
@@ -175,6 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        constexpr int COLS = NT / C::GROUPS;
+        const int first_col = (warp - 4) / 4 * COLS;
         int j = 0;
         for (int u = u0; u < u1; ++j) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
@@ -187,11 +208,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * NT);
             const bool whole = n_units == p.KB;
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = first_col; c < first_col + COLS; c += 16) {
                 uint32_t r[16];
                 tmem_ld_x16(acc + static_cast<uint32_t>(c), r);
                 tmem_ld_wait();
-                if (c + 16 == NT) {
+                if (c + 16 == first_col + COLS) {
                     tc_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_free[j & 1]);
@@ -206,10 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, p.M, r);
                 }
             }
-            if (whole || !piece_arrived(p.counters + tile * 4 + (warp & 3), n_units, p.KB, lane)) continue;
+            if (whole || first_col >= p.M ||
+                !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.KB, lane))
+                continue;
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
 #pragma unroll 1
-            for (int c = 0; c < p.M; c += 16) {
+            for (int c = first_col; c < min(p.M, first_col + COLS); c += 16) {
                 float v[16];
                 sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, p.M, v);
                 finish16<T>(p, n, c, b, v);
@@ -267,7 +290,7 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     p.ldz = g.ldz;
     void *ws = nullptr;
     err = layer_scratch(kScratchStream, stream,
-                        kCounterBytes + static_cast<size_t>(2) * sms[dev] * 256 * kStreamRows * 4, &ws, detail);
+                        kCounterBytes + static_cast<size_t>(2) * sms[dev] * 64 * kStreamRows * 4, &ws, detail);
     if (err != cudaSuccess) return err;
     p.counters = static_cast<unsigned int *>(ws);
     p.pieces = reinterpret_cast<float *>(static_cast<char *>(ws) + kCounterBytes);
@@ -278,7 +301,7 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
         *detail = "cuTensorMapEncodeTiled rejected a matrix";
         return cudaErrorInvalidValue;
     }
-    err = launch_early(kernel, dim3(p.split.ctas), kThreads, C::SMEM, stream, mw, mx, p);
+    err = launch_early(kernel, dim3(p.split.ctas), C::THREADS, C::SMEM, stream, mw, mx, p);
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
     return err;
 }
@@ -292,9 +315,7 @@ template <typename T>
 cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     if (g.M <= 16) return launch_major<16, T>(g, stream, detail);
     if (g.M <= 32) return launch_major<32, T>(g, stream, detail);
-    if (g.M <= 64) return launch_major<64, T>(g, stream, detail);
-    if (g.M <= 128) return launch_major<128, T>(g, stream, detail);
-    return launch_major<256, T>(g, stream, detail);
+    return launch_major<64, T>(g, stream, detail);
 }
 
 }  // namespace
@@ -302,7 +323,7 @@ cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **deta
 bool stream_gemm16_supports(const Gemm16 &g) {
     const long long tiles = (g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows;
     const long long blocks = (g.K + static_cast<long long>(kStreamK) - 1) / kStreamK;
-    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 16) &&
+    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 32) &&
            tiles * blocks <= 0x7fffffffLL;
 }
 
