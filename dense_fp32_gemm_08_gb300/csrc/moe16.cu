@@ -72,52 +72,113 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const Moe16 m, int *ind
         }
 }
 
-// A warp per hidden value f of one (token, choice) pair; h stays in fp32.
-template <typename T>
-__global__ void __launch_bounds__(256) moe_up_kernel(const Moe16 m, const int *index, float *h) {
+// ---- weights that TMA cannot address ----------------------------------------------------------------
+//
+// The products by fp32 FMAs: the rows are read as the aligned 4-byte words around them, 128 bytes
+// per warp and instruction and several rows at once, against values of x (or h) in shared memory.
+// Each (token, choice) reads its expert's weights; the choices of one expert run at the same time,
+// so that memory sees them about once.
+constexpr int kSpan = 4096;  // values of x or h in shared memory at a time
+
+// sum[r] += w_r[0 .. count) . x over this lane's words, ROWS rows at once.
+template <typename T, int ROWS>
+__device__ __forceinline__ void dot_rows(const uint16_t *const (&w)[ROWS], const float *x, int count, int lane,
+                                         float (&sum)[ROWS]) {
     using H = Half16<T>;
-    const int lane = threadIdx.x & 31;
-    const long long f = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int pair = blockIdx.y, t = pair / m.k, e = index[pair];
-    if (f >= m.F || e < 0) return;
-    const uint16_t *x = m.X + t * m.ldx;
-    const uint16_t *u = m.Wu + e * m.su + f * m.ldu;
-    const uint16_t *g = m.Wg ? m.Wg + e * m.su + f * m.ldu : nullptr;
-    float su = 0.0f, sgate = 0.0f;
-    for (int i = lane; i < m.D; i += 32) {
-        const float xv = H::widen(x[i]);
-        su = fmaf(xv, H::widen(u[i]), su);
-        if (g) sgate = fmaf(xv, H::widen(g[i]), sgate);
+    constexpr int UNROLL = 16 / ROWS;
+    const uint32_t *p[ROWS];
+    int shift[ROWS], words = 0;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(w[r]);
+        p[r] = reinterpret_cast<const uint32_t *>(a & ~static_cast<uintptr_t>(3));
+        shift[r] = static_cast<int>(a & 2u) >> 1;
+        words = max(words, (count + shift[r] + 1) / 2);
     }
-    for (int o = 16; o > 0; o >>= 1) {
-        su += __shfl_xor_sync(0xFFFFFFFFu, su, o);
-        sgate += __shfl_xor_sync(0xFFFFFFFFu, sgate, o);
+    for (int i0 = lane; i0 < words; i0 += 32 * UNROLL) {
+        uint32_t v[UNROLL][ROWS];
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+                if (2 * (i0 + 32 * u) - shift[r] < count) v[u][r] = __ldg(p[r] + i0 + 32 * u);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                const int at = 2 * (i0 + 32 * u) - shift[r];  // the word's first value
+                if (at >= count) continue;
+                const float2 f = H::widen2(v[u][r]);
+                if (at >= 0) sum[r] = fmaf(f.x, x[at], sum[r]);
+                if (at + 1 < count) sum[r] = fmaf(f.y, x[at + 1], sum[r]);
+            }
     }
-    if (lane == 0) h[pair * static_cast<long long>(m.F) + f] = g ? activate(sgate, m.act) * su : activate(su, m.act);
 }
 
-// A warp per output value d of one token: the choices in ascending j, then the residual.
+// Two hidden values f per warp (and their gates) of one (token, choice); h stays in fp32.
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(256) moe_up_kernel(const Moe16 m, const int *index, float *h) {
+    using H = Half16<T>;
+    __shared__ float x[kSpan];
+    const int lane = threadIdx.x & 31;
+    const int pair = blockIdx.y, t = pair / m.k, e = index[pair];
+    if (e < 0) return;
+    const int f = blockIdx.x * 16 + (threadIdx.x >> 5) * 2;
+    constexpr int ROWS = GATED ? 4 : 2;
+    float sum[ROWS] = {};
+    for (int d0 = 0; d0 < m.D; d0 += kSpan) {
+        const int count = min(kSpan, m.D - d0);
+        __syncthreads();
+        for (int i = threadIdx.x; i < count; i += 256) x[i] = H::widen(m.X[t * m.ldx + d0 + i]);
+        __syncthreads();
+        const uint16_t *w[ROWS];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)  // a row past the last repeats it: its sum is not used
+            w[r] = (r < 2 ? m.Wu : m.Wg) + e * m.su + min(f + (r & 1), m.F - 1) * m.ldu + d0;
+        dot_rows<T, ROWS>(w, x, count, lane, sum);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+        for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], o);
+    if (lane < 2 && f + lane < m.F) {
+        const float u = lane ? sum[1] : sum[0], g = lane ? sum[ROWS - 1] : sum[ROWS - 2];
+        h[pair * static_cast<long long>(m.F) + f + lane] = GATED ? activate(g, m.act) * u : activate(u, m.act);
+    }
+}
+
+// Four output values d per warp of one token: the choices in ascending j, then the residual.
 template <typename T>
 __global__ void __launch_bounds__(256) moe_down_kernel(const Moe16 m, const int *index,
                                                        const float *weight, const float *h) {
     using H = Half16<T>;
+    __shared__ float x[kSpan];
     const int lane = threadIdx.x & 31, t = blockIdx.y;
-    const long long d = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (d >= m.D) return;
-    float y = 0.0f;
+    const int d = blockIdx.x * 32 + (threadIdx.x >> 5) * 4;
+    float y[4] = {};
     for (int j = 0; j < m.k; ++j) {
         const int pair = t * m.k + j, e = index[pair];
         if (e < 0) continue;
-        const uint16_t *wd = m.Wd + e * m.sd + d * m.ldd;
-        const float *hv = h + pair * static_cast<long long>(m.F);
-        float s = 0.0f;
-        for (int i = lane; i < m.F; i += 32) s = fmaf(hv[i], H::widen(wd[i]), s);
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        y = fmaf(weight[pair], s, y);
+        float sum[4] = {};
+        for (int f0 = 0; f0 < m.F; f0 += kSpan) {
+            const int count = min(kSpan, m.F - f0);
+            __syncthreads();
+            for (int i = threadIdx.x; i < count; i += 256) x[i] = h[pair * static_cast<long long>(m.F) + f0 + i];
+            __syncthreads();
+            const uint16_t *w[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[r] = m.Wd + e * m.sd + min(d + r, m.D - 1) * m.ldd + f0;
+            dot_rows<T, 4>(w, x, count, lane, sum);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], o);
+            y[r] = fmaf(weight[pair], sum[r], y[r]);
+        }
     }
-    if (lane == 0) {
-        if (m.R) y += H::widen(m.R[t * m.ldres + d]);
-        m.Y[t * m.ldy + d] = H::narrow(y);
+    if (lane < 4 && d + lane < m.D) {
+        float v = lane == 0 ? y[0] : lane == 1 ? y[1] : lane == 2 ? y[2] : y[3];
+        if (m.R) v += H::widen(m.R[t * m.ldres + d + lane]);
+        m.Y[t * m.ldy + d + lane] = H::narrow(v);
     }
 }
 
@@ -131,10 +192,12 @@ cudaError_t launch(const Moe16 &m, cudaStream_t stream, const char **detail) {
     float *weight = reinterpret_cast<float *>(index + pairs);
     float *h = weight + pairs;
     moe_router_kernel<T><<<m.T, 256, 0, stream>>>(m, index, weight);
-    if (m.F > 0)
-        moe_up_kernel<T><<<dim3((m.F + 7) / 8, static_cast<unsigned>(pairs)), 256, 0, stream>>>(m, index, h);
+    if (m.F > 0) {
+        auto up = m.Wg ? moe_up_kernel<T, true> : moe_up_kernel<T, false>;
+        up<<<dim3((m.F + 15LL) / 16, static_cast<unsigned>(pairs)), 256, 0, stream>>>(m, index, h);
+    }
     if (m.D > 0)
-        moe_down_kernel<T><<<dim3((m.D + 7) / 8, m.T), 256, 0, stream>>>(m, index, weight, h);
+        moe_down_kernel<T><<<dim3((m.D + 31LL) / 32, m.T), 256, 0, stream>>>(m, index, weight, h);
     err = cudaGetLastError();
     if (err != cudaSuccess) *detail = "mixture-of-experts kernel launch failed";
     return err;
