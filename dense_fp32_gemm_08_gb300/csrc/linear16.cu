@@ -259,10 +259,11 @@ cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const 
             }
         }
     }
-    // Products that stream weights for a few rows go alone; the others share one launch.
+    // Products that stream weights for a few rows go alone; the others share one launch (and a
+    // gradient's two always do when there are more rows: apart, they took longer).
     int together = 0;
     for (int i = 0; i < products; ++i) {
-        if (stream_gemm16_supports(q[i])) {
+        if (stream_gemm16_supports(q[i]) && (n == 1 || q[i].M <= 64)) {
             err = stream_gemm16_launch(q[i], stream, detail);
             if (err != cudaSuccess) return err;
         } else {

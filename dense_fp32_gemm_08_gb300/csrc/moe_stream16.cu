@@ -68,7 +68,7 @@ constexpr uint16_t kNone = 0xFFFF;
 template <int NT, bool GATED>
 struct MoeConfig {
     static constexpr int ACCS = GATED ? 2 : 1;
-    static constexpr int GROUPS = epilogue_groups(NT);
+    static constexpr int GROUPS = NT / 32 > 0 ? NT / 32 : 1;  // of epilogue warps, 32 columns each
     static constexpr int THREADS = 128 + 128 * GROUPS;
     static constexpr uint32_t W_BYTES = kStreamRows * kStreamK * 2;
     static constexpr uint32_t A_BYTES = ACCS * W_BYTES;

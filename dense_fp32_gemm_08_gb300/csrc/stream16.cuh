@@ -2,8 +2,8 @@
 // large weights): the split of the work over CTAs, the shared-memory ring and the MMA loop.
 //
 // The product is computed transposed: a tile's 128 rows are 128 output features (weights are the
-// MMA's A operand) and its NT columns are the tokens, so that every weight passes through shared
-// memory once, whatever the number of tokens up to 256. The k-blocks of all tiles form one line
+// MMA's A operand) and its NT columns are tokens, so that every weight passes through shared memory
+// once for up to NT tokens. The k-blocks of all tiles form one line
 // of units, cut into equal runs, one per CTA (one CTA per SM): each SM streams the same number of
 // bytes, however few tiles there are. A tile cut between CTAs is summed in fp32 from its pieces
 // in the order of k, by the warp whose piece arrives last (nothing waits).
@@ -82,10 +82,6 @@ __device__ __forceinline__ bool piece_arrived(unsigned int *counter, int units, 
     __threadfence();
     return true;
 }
-// Epilogue warps: 4 (one per 32 rows) for up to 32 columns, 8 for 64 and so on: half the columns
-// each, so that their round trips to memory overlap.
-__host__ __device__ constexpr int epilogue_groups(int nt) { return nt <= 32 ? 1 : nt / 32; }
-
 // Runs of fewer units would cut a tile into more pieces than summing them in turn is worth (a
 // unit streams in about 0.1 us, a piece of 16 columns is summed in 0.2 us, of 64 in 0.8 us).
 __host__ __device__ constexpr int min_run(int nt) { return 8 + nt / 8; }

@@ -19,11 +19,11 @@ namespace sg {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kCounterBytes = 256 * 1024;  // arrival counters, up to 8 per tile
+constexpr size_t kCounterBytes = 512 * 1024;  // arrival counters, up to 16 per tile
 
 struct StreamParams {
     int M, N;  // tokens, output features
-    int tiles, KB;
+    int tiles, KB, m_tiles;  // tiles: of weights' rows x m_tiles of tokens, the tokens' running first
     UnitSplit split;
     uint32_t idesc;
     const uint16_t *bias;
@@ -43,12 +43,15 @@ struct StreamConfig {
     static constexpr uint32_t A_BYTES = kStreamRows * kStreamK * 2;
     static constexpr uint32_t B_BYTES = NT * kStreamK * 2;
     static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int GROUPS = epilogue_groups(NT);
+    // Four epilogue warps per 16 columns: their round trips to memory (pieces, outputs) overlap.
+    static constexpr int GROUPS = NT / 16;
     static constexpr int THREADS = 128 + 128 * GROUPS;
-    // About 100 KiB of ring: enough in flight for the memory's full rate, and two CTAs fit on an SM,
-    // so that the stream's next such kernel is resident, and its first weights on their way to L2,
-    // while this one finishes.
-    static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 4;
+    // Up to 32 tokens about 100 KiB of ring: enough in flight for the memory's full rate, and two CTAs
+    // fit on an SM, so that the stream's next such kernel is resident, and its first weights on
+    // their way to L2, while this one finishes (one token 4096 -> 14336: 26.2 -> 24.4 us).
+    static constexpr bool TOKEN_TILES = NT == 64;  // fewer tokens are one tile
+    static constexpr int CTAS = NT <= 32 ? 2 : 1;
+    static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 8;
     static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
     static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
 };
@@ -80,7 +83,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
 }
 
 template <int NT, bool W_MN, typename T>
-__global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
+__global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::CTAS)
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const StreamParams p) {
     using C = StreamConfig<NT>;
@@ -117,22 +120,14 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
     const uint32_t tmem = *tmem_slot;
     // The weights of the first stages go to L2 while the kernels before this one finish. (They are
     // read only after those have: L2 sees any write in between.)
-    auto load_weights = [&](uint8_t *dst, uint64_t *bar, int tile, int kb) {
-        if (W_MN) {
-            tma_load_2d(dst, &map_w, bar, tile * kStreamRows, kb * kStreamK);
-            tma_load_2d(dst + 8192, &map_w, bar, tile * kStreamRows + 64, kb * kStreamK);
-        } else {
-            tma_load_2d(dst, &map_w, bar, kb * kStreamK, tile * kStreamRows);
-        }
-    };
     if (threadIdx.x == 0) {
         for (int u = u0; u < min(u1, u0 + STAGES); ++u) {
-            const int tile = u / p.KB, kb = u - tile * p.KB;
+            const int tile = u / p.KB, kb = u - tile * p.KB, n0 = tile / p.m_tiles * kStreamRows;
             if (W_MN) {
-                tma_prefetch_2d(&map_w, tile * kStreamRows, kb * kStreamK);
-                tma_prefetch_2d(&map_w, tile * kStreamRows + 64, kb * kStreamK);
+                tma_prefetch_2d(&map_w, n0, kb * kStreamK);
+                tma_prefetch_2d(&map_w, n0 + 64, kb * kStreamK);
             } else {
-                tma_prefetch_2d(&map_w, kb * kStreamK, tile * kStreamRows);
+                tma_prefetch_2d(&map_w, kb * kStreamK, n0);
             }
         }
     }
@@ -142,19 +137,29 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
         if (lane == 0) {
             RingCursor<STAGES> ring;
             int issued = 0;
-            int tile = u0 / p.KB, kb = u0 - tile * p.KB;
+            const int tile0 = u0 / p.KB;
+            int kb = u0 - tile0 * p.KB, n0 = tile0 / p.m_tiles * kStreamRows, m0 = tile0 % p.m_tiles * NT;
             for (int u = u0; u < u1; ++u) {
                 if (issued >= STAGES && !mbar_wait(&empty[ring.stage], ring.parity ^ 1u)) break;
                 uint8_t *sw = smem + ring.stage * C::STAGE_BYTES, *sx = sw + C::A_BYTES;
                 uint64_t *bar = &full[ring.stage];
                 mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
-                load_weights(sw, bar, tile, kb);
-                tma_load_2d(sx, &map_x, bar, kb * kStreamK, 0);
+                if (W_MN) {
+                    tma_load_2d(sw, &map_w, bar, n0, kb * kStreamK);
+                    tma_load_2d(sw + 8192, &map_w, bar, n0 + 64, kb * kStreamK);
+                } else {
+                    tma_load_2d(sw, &map_w, bar, kb * kStreamK, n0);
+                }
+                tma_load_2d(sx, &map_x, bar, kb * kStreamK, m0);
                 ring.next();
                 ++issued;
                 if (++kb == p.KB) {
                     kb = 0;
-                    ++tile;
+                    m0 += NT;
+                    if (m0 >= p.M) {
+                        m0 = 0;
+                        n0 += kStreamRows;
+                    }
                 }
             }
             grid_dependents();  // every copy is on its way: the next kernel may start its prologue
@@ -201,7 +206,8 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
             const int n_units = min(p.KB - kb0, u1 - u);
             u += n_units;
-            const int n = tile * kStreamRows + row;
+            const int n = (C::TOKEN_TILES ? tile / p.m_tiles : tile) * kStreamRows + row;
+            const int m0 = C::TOKEN_TILES ? tile % p.m_tiles * NT : 0, tokens = min(NT, p.M - m0);
             const float b = p.bias && n < p.N ? Half16<T>::widen(p.bias[n]) : 0.0f;
             if (!mbar_wait(&acc_full[j & 1], (j >> 1) & 1)) break;
             tc_after_sync();
@@ -217,25 +223,25 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, 2)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&acc_free[j & 1]);
                 }
-                if (c >= p.M) continue;
+                if (c >= tokens) continue;
                 if (whole) {
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T>(p, n, c, b, v);
+                    finish16<T>(p, n, m0 + c, b, v);
                 } else {
-                    put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, p.M, r);
+                    put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, tokens, r);
                 }
             }
-            if (whole || first_col >= p.M ||
+            if (whole || first_col >= tokens ||
                 !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.KB, lane))
                 continue;
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
 #pragma unroll 1
-            for (int c = first_col; c < min(p.M, first_col + COLS); c += 16) {
+            for (int c = first_col; c < min(tokens, first_col + COLS); c += 16) {
                 float v[16];
-                sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, p.M, v);
-                finish16<T>(p, n, c, b, v);
+                sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, tokens, v);
+                finish16<T>(p, n, m0 + c, b, v);
             }
         }
     }
@@ -275,7 +281,8 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     StreamParams p;
     p.M = g.M;
     p.N = g.N;
-    p.tiles = static_cast<int>((g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows);
+    p.m_tiles = (g.M + NT - 1) / NT;
+    p.tiles = static_cast<int>((g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows) * p.m_tiles;
     p.KB = static_cast<int>((g.K + static_cast<long long>(kStreamK) - 1) / kStreamK);
     p.split.total = p.tiles * p.KB;
     p.split.ctas = std::min(sms[dev], std::max({1, p.split.total / min_run(NT), std::min(p.tiles, sms[dev])}));
@@ -320,10 +327,15 @@ cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **deta
 
 }  // namespace
 
+// Up to 64 rows always. With more, the tiles here are 128 x 64 and a block of one takes 0.38 us on
+// all SMs; the pair kernel's are 256 x 256 and take 0.30 us, one round of them up to 76. So this one
+// wins while its tiles are fewer than 128 (256 rows 1024 -> 1024: 9.3 us here, 12.3 there; 128 rows
+// 4096 -> 512: 12.5 and 26; 256 rows 4096 -> 4096, 128 tiles: 27.8 and 27.7; 512 rows: 45 and 28).
 bool stream_gemm16_supports(const Gemm16 &g) {
-    const long long tiles = (g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows;
+    const long long m_tiles = (g.M + 63LL) / 64;
+    const long long tiles = (g.N + static_cast<long long>(kStreamRows) - 1) / kStreamRows * m_tiles;
     const long long blocks = (g.K + static_cast<long long>(kStreamK) - 1) / kStreamK;
-    return !g.a_mn && g.M <= 64 && tiles <= static_cast<long long>(kCounterBytes / 32) &&
+    return !g.a_mn && (g.M <= 64 || tiles <= 128) && tiles <= static_cast<long long>(kCounterBytes / 64) &&
            tiles * blocks <= 0x7fffffffLL;
 }
 
