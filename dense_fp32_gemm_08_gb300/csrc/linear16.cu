@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(256) pack16_kernel(const PackJob j0, const Pac
     const int bid = static_cast<int>(blockIdx.x) - (second ? first : 0);
     const int bx = bid % j.gx, by = bid / j.gx;
     // Two rows at a time, so that twice the loads are under way.
-    for (int c = 8 * (bx * 256 + static_cast<int>(threadIdx.x)); c < j.cols; c += 2048 * j.gx) {
-        const int count = min(8, j.cols - c);
-        for (int r = by; r < j.rows; r += 2 * j.gy) {
+    for (long long c = 8 * (bx * 256LL + threadIdx.x); c < j.cols; c += 2048LL * j.gx) {
+        const int count = static_cast<int>(min(8LL, j.cols - c));
+        for (long long r = by; r < j.rows; r += 2LL * j.gy) {
             const bool two = r + j.gy < j.rows;
             const uint16_t *s0 = j.src + r * j.ld + c, *s1 = s0 + j.gy * j.ld;
             uint32_t v0[5] = {}, v1[5] = {};

@@ -535,7 +535,7 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
                     for (int a = 0; a < ACCS; ++a) put_piece<NT>(p.up_pieces, slot + a, c, row, m.T, r[a]);
                 }
             }
-            if (whole || !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.kb_up, lane))
+            if (whole || !piece_arrived(p.counters + static_cast<size_t>(tile) * (4 * C::GROUPS) + warp - 4, n_units, p.kb_up, lane))
                 continue;
             const int c0 = up.owner(tile * p.kb_up), c1 = up.owner(tile * p.kb_up + p.kb_up - 1);
 #pragma unroll 1

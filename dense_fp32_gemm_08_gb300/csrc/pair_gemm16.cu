@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int KB = p.g[i].KB;
                 auto blocks = [&](auto a_layout, auto b_layout) {
                     constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
-                    for (int k0 = 0; k0 < KB * kBK; k0 += kBK, ++it) {
-                        const int s = it % kStages;
+                    for (int kb = 0; kb < KB; ++kb, ++it) {
+                        const int s = it % kStages, k0 = kb * kBK;
                         if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1)) {
                             ok = false;
                             break;

@@ -407,3 +407,46 @@ def test_moe_in_place_residual_streams_and_graph(sgemm_lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want)
+
+
+# ---- offsets past 32 bits ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,pitch", [(12, 1 << 28), (300, 1 << 23)])
+def test_linear_offsets_past_32_bits(sgemm_lib, rows, pitch):
+    """x, residual, pre-activation and output as columns of one buffer whose last rows lie more than
+    2^31 values in."""
+    sg = sgemm_lib
+    K, N = 264, 328
+    assert rows * pitch > 1 << 31
+    buf = torch.empty(rows, pitch, dtype=torch.bfloat16, device="cuda")
+    x, r, out, dy, z = (buf[:, at:at + n] for at, n in ((0, K), (512, N), (1024, N), (1536, N), (2048, N)))
+    x.copy_(normal(1, rows, K))
+    r.copy_(normal(2, rows, N))
+    w = normal(3, N, K, scale=1 / 16)
+    sg.linear(x, w, act="silu", residual=r, out=out)
+    want, _, tol, _ = ref.linear_ref(x, w, None, "silu", r, "T")
+    assert ref.worst(out, want, tol) <= 1.0
+    dy.copy_(normal(4, rows, N))
+    z.copy_(normal(5, rows, N))
+    got = sg.linear_backward(dy, x, w, pre=z, act="gelu")
+    rx, rw, rb, xt, wt, bt = ref.backward_ref(dy, x, w, z, "gelu", "T")
+    assert max(ref.worst(got[0], rx, xt), ref.worst(got[1], rw, wt), ref.worst(got[2], rb, bt)) <= 1.0
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+
+
+@pytest.mark.parametrize("shift", [0, 1])
+def test_moe_expert_offsets_past_32_bits(sgemm_lib, shift):
+    sg = sgemm_lib
+    T, E, D, F, stride = 5, 4, 136, 72, (1 << 30) - 8 * 5
+    buf = torch.empty(E * stride, dtype=torch.bfloat16, device="cuda")
+    assert (E - 1) * stride > 1 << 31
+    up = buf[shift:].as_strided((E, F, D), (stride, D, 1))
+    gate = buf[1 << 20:].as_strided((E, F, D), (stride, D, 1), (1 << 20) + shift)
+    down = buf.as_strided((E, D, F), (stride, F, 1), (1 << 21) + shift)
+    for i, t in enumerate((up, gate, down)):
+        t.copy_(normal(10 + i, *t.shape, scale=0.1))
+    x, router = normal(1, T, D), normal(2, E, D, scale=0.2)
+    y, index, weight = sg.moe(x, router, gate, up, down, 2)
+    want, ri, rw, tol, wtol = ref.moe_ref(x, router, gate, up, down, 2, "silu", True, None, None)
+    assert torch.equal(index, ri) and ref.worst(y, want, tol) <= 1.0
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
