@@ -279,10 +279,11 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
         err = launch_early(zero_kernel, dim3(static_cast<unsigned>((g.N + 255LL) / 256)), 256, 0, stream, g.db,
                            g.N);
     } else {
-        // Rows per CTA: about 8 CTAs of 256 threads per SM and three rounds of them, in 8 to 256
-        // rows (few enough parts to add; 16384 x 14336: 64 parts of 256 rows).
+        // Rows per CTA, in eights: three rounds of CTAs at eight per SM, but at most 64 row blocks
+        // (the last CTA of a column block adds them one after another: 4095 x 3001 unaligned with 256
+        // blocks of 16 rows took 39 us) and at most 256 rows.
         const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
-        const long long want = std::max<long long>(1, 3 * 8 * 152 / blocks);
+        const long long want = std::min<long long>(64, std::max<long long>(1, 3 * 8 * 152 / blocks));
         long long rows = (g.M + want - 1) / want;
         rows = std::min<long long>(256, (rows + 7) / 8 * 8);
         rows = std::max(rows, (g.M + 65534LL) / 65535);
