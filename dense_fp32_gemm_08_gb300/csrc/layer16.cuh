@@ -121,6 +121,8 @@ enum LayerScratch : int {
     kScratchStream = 4,  // arrival counters and partial tiles of the weight-streaming product
     kScratchMoeSync = 5,  // its barriers and arrival counters
     kScratchSumSync = 6,  // arrival counters of the column sums
+    kScratchPair = 7,      // pieces of the pair product's cut tiles
+    kScratchPairSync = 8,  // their arrival counters
     kScratchUses
 };
 cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, void **out,

@@ -78,7 +78,8 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols) {
 // thread 8 columns (16 bytes) of every eighth row, four rows' loads in flight at once. Its 8 fp32
 // sums are added over the CTA's 8 threads of a column in a fixed order into part[row block][n], and
 // the CTA that completes a column block's last part (a count in memory; nothing waits) adds the
-// parts in ascending order, so that db does not depend on timing.
+// parts, four runs of them at once and then the runs' sums, in an order of their own, so that db
+// does not depend on timing.
 constexpr int kGradCols = 256;
 
 template <bool VEC, int W>
@@ -153,7 +154,7 @@ __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, lo
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int rows, float *part,
                                                        unsigned int *counters) {
-    __shared__ float sums[8][kGradCols];
+    __shared__ __align__(16) float sums[8][kGradCols];
     __shared__ unsigned int arrived;
     grid_dependents();
     grid_dependency();
@@ -180,7 +181,8 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int r
         if (n < g.N) g.db[n] = s;
         return;
     }
-    if (n < g.N) __stcg(part + static_cast<long long>(blockIdx.y) * g.N + n, s);
+    const long long ldp = static_cast<long long>(gridDim.x) * kGradCols;
+    __stcg(part + blockIdx.y * ldp + n, s);
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -189,12 +191,23 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int r
         if (arrived == static_cast<unsigned>(parts - 1)) counters[blockIdx.x] = 0;
     }
     __syncthreads();
-    if (arrived != static_cast<unsigned>(parts - 1) || n >= g.N) return;
+    if (arrived != static_cast<unsigned>(parts - 1)) return;
     __threadfence();
-    s = 0.0f;
+    // Thread (run, quad): columns 4 quad .. + 3 of every fourth part from `run` on.
+    const int run = threadIdx.x >> 6, quad = threadIdx.x & 63;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 16
-    for (int i = 0; i < parts; ++i) s += __ldcg(part + static_cast<long long>(i) * g.N + n);
-    g.db[n] = s;
+    for (int i = run; i < parts; i += 4) {
+        const float4 q = __ldcg(reinterpret_cast<const float4 *>(part + i * ldp + blockIdx.x * kGradCols) + quad);
+        a.x += q.x;
+        a.y += q.y;
+        a.z += q.z;
+        a.w += q.w;
+    }
+    *reinterpret_cast<float4 *>(&sums[run][4 * quad]) = a;
+    __syncthreads();
+    if (n < g.N)
+        g.db[n] = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
 }
 
 __global__ void zero_kernel(float *p, int n) {
@@ -279,13 +292,13 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
         err = launch_early(zero_kernel, dim3(static_cast<unsigned>((g.N + 255LL) / 256)), 256, 0, stream, g.db,
                            g.N);
     } else {
-        // Rows per CTA, in eights: three rounds of CTAs at eight per SM, but at most 64 row blocks
-        // (the last CTA of a column block adds them one after another: 4095 x 3001 unaligned with 256
-        // blocks of 16 rows took 39 us) and at most 256 rows.
+        // Rows per CTA, in eights: about four CTAs per SM, of 16 to 256 rows, in at most 256 row
+        // blocks for the last CTA of a column block to add. (2048 x 2048 in blocks of 8 rows: 19 us,
+        // of 32: 8 us.)
         const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
-        const long long want = std::min<long long>(64, std::max<long long>(1, 3 * 8 * 152 / blocks));
-        long long rows = (g.M + want - 1) / want;
-        rows = std::min<long long>(256, (rows + 7) / 8 * 8);
+        const long long want = std::min<long long>(256, std::max<long long>(1, 4 * 152 / blocks));
+        long long rows = ((g.M + want - 1) / want + 7) / 8 * 8;
+        rows = std::min<long long>(256, std::max<long long>(16, rows));
         rows = std::max(rows, (g.M + 65534LL) / 65535);
         const int parts = static_cast<int>((g.M + rows - 1) / rows);
         float *part = nullptr;
@@ -293,7 +306,7 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
         if (g.db && parts > 1) {
             void *p = nullptr, *q = nullptr;
             err = layer_scratch(kScratchSums, stream,
-                                static_cast<size_t>(parts) * static_cast<size_t>(g.N) * 4, &p, detail);
+                                static_cast<size_t>(parts) * static_cast<size_t>(blocks) * kGradCols * 4, &p, detail);
             if (err == cudaSuccess)
                 err = layer_scratch(kScratchSumSync, stream, static_cast<size_t>(blocks) * 4, &q, detail);
             if (err != cudaSuccess) return err;

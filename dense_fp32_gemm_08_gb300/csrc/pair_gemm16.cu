@@ -6,6 +6,9 @@
 //
 // A persistent grid of pairs walks the output tiles of one product, or of the two of a gradient
 // one after the other (the idle part of a last round is then paid once), in grouped-raster order.
+// A product with few tiles and a long k (a weight gradient over many rows) has its tiles cut along
+// k: the pieces go to scratch in fp32, and each epilogue warp that finds its 32 x 64 values complete
+// (a count in memory; nothing waits) sums them in the order of k.
 // Roles of a CTA's 20 warps:
 //   warp 0, lane 0: TMA producer: this CTA's 128 rows of A and 128 columns of B per 64-wide
 //                   k-block into a ring of 5 stages; both CTAs' copies complete on the leader's
@@ -14,13 +17,13 @@
 //                   TMEM accumulators of 256 columns; commits free the stage in both CTAs and,
 //                   at a tile's end, hand the accumulator to both CTAs' epilogues.
 //   warp 2:         allocates and frees the pair's TMEM.
-//   warps 4..19:    epilogue of this CTA's 128 rows while the next tile multiplies: warp w reads
-//                   TMEM lanes 32 (w % 4) .. + 31 and 64 of the columns, 32 at a time; bias,
+//   warps 4..19:    epilogue of this CTA's 128 rows while the next tile multiplies: warp w has TMEM
+//                   lanes 32 (w % 4) .. + 31 and 64 of the columns, 32 at a time; bias,
 //                   pre-activation, activation and residual in fp32, one rounding, through shared
 //                   memory to TMA stores (or, for outputs TMA cannot address, to stores of 64
-//                   consecutive bytes per row). Four warps per scheduler hide one another's waits:
-//                   with two, a tile's epilogue took 11 us against 20 us of MMAs at K = 4096 (bias,
-//                   GELU, residual and pre-activation; 256 x 256).
+//                   consecutive bytes per row). Four warps per scheduler
+//                   hide one another's waits: with two, a tile's epilogue took 11 us against 20 us
+//                   of MMAs at K = 4096 (bias, GELU, residual and pre-activation).
 // Either operand may be stored with k or with its other dimension contiguous: TMA boxes and the
 // MMA descriptors differ, the arithmetic does not, so the three products of a linear layer and
 // its gradient need no transposed copies.
@@ -31,7 +34,7 @@
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
 #include "raster.cuh"
-#include "tc16.cuh"
+#include "stream16.cuh"
 
 #include <algorithm>
 #include <mutex>
@@ -54,7 +57,8 @@ static_assert(kSmem <= 227 * 1024, "ring and store buffers fit in shared memory"
 
 struct PairProduct {
     int M, N, KB;  // KB: k-blocks
-    int tiles_m, tiles_n, tiles;
+    int tiles_m, tiles_n, split, items;  // items: tiles x split pieces along k
+    int piece0, tile0;                   // first piece and first counted tile in scratch (split > 1)
     int a_mn, b_mn;
     uint32_t idesc;
     uint16_t *D;
@@ -63,7 +67,9 @@ struct PairProduct {
 };
 struct PairParams {
     PairProduct g[kMaxProducts];
-    int total_tiles;
+    int total_items;
+    float *pieces;           // [pieces][2 CTAs][256 columns][128 rows]
+    unsigned int *counters;  // [tiles][2 CTAs][epilogue warps], zero between calls
     // The epilogue's matrices, of a launch with one product.
     const uint16_t *bias;
     int act;
@@ -79,12 +85,20 @@ struct PairMaps {
 };
 constexpr int kGroupM = 8;  // tile rows of the raster's groups
 
-// Tile t of the launch: its product and place.
-__device__ __forceinline__ int locate(const PairParams &p, int t, int &tm, int &tn) {
-    const int i = t >= p.g[0].tiles ? 1 : 0;
-    tile_coords(i ? t - p.g[0].tiles : t, p.g[i].tiles_m, p.g[i].tiles_n, kGroupM, tm, tn);
-    return i;
-}
+// Item t of the launch: its product, tile and k-blocks [kb0, kb0 + n).
+struct Item {
+    int product, tile, piece, tm, tn, kb0, n;
+    __device__ __forceinline__ Item(const PairParams &p, int t) {
+        product = t >= p.g[0].items ? 1 : 0;
+        const PairProduct &g = p.g[product];
+        if (product) t -= p.g[0].items;
+        tile = t / g.split;
+        piece = t - tile * g.split;
+        tile_coords(tile, g.tiles_m, g.tiles_n, kGroupM, tm, tn);
+        kb0 = static_cast<int>(static_cast<long long>(piece) * g.KB / g.split);
+        n = static_cast<int>((piece + 1LL) * g.KB / g.split) - kb0;
+    }
+};
 
 // Calls body with the operands' layouts as compile-time constants.
 template <typename Body>
@@ -275,16 +289,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0) {
             int it = 0;
             bool ok = true;
-            for (int t = pair; t < p.total_tiles && ok; t += pairs) {
-                int tm, tn;
-                const int i = locate(p, t, tm, tn);
-                const CUtensorMap *ma = &maps.a[i], *mb = &maps.b[i];
-                const int m0 = tm * 256 + static_cast<int>(rank) * kBM;
-                const int n0 = tn * kBN + static_cast<int>(rank) * (kBN / 2);
-                const int KB = p.g[i].KB;
+            for (int t = pair; t < p.total_items && ok; t += pairs) {
+                const Item item(p, t);
+                const CUtensorMap *ma = &maps.a[item.product], *mb = &maps.b[item.product];
+                const int m0 = item.tm * 256 + static_cast<int>(rank) * kBM;
+                const int n0 = item.tn * kBN + static_cast<int>(rank) * (kBN / 2);
                 auto blocks = [&](auto a_layout, auto b_layout) {
                     constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
-                    for (int kb = 0; kb < KB; ++kb, ++it) {
+                    for (int kb = item.kb0; kb < item.kb0 + item.n; ++kb, ++it) {
                         const int s = it % kStages, k0 = kb * kBK;
                         if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1)) {
                             ok = false;
@@ -307,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
                 };
-                with_layout(p.g[i], blocks);
+                with_layout(p.g[item.product], blocks);
             }
             // Shared memory must outlive every copy: the leader waits (bounded) for the last
             // stages of both CTAs; the final cluster barrier holds the other CTA until then.
@@ -319,13 +331,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0 && rank == 0) {
             int it = 0, j = 0;
             bool ok = true;
-            for (int t = pair; t < p.total_tiles && ok; t += pairs, ++j) {
-                const int i = t >= p.g[0].tiles ? 1 : 0;
+            for (int t = pair; t < p.total_items && ok; t += pairs, ++j) {
+                const Item item(p, t);
+                const int i = item.product;
                 const int set = j & 1;
                 if (j >= 2 && !mbar_wait_cluster(&acc_free[set], ((j >> 1) - 1) & 1)) break;
                 tc_after_sync();
                 const uint32_t d = tmem + static_cast<uint32_t>(set * kBN);
-                const int KB = p.g[i].KB;
+                const int KB = item.n;
                 const uint32_t idesc = p.g[i].idesc;
                 auto blocks = [&](auto a_layout, auto b_layout) {
                     constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
@@ -356,54 +369,102 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         uint8_t *bufs = store_bufs + w * 2 * kStoreBytes;
         const uint32_t free0 = map_to_rank(&acc_free[0], 0), free1 = map_to_rank(&acc_free[1], 0);
-        const int cfirst = group * 64, cend = cfirst + 64;
+        const int c0 = group * 64;
         int j = 0, nbuf = 0;
         uint32_t raw[20];  // the next block's residual
-        float bias = 0.0f;  // and bias, of column col0 + lane
-        auto fetch = [&](int row0, int col0) {
-            if (p.res) fetch_residual(raw, p, row0, col0, lane);
-            if (p.bias) bias = col0 + lane < p.g[0].N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
-        };
-        for (int t = pair; t < p.total_tiles; t += pairs, ++j) {
+        float bias[2] = {0.0f, 0.0f};  // of columns col0 + lane and col0 + 32 + lane
+        for (int t = pair; t < p.total_items; t += pairs, ++j) {
             const int set = j & 1;
-            int tm, tn;
-            const int i = locate(p, t, tm, tn);
-            const PairProduct g = p.g[i];
-            const int row0 = tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
-            if (row0 < g.M && tn * kBN + cfirst < g.N) fetch(row0, tn * kBN + cfirst);
+            const Item item(p, t);
+            const PairProduct g = p.g[item.product];
+            const int row0 = item.tm * 256 + static_cast<int>(rank) * kBM + quarter * 32;
+            const int col0 = item.tn * kBN + c0;
+            const bool inside = row0 < g.M && col0 < g.N;
+            const int blocks = g.N - col0 > 32 ? 2 : 1;
+            if (inside && g.split == 1) {
+                if (p.res) fetch_residual(raw, p, row0, col0, lane);
+                if (p.bias) {
+                    bias[0] = col0 + lane < g.N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
+                    bias[1] = g.N - col0 - 32 > lane ? Half16<T>::widen(p.bias[col0 + 32 + lane]) : 0.0f;
+                }
+            }
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
             tc_after_sync();
-            const uint32_t tset = tmem + lane_base + static_cast<uint32_t>(set * kBN);
+            const uint32_t tset = tmem + lane_base + static_cast<uint32_t>(set * kBN + c0);
+            auto release = [&]() {  // the warp's last read of this accumulator
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_at(set ? free1 : free0);
+            };
+            if (!inside) {
+                release();
+                continue;
+            }
+            const float *pieces = nullptr;  // of this lane's row, the tile's first one
+            constexpr size_t kPiece = 2ull * kBN * kBM;
+            if (g.split > 1) {
+                const size_t at = static_cast<size_t>(g.piece0 + item.tile * g.split);
+                float *base = p.pieces + (2 * at + rank) * kBN * kBM + c0 * kBM + quarter * 32 + lane;
 #pragma unroll 1
-            for (int c0 = cfirst; c0 < cend; c0 += 32) {
-                float v[32];
-                tmem_ld_x32(tset + static_cast<uint32_t>(c0), reinterpret_cast<uint32_t(&)[32]>(v));
-                tmem_ld_wait();
-                if (c0 + 32 == cend) {  // the warp's last read of this accumulator
-                    tc_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_at(set ? free1 : free0);
-                }
-                const int col0 = tn * kBN + c0;
-                if (row0 >= g.M || col0 >= g.N) continue;
-                if (p.bias) {
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t r[32];
+                    tmem_ld_x32(tset + static_cast<uint32_t>(32 * b), r);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) v[k] += __shfl_sync(0xFFFFFFFFu, bias, k);
+                    for (int i = 0; i < 32; ++i)
+                        __stcg(base + item.piece * kPiece + (32 * b + i) * kBM, __uint_as_float(r[i]));
+                }
+                release();
+                unsigned int *counter =
+                    p.counters + (2 * static_cast<size_t>(g.tile0 + item.tile) + rank) * kEpiWarps + w;
+                if (!piece_arrived(counter, 1, g.split, lane)) continue;
+                pieces = base;
+                if (p.res) fetch_residual(raw, p, row0, col0, lane);
+                if (p.bias) {
+                    bias[0] = col0 + lane < g.N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
+                    bias[1] = g.N - col0 - 32 > lane ? Half16<T>::widen(p.bias[col0 + 32 + lane]) : 0.0f;
+                }
+            }
+            // The product's 32 columns of block b: the accumulator, or the pieces in the order of k.
+            auto values = [&](int b, float(&v)[32]) {
+                if (pieces) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+                    for (int k = 0; k < g.split; ++k)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] += __ldcg(pieces + k * kPiece + (32 * b + i) * kBM);
+                } else {
+                    tmem_ld_x32(tset + static_cast<uint32_t>(32 * b), reinterpret_cast<uint32_t(&)[32]>(v));
+                    tmem_ld_wait();
+                }
+            };
+#pragma unroll 1
+            for (int b = 0; b < blocks; ++b) {
+                const int col = col0 + 32 * b;
+                float v[32];
+                values(b, v);
+                if (b == blocks - 1 && !pieces) release();
+                if (p.bias) {
+                    const float mine = b ? bias[1] : bias[0];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
                 }
                 if (p.pre) {
                     if (lane == 0) bulk_wait_read<1>();
                     __syncwarp();
                     store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.z, p.z_tma, p.pre, p.ldz, g.M, g.N,
-                                   row0, col0, lane);
+                                   row0, col, lane);
                     nbuf ^= 1;
                 }
                 activate32(v, p.act);
                 if (lane == 0) bulk_wait_read<1>();
                 __syncwarp();
-                if (p.res) add_residual<T>(v, raw, bufs + nbuf * kStoreBytes, p, row0, col0, lane);
-                if (c0 + 32 < cend && col0 + 32 < g.N) fetch(row0, col0 + 32);
-                store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.d[i], g.d_tma, g.D, g.ldd, g.M, g.N, row0,
-                               col0, lane);
+                if (p.res) {
+                    add_residual<T>(v, raw, bufs + nbuf * kStoreBytes, p, row0, col, lane);
+                    if (b + 1 < blocks) fetch_residual(raw, p, row0, col + 32, lane);
+                }
+                store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.d[item.product], g.d_tma, g.D, g.ldd, g.M, g.N,
+                               row0, col, lane);
                 nbuf ^= 1;
             }
         }
@@ -469,7 +530,7 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
     PairMaps maps;
     // Tiles with the longer k first: the shorter ones fill the last round.
     const int order[2] = {n == 2 && list[1].K > list[0].K ? 1 : 0, n == 2 && list[1].K > list[0].K ? 0 : 1};
-    long long total = 0;
+    long long work = 0;  // k-blocks of all tiles
     for (int i = 0; i < n; ++i) {
         const Gemm16 &g = list[order[i]];
         PairProduct &q = p.g[i];
@@ -479,12 +540,13 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
         q.tiles_m = static_cast<int>((g.M + 255LL) / 256);
         q.tiles_n = static_cast<int>((g.N + static_cast<long long>(kBN) - 1) / kBN);
         const long long tiles = static_cast<long long>(q.tiles_m) * q.tiles_n;
-        total += tiles;
-        if (total > 0x3fffffffLL) {
+        if (tiles > 0x3fffffffLL) {
             *detail = "too many output tiles";
             return cudaErrorInvalidValue;
         }
-        q.tiles = static_cast<int>(tiles);
+        q.split = 1;
+        q.items = static_cast<int>(tiles);
+        work += tiles * q.KB;
         q.a_mn = g.a_mn;
         q.b_mn = g.b_mn;
         q.idesc = idesc_16(256, kBN, Half16<T>::kind, g.a_mn, g.b_mn);
@@ -502,7 +564,35 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
             return cudaErrorInvalidValue;
         }
     }
-    p.total_tiles = static_cast<int>(total);
+    // A tile whose k-blocks (0.3 us each) exceed an even share of the work is cut into pieces of about
+    // that share, 16 blocks at least (gradients of 6338 rows 80 -> 288, two tiles of 100 blocks
+    // for dW: 47 us whole, 31 us cut).
+    size_t pieces = 0, cut_tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        PairProduct &q = p.g[i];
+        const long long share = std::max<long long>(16, (work + max_pairs - 1) / max_pairs);
+        const int tiles = q.items;
+        int most = 1;  // summing s pieces takes about 2 s us: no more than minimise 0.3 KB / s + 2 s
+        while (most < 8 && 20 * (most + 1) * (most + 1) <= 3 * q.KB) ++most;
+        q.split = static_cast<int>(std::min<long long>(most, (q.KB + share - 1) / share));
+        if (q.split > 1) {
+            q.items = tiles * q.split;  // fewer than 2 max_pairs: tiles x KB <= work < KB x max_pairs
+            q.piece0 = static_cast<int>(pieces);
+            q.tile0 = static_cast<int>(cut_tiles);
+            pieces += static_cast<size_t>(q.items);
+            cut_tiles += static_cast<size_t>(tiles);
+        }
+        p.total_items += q.items;
+    }
+    if (pieces > 0) {
+        void *data = nullptr, *sync = nullptr;
+        err = layer_scratch(kScratchPair, stream, pieces * 2 * kBN * kBM * 4, &data, detail);
+        if (err == cudaSuccess)
+            err = layer_scratch(kScratchPairSync, stream, cut_tiles * 2 * kEpiWarps * 4, &sync, detail);
+        if (err != cudaSuccess) return err;
+        p.pieces = static_cast<float *>(data);
+        p.counters = static_cast<unsigned int *>(sync);
+    }
     if (n == 1) {
         const Gemm16 &g = list[0];
         p.bias = g.bias;
@@ -518,7 +608,7 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
             return cudaErrorInvalidValue;
         }
     }
-    const int pairs = std::min(p.total_tiles, max_pairs);
+    const int pairs = std::min(p.total_items, max_pairs);
     err = launch_early(pair_gemm16_kernel<T>, dim3(2u * static_cast<unsigned>(pairs)), kThreads, kSmem,
                        stream, maps, p);
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
