@@ -31,7 +31,8 @@ __global__ void __launch_bounds__(256) no_product_kernel(const Gemm16 g) {
 //
 // A matrix whose base or leading dimension is not a multiple of 16 bytes is copied once into
 // scratch with an aligned leading dimension, at memory speed, and the product runs on the copy.
-// A thread writes 8 values from the aligned 4-byte words around them.
+// A thread writes 8 values from the aligned 4-byte words around them (X and W of 4095 x 3001 x 1537:
+// 8.8 to 10.4 us for 44 MB read and written).
 struct PackJob {
     const uint16_t *src;
     long long ld;
@@ -74,7 +75,8 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols) {
 
 // ---- dz = dy * act'(z) and its column sums --------------------------------------------------
 //
-// Bound by memory (two matrices read, one written). A CTA covers 256 columns and `rows` rows: a
+// Bound by memory (two matrices read, one written; 16384 x 14336 bf16 with GELU: 235 us, 6.0 TB/s;
+// 4095 x 3001 f16 in unaligned rows: 27 us, 2.7 TB/s). A CTA covers 256 columns and `rows` rows: a
 // thread 8 columns (16 bytes) of every eighth row, four rows' loads in flight at once. Its 8 fp32
 // sums are added over the CTA's 8 threads of a column in a fixed order into part[row block][n], and
 // the CTA that completes a column block's last part (a count in memory; nothing waits) adds the
@@ -293,8 +295,8 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
                            g.N);
     } else {
         // Rows per CTA, in eights: about four CTAs per SM, of 16 to 256 rows, in at most 256 row
-        // blocks for the last CTA of a column block to add. (2048 x 2048 in blocks of 8 rows: 19 us,
-        // of 32: 8 us.)
+        // blocks for the last CTA of a column block to add (all gradients at 2048 x 2048 x 2048: 52 us with
+        // blocks of 8 rows, 40 us with 32).
         const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
         const long long want = std::min<long long>(256, std::max<long long>(1, 4 * 152 / blocks));
         long long rows = ((g.M + want - 1) / want + 7) / 8 * 8;

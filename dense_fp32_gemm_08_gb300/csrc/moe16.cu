@@ -4,6 +4,9 @@
 //   w_j = p_chosen(j), divided by their sum when `renormalize`
 //   h_j = act(G_e x) * (U_e x)   or, without a gate, act(U_e x)
 //   y   = sum_j w_j D_e h_j + residual
+//
+// The fused kernel (moe_stream16.cu) takes layers whose matrices TMA can address; this file has the
+// choice and the kernels for the others.
 #include "epilogue.cuh"
 #include "half16.cuh"
 #include "moe16.cuh"
@@ -77,7 +80,10 @@ __global__ void __launch_bounds__(256) moe_router_kernel(const Moe16 m, int *ind
 // The products by fp32 FMAs: the rows are read as the aligned 4-byte words around them, 128 bytes
 // per warp and instruction and several rows at once, against values of x (or h) in shared memory.
 // Each (token, choice) reads its expert's weights; the choices of one expert run at the same time,
-// so that memory sees them about once.
+// so that memory sees them about once. 7 tokens, 4 experts of 1537 x 3001 bf16: 52 us (router 7, up 23,
+// down 23) for 64 MB. (Loaders that bring such rows into the fused kernel's swizzled stages, through
+// registers or cp.async, took 72 to 102 us: putting unaligned rows together costs more
+// instructions than the two products here.)
 constexpr int kSpan = 4096;  // values of x or h in shared memory at a time
 
 // sum[r] += w_r[0 .. count) . x over this lane's words, ROWS rows at once.

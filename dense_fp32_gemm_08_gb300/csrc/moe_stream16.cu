@@ -3,7 +3,8 @@
 // The layer is bound by reading the chosen experts' weights once: 2 bytes per weight against
 // 2 x (tokens of that expert) operations. One cooperative grid, one CTA per SM, runs four steps
 // with a grid barrier between them, so that nothing but the weights moves far:
-//   1. scores s = X . Wr^T, an expert per CTA in turn, fp32 FMAs;
+//   1. scores s = X . Wr^T, an expert and 8 tokens per CTA in turn, fp32 FMAs (every CTA for itself,
+//      without the barrier, for up to 8 scores);
 //   2. routing, computed by every CTA for itself (a few hundred values): softmax statistics in
 //      fp32, the k largest scores with ties to the lowest index, and the list of chosen experts
 //      with their tokens as 64-bit masks;
@@ -13,6 +14,12 @@
 //      its token's experts in the order of their rank, adds the residual and is rounded once.
 // The ring runs across the barrier between 3 and 4: the weights of step 4 do not depend on h, so
 // the first stages are under way before h is complete.
+//
+// Measured, one token through 2 of 8 experts of 4096 x 14336 bf16 (704 MB of weights): 131 us, 5.4
+// TB/s: scores and routing 4.4, step 3 77 (6.1 TB/s), its barrier 6, step 4 38 (6.2 TB/s), its barrier
+// 2.8, the sum 1. 24 tokens through 64 experts of 2048 x 1024 f16 (774 MB): 163 us, 4.7 TB/s; DRAM reads
+// 777 MB. The memory's rate bounds the steps, the slowest CTA's pieces the barriers. (Sending the next
+// weights to L2 during the barrier or the routing, 10 to 64 blocks per CTA, made it 1 to 5% slower.)
 //
 // h is rounded to the call's 16-bit type, as the tensor cores need it and as a layer computed in
 // separate products would hold it; every sum is in fp32, cut tiles are summed in the order of k.

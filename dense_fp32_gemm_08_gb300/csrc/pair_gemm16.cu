@@ -28,6 +28,12 @@
 // MMA descriptors differ, the arithmetic does not, so the three products of a linear layer and
 // its gradient need no transposed copies.
 //
+// Measured: 16384 x 14336 x 4096 bf16 with bias, GELU and kept pre-activation 1.10 ms (1,745 TFLOP/s;
+// 1.24 ms when run without a pause, at the clocks that the power limit then leaves), its two gradient
+// products 2.15 ms (1,790 TFLOP/s): bound by the tensor cores. 512 x 12288 x 4096: 49 us, two rounds of
+// tiles for 1.26 (tensor pipe busy 66%). 4095 x 3001 x 1537 f16 with every epilogue part in unaligned
+// rows: 55 us, bound by the epilogue's 2-byte stores.
+//
 // Every wait is bounded (ptx.cuh); a wait that expires ends the role, and the CTAs still meet at
 // the final cluster barrier and free their TMEM.
 #include "activation16.cuh"

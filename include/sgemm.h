@@ -266,7 +266,10 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * widened exactly when read. Every sum, softmax statistic and activation is held in fp32 and
  * each output is rounded once, to nearest even. Conventions (streams, workspaces, errors,
  * thread safety) are those above; pointers need their type's own alignment only, and 16-byte
- * aligned matrices with leading dimensions that are multiples of 8 select the TMA path.
+ * aligned matrices with leading dimensions that are multiples of 8 select the TMA path. A stream's
+ * workspaces are allocated by its first call of a kind and size: make that call before capturing
+ * the stream into a graph. A call's kernels may start while the stream's earlier ones finish; they
+ * read and write memory only after those are complete.
  */
 typedef enum sgemm_dtype {
     SGEMM_DTYPE_BF16 = 0,
