@@ -11,8 +11,9 @@
 // (a count in memory; nothing waits) sums them in the order of k.
 // Roles of a CTA's 20 warps:
 //   warp 0, lane 0: TMA producer: this CTA's 128 rows of A and 128 columns of B per 64-wide
-//                   k-block into a ring of 5 stages; both CTAs' copies complete on the leader's
-//                   "full" barrier.
+//                   k-block into a ring of 6 stages (512 x 12288 x 4096 with 4, 5, 6: 55, 49.3 and
+//                   47.5 us, so the sixth has the room of a second store buffer per epilogue warp);
+//                   both CTAs' copies complete on the leader's "full" barrier.
 //   warp 1, lane 0: (leader CTA) issues the MMAs, four k-steps of 16 per block, into one of two
 //                   TMEM accumulators of 256 columns; commits free the stage in both CTAs and,
 //                   at a tile's end, hand the accumulator to both CTAs' epilogues.
@@ -56,9 +57,9 @@ constexpr int kEpiWarps = 16;  // 4 row quarters x 4 groups of 64 columns
 constexpr int kThreads = 128 + 32 * kEpiWarps;
 constexpr uint32_t kPartBytes = kBM * kBK * 2;  // A's or B's share of a stage
 constexpr uint32_t kStageBytes = 2 * kPartBytes;
-constexpr int kStages = 5;
+constexpr int kStages = 6;
 constexpr uint32_t kStoreBytes = 2048;  // 32 rows x 32 values
-constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * 2 * kStoreBytes + (2 * kStages + 4) * 8 + 16 + 1024;
+constexpr size_t kSmem = kStages * kStageBytes + kEpiWarps * kStoreBytes + (2 * kStages + 4) * 8 + 16 + 1024;
 static_assert(kSmem <= 227 * 1024, "ring and store buffers fit in shared memory");
 
 struct PairProduct {
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
     uint8_t *store_bufs = smem + kStages * kStageBytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(store_bufs + kEpiWarps * 2 * kStoreBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(store_bufs + kEpiWarps * kStoreBytes);
     uint64_t *empty = full + kStages;
     uint64_t *acc_full = empty + kStages;  // [2]
     uint64_t *acc_free = acc_full + 2;     // [2], the leader's are used
@@ -373,10 +374,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     } else if (warp >= 4) {
         const int w = warp - 4, quarter = warp & 3, group = w >> 2;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        uint8_t *bufs = store_bufs + w * 2 * kStoreBytes;
+        uint8_t *buf = store_bufs + w * kStoreBytes;
         const uint32_t free0 = map_to_rank(&acc_free[0], 0), free1 = map_to_rank(&acc_free[1], 0);
         const int c0 = group * 64;
-        int j = 0, nbuf = 0;
+        int j = 0;
         uint32_t raw[20];  // the next block's residual
         float bias[2] = {0.0f, 0.0f};  // of columns col0 + lane and col0 + 32 + lane
         for (int t = pair; t < p.total_items; t += pairs, ++j) {
@@ -456,22 +457,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
                 }
                 if (p.pre) {
-                    if (lane == 0) bulk_wait_read<1>();
+                    if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
-                    store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.z, p.z_tma, p.pre, p.ldz, g.M, g.N,
-                                   row0, col, lane);
-                    nbuf ^= 1;
+                    store_block<T>(v, buf, &maps.z, p.z_tma, p.pre, p.ldz, g.M, g.N, row0, col, lane);
                 }
                 activate32(v, p.act);
-                if (lane == 0) bulk_wait_read<1>();
+                if (lane == 0) bulk_wait_read<0>();
                 __syncwarp();
                 if (p.res) {
-                    add_residual<T>(v, raw, bufs + nbuf * kStoreBytes, p, row0, col, lane);
+                    add_residual<T>(v, raw, buf, p, row0, col, lane);
                     if (b + 1 < blocks) fetch_residual(raw, p, row0, col + 32, lane);
                 }
-                store_block<T>(v, bufs + nbuf * kStoreBytes, &maps.d[item.product], g.d_tma, g.D, g.ldd, g.M, g.N,
-                               row0, col, lane);
-                nbuf ^= 1;
+                store_block<T>(v, buf, &maps.d[item.product], g.d_tma, g.D, g.ldd, g.M, g.N, row0, col, lane);
             }
         }
         if (lane == 0) bulk_wait_read<0>();
