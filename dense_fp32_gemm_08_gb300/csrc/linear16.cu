@@ -75,8 +75,8 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols) {
 
 // ---- dz = dy * act'(z) and its column sums --------------------------------------------------
 //
-// Bound by memory (two matrices read, one written; 16384 x 14336 bf16 with GELU: 235 us, 6.0 TB/s;
-// 4095 x 3001 f16 in unaligned rows: 27 us, 2.7 TB/s). A CTA covers 256 columns and `rows` rows: a
+// Bound by memory (two matrices read, one written; db alone, so that none is written: 16384 x 14336
+// bf16 with GELU 191 us, 4.9 TB/s; 4095 x 3001 f16 in unaligned rows 19.4 us, 2.5 TB/s). A CTA covers 256 columns and `rows` rows: a
 // thread 8 columns (16 bytes) of every eighth row, four rows' loads in flight at once. Its 8 fp32
 // sums are added over the CTA's 8 threads of a column in a fixed order into part[row block][n], and
 // the CTA that completes a column block's last part (a count in memory; nothing waits) adds the
@@ -275,7 +275,8 @@ cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const 
         }
     }
     // Products that stream weights for a few rows go alone; the others share one launch (and a
-    // gradient's two always do when there are more rows: apart, they took longer).
+    // gradient's two always do when there are more rows: 256 rows 1024 -> 1024 15.4 us, apart 22.5;
+    // 4095 x 3001 x 1537 f16 108 us, apart 130).
     int together = 0;
     for (int i = 0; i < products; ++i) {
         if (stream_gemm16_supports(q[i]) && (n == 1 || q[i].M <= 64)) {
@@ -294,13 +295,17 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
         err = launch_early(zero_kernel, dim3(static_cast<unsigned>((g.N + 255LL) / 256)), 256, 0, stream, g.db,
                            g.N);
     } else {
-        // Rows per CTA, in eights: about four CTAs per SM, of 16 to 256 rows, in at most 256 row
-        // blocks for the last CTA of a column block to add (all gradients at 2048 x 2048 x 2048: 52 us with
-        // blocks of 8 rows, 40 us with 32).
+        const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) && (g.act == kActNone || tma_rows(g.z, g.ldz));
+        // Rows per CTA, in whole steps: about whole rounds of the 3 x 152 CTAs that run at once, with 256
+        // rows or so at most (a short last round) and a step at least (the last CTA of a column
+        // block adds the sums of all of them). db alone, 2048 x 2048: 18.0 us with 8 rows, 9.5 with 32;
+        // 4095 x 3001 unaligned: 49 us with 8 rows, 24.8 with 88 (1.2 rounds), 19.2 with 112 (one).
+        const long long step = vec ? 32 : 16;  // rows that a CTA has under way at once
         const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
-        const long long want = std::min<long long>(256, std::max<long long>(1, 4 * 152 / blocks));
-        long long rows = ((g.M + want - 1) / want + 7) / 8 * 8;
-        rows = std::min<long long>(256, std::max<long long>(16, rows));
+        const long long resident = 3 * 152;
+        const long long rounds = g.M / std::max<long long>(1, resident / blocks) / 256 + 1;
+        const long long want = std::max<long long>(1, rounds * resident / blocks);
+        long long rows = std::max(step, (g.M / want + step / 2) / step * step);
         rows = std::max(rows, (g.M + 65534LL) / 65535);
         const int parts = static_cast<int>((g.M + rows - 1) / rows);
         float *part = nullptr;
@@ -316,7 +321,6 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
             counters = static_cast<unsigned int *>(q);
         }
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
-        const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) && (g.act == kActNone || tma_rows(g.z, g.ldz));
         auto kernel = g.dtype == kBf16
                           ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
                           : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);

@@ -1,8 +1,9 @@
 // pair_gemm16.cu: D = act(A . B + bias) + res on 16-bit values with tcgen05 MMAs over pairs of
 // CTAs (cta_group::2): one MMA multiplies 256 rows by 256 columns, each CTA of the pair holding
 // half of A's rows and half of B's columns in its own shared memory, so each SM stages half the
-// operand bytes per multiply-add of a one-CTA tile. (Narrower tiles, 128 and 192 columns, took as
-// long per k-block as 256, 0.29 us: the operands' way from L2 bounds them.)
+// operand bytes per multiply-add of a one-CTA tile. (Narrower tiles, 128 to 192 columns, took about as
+// long per k-block as 256, 0.30 us: a stage's way from L2 bounds them. 224 gained 1 to 3% where
+// the rounds of tiles stay the same and lost 7% on large products.)
 //
 // A persistent grid of pairs walks the output tiles of one product, or of the two of a gradient
 // one after the other (the idle part of a last round is then paid once), in grouped-raster order.
@@ -30,10 +31,10 @@
 // its gradient need no transposed copies.
 //
 // Measured: 16384 x 14336 x 4096 bf16 with bias, GELU and kept pre-activation 1.10 ms (1,745 TFLOP/s;
-// 1.24 ms when run without a pause, at the clocks that the power limit then leaves), its two gradient
-// products 2.15 ms (1,790 TFLOP/s): bound by the tensor cores. 512 x 12288 x 4096: 49 us, two rounds of
-// tiles for 1.26 (tensor pipe busy 66%). 4095 x 3001 x 1537 f16 with every epilogue part in unaligned
-// rows: 55 us, bound by the epilogue's 2-byte stores.
+// 1.27 ms when run without a pause, at the clocks that the power limit then leaves): bound by the
+// tensor cores. 512 x 12288 x 4096: 48.5 us, two rounds of tiles for 1.26 (tensor pipe busy 63%).
+// 4095 x 3001 x 1537 f16 with every epilogue part in unaligned rows: 56 us without the repacking, bound
+// by the epilogue's 2-byte stores. (Asking L2 for operands 6 to 12 k-blocks ahead: 4 to 25% longer.)
 //
 // Every wait is bounded (ptx.cuh); a wait that expires ends the role, and the CTAs still meet at
 // the final cluster barrier and free their TMEM.

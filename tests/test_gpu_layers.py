@@ -82,6 +82,12 @@ def test_linear_sizes(sgemm_lib, M, N, K, transw, dtype):
     run_linear(sgemm_lib, M, N, K, dtype, "gelu", transw, True, False, True, seed=5)
 
 
+@pytest.mark.parametrize("M,N,K", [(1400, 1500, 5000), (700, 2999, 9001), (2048, 1536, 20000), (300, 260, 30000)])
+@pytest.mark.parametrize("transw", ["T", "N"])
+def test_linear_long_k_with_few_tiles(sgemm_lib, M, N, K, transw):
+    run_linear(sgemm_lib, M, N, K, torch.bfloat16, "gelu", transw, True, True, True, seed=K)
+
+
 @pytest.mark.parametrize("M", [1, 6, 33, 100, 300])
 @pytest.mark.parametrize("N,K,pad,offset", [(301, 257, 0, 0), (304, 264, 3, 0), (304, 264, 8, 0), (304, 264, 8, 1),
                                             (304, 264, 0, 5), (303, 264, 1, 0), (304, 263, 1, 8)])
@@ -198,6 +204,12 @@ def test_backward_activations(sgemm_lib, dtype, act, transw):
 @pytest.mark.parametrize("transw", ["T", "N"])
 def test_backward_sizes(sgemm_lib, M, N, K, transw):
     run_backward(sgemm_lib, M, N, K, torch.bfloat16, "gelu", transw, seed=2)
+
+
+@pytest.mark.parametrize("M,N,K", [(6000, 80, 288), (9000, 303, 72), (200, 9000, 260), (4000, 2000, 700)])
+@pytest.mark.parametrize("transw", ["T", "N"])
+def test_backward_long_k_with_few_tiles(sgemm_lib, M, N, K, transw):
+    run_backward(sgemm_lib, M, N, K, torch.bfloat16, "silu", transw, seed=M)
 
 
 @pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1), (8, 3)])
