@@ -83,8 +83,8 @@ __device__ __forceinline__ bool piece_arrived(unsigned int *counter, int units, 
     return true;
 }
 // Runs of fewer units would cut a tile into more pieces than summing them in turn is worth (a
-// unit streams in about 0.1 us, a piece of 16 columns is summed in 0.2 us, of 64 in 0.8 us: 8 rows
-// 512 -> 512 5.0 us, with runs down to one unit 6.4; 13 rows 1537 -> 3001 14.5 and 15.1).
+// unit streams in about 0.1 us, a piece of 16 columns is summed in 0.2 us, of 64 in 0.8 us: equal runs
+// over 8 rows 512 -> 512 take 5.0 us so, 6.4 with runs down to one unit).
 __host__ __device__ constexpr int min_run(int nt) { return 8 + nt / 8; }
 
 // Position in the ring, kept by each role across tiles and phases.
