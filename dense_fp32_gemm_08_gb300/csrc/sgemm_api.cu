@@ -473,14 +473,17 @@ sgemm_status_t moe(const sg::Moe16 &m, int64_t T, int64_t E, int64_t topk, int64
     return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
 }
 
-// Runs `body`, turning a C++ exception (host memory exhausted) into a status. A call's launches
-// share the stream's scratch, so calls from several host threads queue theirs one call at a time.
+// The launches of one layer operator's call share the stream's scratch, and a larger call moves it:
+// calls from several host threads, of the same operator or not, queue theirs one call at a time.
+// Freeing or clearing the scratch takes the same lock.
+std::mutex g_layer_queueing;
+
+// Runs `body` under that lock, turning a C++ exception (host memory exhausted) into a status.
 template <typename Body>
 sgemm_status_t guarded(Body body) {
-    static std::mutex queueing;
     t_last_error[0] = '\0';
     try {
-        std::lock_guard<std::mutex> lock(queueing);
+        std::lock_guard<std::mutex> lock(g_layer_queueing);
         return body();
     } catch (...) {
         return fail(SGEMM_ERR_LAUNCH, "out of host memory");
@@ -733,6 +736,7 @@ sgemm_status_t sgemm_device_status(void *stream_ptr) {
     if (err != cudaSuccess) return fail_cuda("stream synchronize", err);
     const unsigned int word = sg::take_fault_words(stream);
     if (word & sg::kFaultTimeout) {
+        std::lock_guard<std::mutex> lock(g_layer_queueing);
         sg::layer_scratch_distrust();
         return fail(SGEMM_ERR_TIMEOUT, "a bounded wait inside a kernel expired");
     }
@@ -748,8 +752,13 @@ sgemm_status_t sgemm_release_workspace(void) {
     cudaError_t err3 = sg::release_pack_workspaces();
     cudaError_t err4 = sg::release_host_buffers();
     if (err3 == cudaSuccess) err3 = err4;
-    cudaError_t err5 = sg::release_layer_workspaces();
-    if (err3 == cudaSuccess) err3 = err5;
+    {
+        // A call that another thread has queued since the synchronisation above may use the buffers.
+        std::lock_guard<std::mutex> lock(g_layer_queueing);
+        cudaError_t err5 = cudaDeviceSynchronize();
+        if (err5 == cudaSuccess) err5 = sg::release_layer_workspaces();
+        if (err3 == cudaSuccess) err3 = err5;
+    }
     cudaError_t err2 = sg::tf32x3_release_workspaces();
     if (err == cudaSuccess) err = err3;
     if (err != cudaSuccess) return fail_cuda("workspace free", err);
