@@ -112,7 +112,7 @@ constexpr int kMoeMaxTopk = 16;
 cudaError_t moe16_launch(const Moe16 &m, cudaStream_t stream, const char **detail);
 
 // Per-(device, stream) scratch of the layer operators, one buffer per use. Grown when a call
-// needs more and kept until release_layer_workspaces().
+// needs more; buffers and the ones they outgrew are kept until release_layer_workspaces().
 enum LayerScratch : int {
     kScratchDz = 0,    // the gradient's dz
     kScratchSums = 1,  // partial column sums

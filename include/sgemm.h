@@ -266,10 +266,15 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * widened exactly when read. Every sum, softmax statistic and activation is held in fp32 and
  * each output is rounded once, to nearest even. Conventions (streams, workspaces, errors,
  * thread safety) are those above; pointers need their type's own alignment only, and 16-byte
- * aligned matrices with leading dimensions that are multiples of 8 select the TMA path. A stream's
- * workspaces are allocated by its first call of a kind and size: make that call before capturing
- * the stream into a graph. A call's kernels may start while the stream's earlier ones finish; they
- * read and write memory only after those are complete.
+ * aligned matrices with leading dimensions that are multiples of 8 select the TMA path. A call's
+ * kernels may start while the stream's earlier ones finish; they read and write memory only after
+ * those are complete.
+ * Graphs: a stream's workspaces are allocated by its first call of a kind and size. Make that call
+ * before capturing the stream: a captured call that needs a larger workspace is refused
+ * (SGEMM_ERR_LAUNCH). Workspaces that later calls outgrow are kept,
+ * so a graph stays valid until sgemm_release_workspace(). A graph uses the workspaces of the
+ * stream that it was captured on: its replays must not overlap that stream's other calls, nor
+ * the replays of another graph captured there.
  */
 typedef enum sgemm_dtype {
     SGEMM_DTYPE_BF16 = 0,
@@ -375,7 +380,8 @@ sgemm_status_t sgemm_selftest_bounded_wait(int which, void *stream);
 
 /* Frees every workspace: stream-K and split-K partial sums, repacked and transposed operand
  * copies, TF32 split operands, the layer operators' buffers and the host-memory path's (the
- * next call that needs one allocates it again). Synchronises the device first. */
+ * next call that needs one allocates it again). Synchronises the device first. Graphs that hold
+ * captured calls must not be replayed afterwards. */
 sgemm_status_t sgemm_release_workspace(void);
 
 /*
