@@ -3,14 +3,26 @@
 
 #include <algorithm>
 #include <mutex>
+#include <thread>
 #include <vector>
 
 namespace sg {
 namespace {
 
-struct Entry {
+// A handle does not identify a stream: cudaStreamPerThread names one of each host thread, and a
+// destroyed stream's handle may be given to a new one while the old one's kernels still run. The
+// stream's id does, but it cannot be asked for while the stream is being captured. The buffers are
+// then the ones that the handle named last, outside a capture.
+struct Name {
     int dev;
-    cudaStream_t stream;
+    cudaStream_t handle;
+    std::thread::id thread;  // of cudaStreamPerThread
+    bool operator==(const Name &o) const { return dev == o.dev && handle == o.handle && thread == o.thread; }
+};
+struct Entry {
+    Name name;
+    bool named = true;  // false: the handle has named another stream since
+    unsigned long long stream;  // its id
     int use;
     void *ptr;
     size_t bytes;
@@ -38,24 +50,32 @@ cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, v
         *detail = "cudaGetDevice failed";
         return err;
     }
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    err = cudaStreamIsCapturing(stream, &status);
+    const bool captured = status != cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (err == cudaSuccess && !captured) err = cudaStreamGetId(stream, &id);
+    if (err != cudaSuccess) {
+        cudaGetLastError();
+        *detail = "the stream cannot be used now";
+        return err;
+    }
+    const Name name{dev, stream, stream == cudaStreamPerThread ? std::this_thread::get_id() : std::thread::id()};
     std::lock_guard<std::mutex> lock(g_mutex);
     Entry *e = nullptr;
     for (auto &w : g_entries)
-        if (w.dev == dev && w.stream == stream && w.use == use) e = &w;
-    if (!e) {
-        g_entries.push_back({dev, stream, use, nullptr, 0});
-        e = &g_entries.back();
+        if (w.use == use && (captured ? w.named && w.name == name : w.stream == id && w.name.dev == dev)) e = &w;
+    if ((!e || e->bytes < bytes || e->distrusted) && captured) {
+        *detail = "a captured call needs a larger or cleared workspace (make a call of its kind and sizes on the "
+                  "stream before the capture)";
+        return cudaErrorStreamCaptureUnsupported;
     }
-    if (e->bytes < bytes || e->distrusted) {
-        cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-        err = cudaStreamIsCapturing(stream, &capture);
-        if (err == cudaSuccess && capture != cudaStreamCaptureStatusNone) err = cudaErrorStreamCaptureUnsupported;
-        if (err != cudaSuccess) {
-            cudaGetLastError();
-            *detail = "a captured call needs a larger or cleared workspace (make a call of its kind and sizes on "
-                      "the stream before the capture)";
-            return err;
-        }
+    if (!e) {
+        for (auto &w : g_entries)
+            if (w.name == name && w.stream != id) w.named = false;
+        Entry fresh{name, true, id, use, nullptr, 0};
+        g_entries.push_back(fresh);
+        e = &g_entries.back();
     }
     if (e->bytes < bytes) {
         // Half as much again at least, so that the outgrown buffers add up to twice the last one at most.
@@ -106,7 +126,7 @@ cudaError_t release_layer_workspaces() {
         const cudaError_t err = cudaFree(ptr);
         if (err != cudaSuccess && first == cudaSuccess) first = err;
     };
-    for (auto &w : g_entries) release(w.dev, w.ptr);
+    for (auto &w : g_entries) release(w.name.dev, w.ptr);
     for (auto &w : g_outgrown) release(w.dev, w.ptr);
     cudaSetDevice(cur);
     g_entries.clear();

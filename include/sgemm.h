@@ -271,7 +271,7 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * those are complete.
  * Graphs: a stream's workspaces are allocated by its first call of a kind and size. Make that call
  * before capturing the stream: a captured call that needs a larger workspace is refused
- * (SGEMM_ERR_LAUNCH). Workspaces that later calls outgrow are kept,
+ * (SGEMM_ERR_LAUNCH). Workspaces that later calls outgrow, and those of destroyed streams, are kept,
  * so a graph stays valid until sgemm_release_workspace(). A graph uses the workspaces of the
  * stream that it was captured on: its replays must not overlap that stream's other calls, nor
  * the replays of another graph captured there.

@@ -10,8 +10,9 @@ namespace {
 std::map<void *, size_t> live;
 size_t room = ~static_cast<size_t>(0);  // of one allocation
 int clears = 0, failures = 0, device = 0;
+std::map<cudaStream_t, unsigned long long> ids;  // of handles that are not their own id
 bool fail_clear = false;
-cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+cudaStream_t captured = nullptr;  // the stream that is being captured
 
 void expect(bool ok, const char *what) {
     if (ok) return;
@@ -47,7 +48,13 @@ cudaError_t cudaMemsetAsync(void *p, int, size_t bytes, cudaStream_t) {
     ++clears;
     return cudaSuccess;
 }
-cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus *s) { return *s = capture, cudaSuccess; }
+cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long *id) {
+    expect(s != captured, "the id is not asked for during the stream's capture (which that ends)");
+    return *id = ids.count(s) ? ids[s] : reinterpret_cast<size_t>(s), cudaSuccess;
+}
+cudaError_t cudaStreamIsCapturing(cudaStream_t q, cudaStreamCaptureStatus *s) {
+    return *s = q == captured ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone, cudaSuccess;
+}
 }
 
 int main() {
@@ -57,22 +64,43 @@ int main() {
     expect(get(s, 500) == a && get(s, 1000) == a && clears == 1, "a large enough buffer is used again as it is");
     expect(get(t, 1000) != a && get(s, 1000, sg::kScratchDz) != a, "streams and uses do not share");
 
+    void *mine = get(cudaStreamPerThread, 1000);
+    ids[cudaStreamPerThread] = 77;  // the same handle in another host thread
+    expect(get(cudaStreamPerThread, 1000) != mine, "each thread's default stream has its own");
+    void *old = get(t, 1000);
+    ids[t] = 78;  // a stream created after `t` was destroyed may get its handle
+    expect(get(t, 1000) != old, "a handle used again is another stream");
+    ids.clear();
+    expect(get(cudaStreamPerThread, 1000) == mine, "and the first thread's is still there");
+
     void *b = get(s, 1001);
     expect(b && b != a && live.count(a), "an outgrown buffer, whose address a graph may hold, is kept");
     expect(live[b] >= 1500, "growth is geometric");
     expect(get(s, 1001) == b && get(s, live[b]) == b, "the larger one is used from then on");
 
-    capture = cudaStreamCaptureStatusActive;
+    captured = s;
     size_t buffers = live.size();
     int cleared = clears;
     expect(get(s, 1500) == b, "a capture may use what is there");
     expect(!get(s, 1 << 20) && live.size() == buffers && clears == cleared, "a capture does not grow a buffer");
-    expect(!get(stream_at(0x3000), 16), "a capture allocates none");
+    captured = stream_at(0x3000);
+    expect(!get(captured, 16), "a capture allocates none");
+    expect(get(s, 16) == b, "another stream goes on meanwhile");
+    captured = s;
     sg::layer_scratch_distrust();
     expect(!get(s, 16) && clears == cleared, "a capture does not clear a buffer");
-    capture = cudaStreamCaptureStatusNone;
+    captured = nullptr;
     expect(get(s, 16) == b && clears == cleared + 1, "the next call outside a capture clears it");
     expect(get(s, 16) == b && clears == cleared + 1, "once");
+
+    const cudaStream_t again = stream_at(0x4000);
+    void *first = get(again, 64), *first_dz = get(again, 64, sg::kScratchDz);
+    ids[again] = 79;  // destroyed, and its handle given to a new stream
+    void *second = get(again, 64);
+    captured = again;
+    expect(second != first && get(again, 64) == second, "a capture uses the buffers of the handle's latest stream");
+    expect(first_dz && !get(again, 64, sg::kScratchDz), "and none of the streams before it");
+    captured = nullptr;
 
     fail_clear = true;
     expect(!get(s, 1 << 16), "a clear that fails fails the call");

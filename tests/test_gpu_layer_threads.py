@@ -102,3 +102,28 @@ def test_experts_beside_linear_on_one_stream(sgemm_lib):
     assert sg.sgemm_device_status() == sg.SGEMM_OK
     assert all(torch.equal(a, b) for got in got_moe for a, b in zip(got, want_moe))
     assert all(torch.equal(got, want_linear) for got in got_linear)
+
+
+def test_each_threads_default_stream_has_its_own_workspaces(sgemm_lib):
+    """cudaStreamPerThread is one handle for a different stream in every thread."""
+    sg = sgemm_lib
+    per_thread = 2  # cudaStreamPerThread
+    M, N, K = 260, 264, 4096  # cut along k: pieces and arrival counters in the workspace
+    xs = [normal(i, M, K) for i in range(3)]
+    w = normal(9, N, K, scale=1 / 64)
+    want = [sg.linear(x, w, act="gelu") for x in xs]
+    outs = [[torch.zeros_like(want[0]) for _ in range(40)] for _ in xs]
+    torch.cuda.synchronize()
+
+    def calls(i):
+        def job():
+            for out in outs[i]:
+                sg.sgemm_linear("bf16", "T", M, N, K, xs[i], K, w, K, None, "gelu", None, 0, out, N,
+                                stream=per_thread)
+        return job
+
+    run_together([calls(i) for i in range(len(xs))])
+    torch.cuda.synchronize()
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+    for i, group in enumerate(outs):
+        assert all(torch.equal(out, want[i]) for out in group), i
