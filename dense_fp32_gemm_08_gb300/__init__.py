@@ -308,23 +308,58 @@ def sgemm_selftest_bounded_wait(which: int, stream=None) -> None:
     _check(lib().sgemm_selftest_bounded_wait(which, _stream(stream)))
 
 
+def _side_stream(torch, device, queue):
+    """The stream with the address `queue` (None: the current one) as a torch stream if it is not the
+    current stream of `device`, else None."""
+    if queue is None or queue == torch._C._cuda_getCurrentRawStream(device.index):
+        return None
+    if queue in (0, 1):  # the legacy default stream's two addresses
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(queue, device=device)
+
+
+def _empty(torch, side, shape, dtype, device):
+    """An output. On a side stream its memory comes from that stream's pool, so that no pending work
+    of the current stream still uses it, and is kept while the current stream may use it."""
+    if side is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(side):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _in_use(side, *tensors):
+    """The tensors' memory is not handed out again before the side stream is done with it."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(side)
+
+
 def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, tensor_cores: bool = False,
            stream=None):
     """torch convenience: row-major 2-D CUDA float32 tensors, returns C (allocated if None).
 
-    Rows must be contiguous (stride(1) == 1); the row stride is the leading dimension.
+    Rows must be contiguous (stride(1) == 1); the row stride is the leading dimension. With a
+    ``stream`` other than the current one, the inputs must be ready there and the caller orders
+    later uses of C after it; no tensor's memory is handed out again before the call is done.
     """
     import torch
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[0]:
         raise ValueError("matmul expects A (M x K) and B (K x N)")
     M, K = A.shape
     N = B.shape[1]
+    side = None
+    if stream is not None and A.is_cuda:
+        side = _side_stream(torch, A.device, _stream(stream))
     if C is None:
-        C = torch.empty((M, N), dtype=torch.float32, device=A.device)
+        C = _empty(torch, side, (M, N), torch.float32, A.device)
         beta = 0.0
     for t in (A, B, C):
         if t.stride(1) != 1 and t.shape[1] > 1:
             raise ValueError("rows must be contiguous")
+    if side is not None:
+        _in_use(side, A, B, C)
     fn = sgemm_3xtf32 if tensor_cores else sgemm
     fn(M, N, K, alpha, A, max(A.stride(0), 1), B, max(B.stride(0), 1), beta, C,
        max(C.stride(0), 1), stream)
@@ -335,6 +370,10 @@ def matmul(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, tensor_cores: bo
 #
 # A call on a small layer costs the GPU a few microseconds, so these wrappers keep the host's share
 # small: each tensor is looked at once, and the stream is read without building a Stream object.
+#
+# With a `stream` other than the current one, the inputs must be ready on it and the caller orders
+# later uses of the outputs after it, as for any work on a side stream. The memory of a call's
+# tensors is not handed out again before both streams are done with it, whenever they are dropped.
 
 def _dtype_code(dtype) -> int:
     return dtype if isinstance(dtype, int) else _DTYPES.get(str(dtype), -1)
@@ -420,15 +459,17 @@ def _begin(x):
 
 
 def _queue(torch, device, stream):
-    """The stream's address; the tensors must be on the calling thread's current device."""
+    """(address, side stream or None) of a call's stream; the tensors must be on the calling thread's
+    current device."""
     index = device.index
     if device.type != "cuda":
         raise TypeError("tensor arguments must live on a CUDA device")
     if index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {device}, which is not the current device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index), None
+    queue = stream if isinstance(stream, int) else stream.cuda_stream
+    return queue, _side_stream(torch, device, queue)
 
 
 def _matrix(t, rows, cols, dtype, device, what):
@@ -484,16 +525,19 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
         pb = _vector(bias, N, device, "bias")
     if residual is not None:
         pr, ldr = _matrix(residual, M, N, dtype, device, "residual")
-    if out is None:
-        out, ldy = torch.empty((M, N), dtype=dtype, device=device), max(N, 1)
-        py = out.data_ptr()
-    else:
+    if out is not None:
         py, ldy = _matrix(out, M, N, dtype, device, "out")
+    queue, side = _queue(torch, device, stream)
+    if out is None:
+        out, ldy = _empty(torch, side, (M, N), dtype, device), max(N, 1)
+        py = out.data_ptr()
     if save_pre:
-        pre = torch.empty((M, N), dtype=dtype, device=device)
+        pre = _empty(torch, side, (M, N), dtype, device)
         pz = pre.data_ptr()
+    if side is not None:
+        _in_use(side, x, weight, bias, residual, out)
     status = (_lib or lib()).sgemm_linear(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act), pr,
-                                          ldr, py, ldy, pz, max(N, 1), _queue(torch, device, stream))
+                                          ldr, py, ldy, pz, max(N, 1), queue)
     if status:
         _check(status)
     return (out, pre) if save_pre else out
@@ -510,17 +554,19 @@ def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=Tru
     pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
     pg, ldg = _matrix(dy, M, N, dtype, device, "dy")
     pz, ldz = (None, 0) if pre is None else _matrix(pre, M, N, dtype, device, "pre")
-    queue = _queue(torch, device, stream)
+    queue, side = _queue(torch, device, stream)
     dx = dw = db = px_out = pw_out = pb_out = None
     if need_dx:
-        dx = torch.empty((M, K), dtype=dtype, device=device)
+        dx = _empty(torch, side, (M, K), dtype, device)
         px_out = dx.data_ptr()
     if need_dw:
-        dw = torch.empty(weight.shape, dtype=dtype, device=device)
+        dw = _empty(torch, side, weight.shape, dtype, device)
         pw_out = dw.data_ptr()
     if need_db:
-        db = torch.empty(N, dtype=torch.float32, device=device)
+        db = _empty(torch, side, (N,), torch.float32, device)
         pb_out = db.data_ptr()
+    if side is not None:
+        _in_use(side, dy, x, weight, pre)
     status = (_lib or lib()).sgemm_linear_backward(code, op, M, N, K, pg, ldg, pz, ldz, _act_code(act), px,
                                                    ldx, pw, ldw, px_out, max(K, 1), pw_out,
                                                    max(weight.shape[1], 1), pb_out, queue)
@@ -572,14 +618,16 @@ def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, act
         if active.dtype is not torch.bool and active.dtype is not torch.uint8:
             raise TypeError("active must be bool or uint8")
         pa = _vector(active, T, device, "active")
-    queue = _queue(torch, device, stream)
-    if out is None:
-        out, ldy = torch.empty((T, D), dtype=dtype, device=device), max(D, 1)
-        py = out.data_ptr()
-    else:
+    if out is not None:
         py, ldy = _matrix(out, T, D, dtype, device, "out")
-    index = torch.empty((T, topk), dtype=torch.int32, device=device)
-    weight = torch.empty((T, topk), dtype=torch.float32, device=device)
+    queue, side = _queue(torch, device, stream)
+    if out is None:
+        out, ldy = _empty(torch, side, (T, D), dtype, device), max(D, 1)
+        py = out.data_ptr()
+    index = _empty(torch, side, (T, topk), torch.int32, device)
+    weight = _empty(torch, side, (T, topk), torch.float32, device)
+    if side is not None:
+        _in_use(side, x, router, w_gate, w_up, w_down, active, residual, out)
     status = (_lib or lib()).sgemm_moe(code, _act_code(act), T, E, topk, D, F, px, ldx, pr, ldr, pg, pu, ldu,
                                        su, pd, ldd, sd, 1 if renormalize else 0, pa, ps, lds, py, ldy,
                                        index.data_ptr(), weight.data_ptr(), queue)
