@@ -7,7 +7,7 @@
 //
 // The fused kernel (moe_stream16.cu) takes layers whose matrices TMA can address; this file has the
 // choice and the kernels for the others.
-#include "epilogue.cuh"
+#include "activation16.cuh"
 #include "half16.cuh"
 #include "moe16.cuh"
 
@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(256) moe_up_kernel(const Moe16 m, const int *i
         for (int o = 16; o > 0; o >>= 1) sum[r] += __shfl_xor_sync(0xFFFFFFFFu, sum[r], o);
     if (lane < 2 && f + lane < m.F) {
         const float u = lane ? sum[1] : sum[0], g = lane ? sum[ROWS - 1] : sum[ROWS - 2];
-        h[pair * static_cast<long long>(m.F) + f + lane] = GATED ? activate(g, m.act) * u : activate(u, m.act);
+        float a = GATED ? g : u;
+        with_activation(m.act, [&](auto act) { a = activate16<decltype(act)::value>(a); });
+        h[pair * static_cast<long long>(m.F) + f + lane] = GATED ? a * u : a;
     }
 }
 
