@@ -264,7 +264,8 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * The feed-forward layers around the products above, for models kept in 16 bits: X, W, bias, R,
  * Y and the rest are bfloat16 or IEEE half values (`dtype`; all of a call's matrices alike),
  * widened exactly when read. Every sum, softmax statistic and activation is held in fp32 and
- * each output is rounded once, to nearest even. Conventions (streams, workspaces, errors,
+ * each output is rounded once, to nearest even; two intermediate matrices are rounded as well, dZ of
+ * the gradients and h_e of the experts (see there). Conventions (streams, workspaces, errors,
  * thread safety) are those above; pointers need their type's own alignment only, and 16-byte
  * aligned matrices with leading dimensions that are multiples of 8 select the TMA path. A call's
  * kernels may start while the stream's earlier ones finish; they read and write memory only after
@@ -342,6 +343,9 @@ sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int
  *          expert: its Y is R (or 0), its indices -1, its weights 0, and its X is not used.
  *   R      T x D, ldr >= max(1, D), or NULL; it may be Y itself.   Y  T x D, ldy >= max(1, D).
  *   topk_index (int32) and topk_weight (fp32): T x topk each, largest score first, or NULL.
+ * h_e is rounded to the call's dtype before the second product, whose operands the tensor cores take
+ * in 16 bits. In half, finite values of h_e beyond 65504 stay finite: such a row is held divided by
+ * a power of two. Matrices that TMA cannot address run without tensor cores and keep h_e in fp32.
  * A NaN score counts as the largest and makes its token's weights NaN. Only the chosen experts'
  * weights are read. The result does not depend on timing, and a token's does not depend on the
  * values of the other tokens (an infinity or NaN stays in its own row).
