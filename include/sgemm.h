@@ -347,8 +347,9 @@ sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int
  * in 16 bits. In half, finite values of h_e beyond 65504 stay finite: such a row is held divided by
  * a power of two. Matrices that TMA cannot address run without tensor cores and keep h_e in fp32.
  * A NaN score counts as the largest and makes its token's weights NaN. Only the chosen experts'
- * weights are read. The result does not depend on timing, and a token's does not depend on the
- * values of the other tokens (an infinity or NaN stays in its own row).
+ * weights are read. The result does not depend on timing. An infinity or NaN stays in its own
+ * token's row. Which experts a batch uses decides how the fp32 sums are grouped, so the last bits
+ * of a token's result may differ from batch to batch.
  */
 sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T, int64_t E,
                          int64_t topk, int64_t D, int64_t F, const void *X, int64_t ldx,
