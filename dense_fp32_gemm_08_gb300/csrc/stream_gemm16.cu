@@ -289,13 +289,17 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     p.KB = static_cast<int>((g.K + static_cast<long long>(kStreamK) - 1) / kStreamK);
     p.split.total = p.tiles * p.KB;
     // Equal pieces of every tile, of 5 blocks or more (8 for more columns, whose pieces take longer to
-    // sum), where they occupy enough SMs or more would be shorter: a CTA then has one piece, and the
-    // tiles complete together. Else the blocks of all tiles in equal runs over all SMs. (Whole,
-    // 4 pieces, equal runs: 13 rows 1536 -> 3008 10.3, 7.8, 11.2 us; 1 row 2048 -> 2048 12.9, 8.1, 10.3; 96
-    // tiles of 64 blocks, 1 row 4096 -> 12288: 23.7 whole, 22.1 in equal runs.)
+    // sum): a CTA then has one piece, and the tiles complete together. Else the blocks of all tiles in
+    // equal runs over all SMs. Pieces where more would be shorter than that anyway, or where they take
+    // less time: a block streams in 0.325 us on some of the SMs and 0.369 on all, whose rate memory
+    // bounds; a whole tile takes 2.9 us besides, a cut one 4.4, runs that cross tiles 7.5. (One row,
+    // pieces and runs: 96 tiles of 64 blocks 23.7 and 22.2 us, 112 23.9 and 24.9, 120 24.2 and 27.3; 112 of 224
+    // blocks 76.0 and 69.1; 39 of 32 in three pieces 9.5 and 11.3; 52 of 224 in two 42.3 and 35.8.)
     const int by_blocks = std::max(1, p.KB / (NT == 16 ? 5 : 8));
     const int cut = std::min(by_blocks, sms[dev] / p.tiles);
-    if (cut > 0 && (cut == by_blocks || 10LL * p.tiles * cut >= 8LL * sms[dev]))
+    const double pieces_us = cut > 0 ? 0.325 * ((p.KB + cut - 1) / cut) + (cut > 1 ? 4.4 : 2.9) : 0.0;
+    const double runs_us = 0.369 * p.split.total / sms[dev] + 7.5;
+    if (cut > 0 && (cut == by_blocks || pieces_us < runs_us))
         p.split.ctas = p.tiles * cut;
     else
         p.split.ctas = std::min(sms[dev], std::max({1, p.split.total / min_run(NT), std::min(p.tiles, sms[dev])}));
