@@ -296,13 +296,20 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
                            g.N);
     } else {
         const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) && (g.act == kActNone || tma_rows(g.z, g.ldz));
-        // Rows per CTA, in whole steps: about whole rounds of the 3 x 152 CTAs that run at once, with 256
+        // Rows per CTA, in whole steps: about whole rounds of the CTAs that run at once, three per SM, with 256
         // rows or so at most (a short last round) and a step at least (the last CTA of a column
         // block adds the sums of all of them). db alone, 2048 x 2048: 18.0 us with 8 rows, 9.5 with 32;
         // 4095 x 3001 unaligned: 49 us with 8 rows, 24.8 with 88 (1.2 rounds), 19.2 with 112 (one).
         const long long step = vec ? 32 : 16;  // rows that a CTA has under way at once
         const long long blocks = (g.N + static_cast<long long>(kGradCols) - 1) / kGradCols;
-        const long long resident = 3 * 152;
+        int dev = 0, sms = 0;
+        err = cudaGetDevice(&dev);
+        if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err != cudaSuccess) {
+            *detail = "device query failed";
+            return err;
+        }
+        const long long resident = 3LL * sms;
         const long long rounds = g.M / std::max<long long>(1, resident / blocks) / 256 + 1;
         const long long want = std::max<long long>(1, rounds * resident / blocks);
         long long rows = std::max(step, (g.M / want + step / 2) / step * step);

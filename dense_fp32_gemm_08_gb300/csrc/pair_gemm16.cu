@@ -522,8 +522,8 @@ cudaError_t prepare(int dev, int *pairs) {
 // 0.31 us, a piece 0.085 us to write and read (256 KiB at 3 TB/s), and summing s of them 2 s us. (bf16:
 // gradients of 6338 rows 80 -> 288, two tiles of 100 blocks for dW: 41 us whole, 28 cut. 512 x 4096 x
 // 14336, 32 tiles of 224 blocks: 73 and 51. 512 x 12288 x 14336, 96 tiles: 147 and 130. 1024 x 4096 x
-// 4096, 64 tiles of 64 blocks, stays whole: 27, 40 cut in two.) At most four rounds of items, 80 MB
-// of pieces.
+// 4096, 64 tiles of 64 blocks, stays whole: 27, 40 cut in two.) A product's items are four rounds of the
+// pairs at most, its pieces 80 MB.
 void cut_along_k(PairParams &p, int n, int pairs) {
     PairProduct &a = p.g[0], &b = p.g[1];
     const int tiles_a = a.items, tiles_b = n == 2 ? b.items : 0, kb_b = n == 2 ? b.KB : 1;

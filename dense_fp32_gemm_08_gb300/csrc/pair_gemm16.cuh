@@ -19,8 +19,8 @@ bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols
 // matrices may have any alignment.
 cudaError_t pair_gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail);
 
-// The product for few rows of A (at most 256), streaming B's blocks once over all SMs. A and B
-// must satisfy tma_rows; K > 0.
+// The product for few rows of A, streaming B's blocks once over all SMs: up to 64 rows, and more
+// where the 128 x 64 tiles number at most 128. A and B must satisfy tma_rows; K > 0.
 bool stream_gemm16_supports(const Gemm16 &g);
 cudaError_t stream_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail);
 

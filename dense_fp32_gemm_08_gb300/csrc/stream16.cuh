@@ -3,10 +3,11 @@
 //
 // The product is computed transposed: a tile's 128 rows are 128 output features (weights are the
 // MMA's A operand) and its NT columns are tokens, so that every weight passes through shared memory
-// once for up to NT tokens. The k-blocks of all tiles form one line
-// of units, cut into equal runs, one per CTA (one CTA per SM): each SM streams the same number of
-// bytes, however few tiles there are. A tile cut between CTAs is summed in fp32 from its pieces
-// in the order of k, by the warp whose piece arrives last (nothing waits).
+// once for up to NT tokens. The k-blocks of all tiles form one line of units, cut into equal runs, one
+// per CTA. There is a run for each SM at most, so that each streams the same number of bytes however
+// few tiles there are, or as many runs as there are equal pieces of all tiles. A tile cut between
+// CTAs is summed in fp32 from its pieces in the order of k, by the warp whose piece arrives last
+// (nothing waits).
 #pragma once
 
 #include "tc16.cuh"

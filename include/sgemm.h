@@ -270,6 +270,10 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * aligned matrices with leading dimensions that are multiples of 8 select the TMA path. A call's
  * kernels may start while the stream's earlier ones finish; they read and write memory only after
  * those are complete.
+ * Timeouts: after a wait inside a kernel has expired, call sgemm_device_status() before the next
+ * operator, which then clears the arrival counters that the kernel left in the workspaces. Until then
+ * results are undefined. Graphs captured before must be captured again, after
+ * sgemm_release_workspace().
  * Graphs: a stream's workspaces are allocated by its first call of a kind and size. Make that call
  * before capturing the stream: a captured call that needs a larger workspace is refused
  * (SGEMM_ERR_LAUNCH). Workspaces that later calls outgrow, and those of destroyed streams, are kept,
