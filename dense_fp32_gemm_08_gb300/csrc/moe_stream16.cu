@@ -27,7 +27,7 @@
 // the values that do not fit, and the row's largest, in fp32; after its barrier, and only in a call
 // that has such a row, the epilogue's warps divide the row, a further barrier follows, and the
 // sum at the end multiplies the expert's output by the same power. (24 tokens through 64 experts in
-// half, no such row: 165.3 us; 163.8 without the check.)
+// half, no such row: 164.2 us; 163.9 without the check.)
 #include "activation16.cuh"
 #include "layer16.cuh"
 #include "moe16.cuh"
@@ -44,10 +44,10 @@ constexpr int kMaxDevices = 64;
 constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopk;
 
 // Grid barrier state, zero between calls (`gen` only counts up).
-struct MoeSync {
+struct alignas(8) MoeSync {
     unsigned int count[4];
     unsigned int gen;
-    unsigned int wide;  // half: set when a value of h is past the type's range
+    unsigned int wide;  // half: set when a value of h is past the type's range; read with `gen`
     unsigned int done;  // CTAs at the end of such a call
     unsigned int largest[kPairs];  // the largest of a row's finite values past the range (as bits)
 };
@@ -110,11 +110,20 @@ __device__ __forceinline__ unsigned int load_acquire(const unsigned int *p) {
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
     return v;
 }
-// Waits (bounded) until the generation reaches `target`.
-__device__ __forceinline__ bool grid_wait(const unsigned int *gen, unsigned int target) {
+// Waits (bounded) until the generation reaches `target`; the word behind it goes to *next.
+__device__ __forceinline__ bool grid_wait(const unsigned int *gen, unsigned int target, unsigned int *next = nullptr) {
     const unsigned long long t0 = globaltimer_ns();
     for (uint32_t spin = 1;; ++spin) {
-        if (static_cast<int>(load_acquire(gen) - target) >= 0) return true;
+        unsigned int now;
+        if (next) {
+            unsigned long long both;
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(both) : "l"(gen) : "memory");
+            now = static_cast<unsigned int>(both);
+            *next = static_cast<unsigned int>(both >> 32);
+        } else {
+            now = load_acquire(gen);
+        }
+        if (static_cast<int>(now - target) >= 0) return true;
         if ((spin & 63u) == 0u && globaltimer_ns() - t0 > kWaitLimitNs) {
             raise_fault(kFaultTimeout);
             return false;
@@ -331,6 +340,7 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
     float *part = reinterpret_cast<float *>(tmem_slot + 2);  // [8]
     unsigned int *gen_slot = tmem_slot + 10;  // the barriers' generation before step 3's
     unsigned int *wide_slot = tmem_slot + 11;
+    uint64_t *gate = reinterpret_cast<uint64_t *>(tmem_slot + 12);  // half: h is complete and in range
     constexpr bool RANGE = H::kind == kF16;  // h may be past its type's range
     const bool local = scores_local(m);
 
@@ -354,6 +364,7 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
             mbar_init(&acc_full[j], 1);
             mbar_init(&acc_free[j], 4 * C::GROUPS);
         }
+        mbar_init(gate, 1);
         mbar_init_fence();
     }
     if (warp == 2) tmem_alloc<1>(tmem_slot, C::TMEM_COLS);
@@ -424,8 +435,7 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
                 }
             };
             auto open_gate = [&]() {
-                ok = grid_wait(&p.sync->gen, gen0 + 1) && ok;
-                if (RANGE && load_acquire(&p.sync->wide)) ok = grid_wait(&p.sync->gen, gen0 + 2) && ok;
+                ok = (RANGE ? mbar_wait(gate, 0) : grid_wait(&p.sync->gen, gen0 + 1)) && ok;
                 asm volatile("fence.proxy.async;" ::: "memory");  // h was written by plain stores
                 open = true;
                 for (; waiting > 0; --waiting) load_rows();
@@ -591,8 +601,10 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
         if (threadIdx.x == 128) grid_arrive(&p.sync->count[1], &p.sync->gen, ctas);
         if (RANGE) {
             if (threadIdx.x == 128) {
-                grid_wait(&p.sync->gen, *gen_slot + 1);
-                *wide_slot = load_acquire(&p.sync->wide);
+                unsigned int flag = 0;
+                grid_wait(&p.sync->gen, *gen_slot + 1, &flag);
+                *wide_slot = flag;
+                if (!flag) mbar_arrive(gate);
             }
             asm volatile("bar.sync 1, %0;" ::"n"(128 * C::GROUPS) : "memory");
             if (*wide_slot) {
@@ -611,7 +623,11 @@ __global__ void __launch_bounds__((MoeConfig<NT, GATED>::THREADS), 1)
                 asm volatile("fence.proxy.async;" ::: "memory");
                 __threadfence();
                 asm volatile("bar.sync 1, %0;" ::"n"(128 * C::GROUPS) : "memory");
-                if (threadIdx.x == 128) grid_arrive(&p.sync->count[3], &p.sync->gen, ctas);
+                if (threadIdx.x == 128) {
+                    grid_arrive(&p.sync->count[3], &p.sync->gen, ctas);
+                    grid_wait(&p.sync->gen, *gen_slot + 2);
+                    mbar_arrive(gate);
+                }
             }
         }
         const long long ldo = static_cast<long long>(p.tiles_d) * kStreamRows;
