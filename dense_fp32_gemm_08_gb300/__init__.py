@@ -511,7 +511,8 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
     tensors with contiguous rows. ``transw='T'`` takes a weight stored out x in (as
     torch.nn.Linear keeps it), 'N' one stored in x out. Returns y, or (y, pre) with the
     pre-activation that ``linear_backward`` reads when ``save_pre``. ``out`` may be
-    ``residual`` itself."""
+    ``residual`` itself. No gradient is recorded, whether or not the inputs require one
+    (``Linear`` in examples/feed_forward.py does that)."""
     torch, dtype, device, code = _begin(x)
     N, K, op = _weight_shape(weight, transw)
     M = x.shape[0]
@@ -596,7 +597,7 @@ def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, act
     """torch convenience: a whole mixture-of-experts layer for up to 64 tokens. x T x D, router
     E x D, w_gate (or None) and w_up E x F x D, w_down E x D x F, active T booleans or None.
     Returns (y, index, weight) with the chosen experts (int32) and their weights (float32),
-    T x topk each."""
+    T x topk each. No gradient is recorded."""
     torch, dtype, device, code = _begin(x)
     if w_up.dim() != 3:
         raise ValueError("w_up must be 3-D (experts x hidden x width)")

@@ -76,7 +76,7 @@ PackJob pack_job(const uint16_t *src, long long ld, int rows, int cols) {
 // ---- dz = dy * act'(z) and its column sums --------------------------------------------------
 //
 // Bound by memory (two matrices read, one written; db alone, so that none is written: 16384 x 14336
-// bf16 with GELU 191 us, 4.9 TB/s; 4095 x 3001 f16 in unaligned rows 19.4 us, 2.5 TB/s). A CTA
+// bf16 with GELU 202 us, 4.7 TB/s; 4095 x 3001 f16 in unaligned rows 20.3 us, 2.4 TB/s). A CTA
 // covers 256 columns and `rows` rows: a thread 8 columns (16 bytes) of every eighth row, four rows' loads in flight at once. Its 8 fp32
 // sums are added over the CTA's 8 threads of a column in a fixed order into part[row block][n], and
 // the CTA that completes a column block's last part (a count in memory; nothing waits) adds the

@@ -17,7 +17,7 @@
 //
 // Measured, one token through 2 of 8 experts of 4096 x 14336 bf16 (704 MB of weights): 131 us, 5.4
 // TB/s: scores and routing 4.4, step 3 77 (6.1 TB/s), its barrier 6, step 4 38 (6.2 TB/s), its barrier
-// 2.8, the sum 1. 24 tokens through 64 experts of 2048 x 1024 f16 (774 MB): 163 us, 4.7 TB/s; DRAM reads
+// 2.8, the sum 1. 24 tokens through 64 experts of 2048 x 1024 f16 (774 MB): 164 us, 4.7 TB/s; DRAM reads
 // 777 MB. The memory's rate bounds the steps, the slowest CTA's pieces the barriers. (Sending the next
 // weights to L2 during the barrier or the routing, 10 to 64 blocks per CTA, made it 1 to 5% slower.)
 //

@@ -18,8 +18,9 @@
  *   No entry point allocates device memory on every call: workspaces are allocated on first
  *   use (per device and stream: stream-K and split-K partial sums, repacked or transposed
  *   operand copies, the staged product of an unaligned C, the 3xTF32 / TF32 split operands,
- *   the layer operators' intermediate values; per device: the host-memory path's buffers), grown when a larger problem needs more, and
- *   kept until sgemm_release_workspace(). sgemm_noalloc() uses none of them.
+ *   the layer operators' intermediate values; per device: the host-memory path's buffers),
+ *   grown when a larger problem needs more, and kept until sgemm_release_workspace().
+ *   sgemm_noalloc() uses none of them.
  * Streams: every compute call is asynchronous on `stream` (a cudaStream_t; NULL means the
  *   legacy default stream) and does not synchronise. Results are visible to later work on
  *   the same stream.
@@ -320,7 +321,7 @@ sgemm_status_t sgemm_linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, i
  * depend on timing. The two products read dZ rounded to the call's dtype, as a separate
  * activation layer would hand it over: the tensor cores multiply 16-bit values, and a second
  * product for the rounded-off part would double the work for less than the outputs' own
- * rounding. With an activation, dZ lives in a workspace of 2 * M * N' bytes (N' = N rounded up
+ * rounding (in half, |dZ| beyond 65504 is infinite). With an activation, dZ lives in a workspace of 2 * M * N' bytes (N' = N rounded up
  * to a multiple of 8). Outputs must not overlap inputs or each other.
  */
 sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
