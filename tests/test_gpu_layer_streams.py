@@ -19,8 +19,8 @@ def normal(seed, *shape, scale=1.0):
 
 
 def busy():
-    """Some 50 ms of work on the current stream."""
-    torch.cuda._sleep(100_000_000)
+    """Some 0.2 s of work on the current stream, far longer than the calls after it take to queue."""
+    torch.cuda._sleep(400_000_000)
 
 
 def linear(sg, stream):
@@ -81,6 +81,8 @@ def test_outputs_do_not_take_memory_in_use(sgemm_lib, make, by_address):
 def test_dropped_outputs_wait_for_both_streams(sgemm_lib, make):
     s = torch.cuda.Stream()
     _, call, want = make(sgemm_lib, s)
+    call()  # the stream's workspaces exist from here on
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
         busy()
     got = call()
@@ -107,6 +109,8 @@ def test_dropped_outputs_wait_for_both_streams(sgemm_lib, make):
 def test_dropped_inputs_wait_for_the_side_stream(sgemm_lib, make):
     s = torch.cuda.Stream()
     inputs, call, want = make(sgemm_lib, s)
+    call()
+    torch.cuda.synchronize()
     with torch.cuda.stream(s):
         busy()
     got = call()
