@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import Any, NamedTuple
 
 __all__ = [
     "SgemmError", "library_path", "lib", "sgemm", "sgemm_strided_batched", "sgemm_3xtf32",
@@ -23,6 +24,9 @@ __all__ = [
     "sgemm_config_name", "sgemm_select_config", "sgemm_force_config",
     "sgemm_selftest_bounded_wait", "matmul",
     "sgemm_linear", "sgemm_linear_backward", "sgemm_moe", "linear", "linear_backward", "moe",
+    "sgemm_checkpoint8", "sgemm_restore8", "sgemm_linear_checkpoint8",
+    "sgemm_linear_backward_checkpoint8", "sgemm_cross_entropy", "sgemm_cross_entropy_backward",
+    "Checkpoint8", "checkpoint8", "restore8", "cross_entropy", "cross_entropy_backward",
     "SGEMM_DTYPE_BF16", "SGEMM_DTYPE_F16",
     "SGEMM_OK", "SGEMM_ERR_INVALID_VALUE", "SGEMM_ERR_LAUNCH", "SGEMM_ERR_TIMEOUT",
     "SGEMM_ERR_UNSUPPORTED",
@@ -96,6 +100,21 @@ def _bind(L):
     L.sgemm_moe.argtypes = [i32, i32, i64, i64, i64, i64, i64, p, i64, p, i64, p, p, i64, i64, p,
                             i64, i64, i32, p, p, i64, p, i64, p, p, p]
     L.sgemm_moe.restype = i32
+    L.sgemm_checkpoint8.argtypes = [i32, i64, i64, p, i64, p, i64, p, i64, p]
+    L.sgemm_checkpoint8.restype = i32
+    L.sgemm_restore8.argtypes = [i32, i64, i64, p, i64, p, i64, p, i64, p]
+    L.sgemm_restore8.restype = i32
+    L.sgemm_linear_checkpoint8.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i32, p, i64, p,
+                                           i64, p, i64, p, i64, p]
+    L.sgemm_linear_checkpoint8.restype = i32
+    L.sgemm_linear_backward_checkpoint8.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i64,
+                                                    i32, p, i64, p, i64, p, i64, p, i64, p, i64, p, p]
+    L.sgemm_linear_backward_checkpoint8.restype = i32
+    L.sgemm_cross_entropy.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, p, p, p]
+    L.sgemm_cross_entropy.restype = i32
+    L.sgemm_cross_entropy_backward.argtypes = [i32, i32, i64, i64, i64, p, i64, p, i64, p, i64, p, p,
+                                               p, i64, p, i64, p]
+    L.sgemm_cross_entropy_backward.restype = i32
     L.sgemm_status_string.argtypes = [i32]
     L.sgemm_status_string.restype = ctypes.c_char_p
     L.sgemm_last_error.argtypes = []
@@ -435,6 +454,67 @@ def sgemm_moe(dtype, act, T, E, topk, D, F, X, ldx, Wr, ldwr, Wgate, Wup, ldu, s
                            _ptr_as(topk_weight, ("torch.float32",)), _stream(stream)))
 
 
+_INT8, _FLOAT, _LABELS = ("torch.int8",), ("torch.float32",), ("torch.int64",)
+
+
+def sgemm_checkpoint8(dtype, M, N, X, ldx, Q, ldq, S, lds, stream=None) -> None:
+    """The 8-bit checkpoint (Q, S) of X (see include/sgemm.h)."""
+    dt = _dtype_code(dtype)
+    _check(lib().sgemm_checkpoint8(dt, M, N, _ptr_as(X, _NAMES16.get(dt, ())), ldx, _ptr_as(Q, _INT8), ldq,
+                                   _ptr_as(S, _FLOAT), lds, _stream(stream)))
+
+
+def sgemm_restore8(dtype, M, N, Q, ldq, S, lds, X, ldx, stream=None) -> None:
+    """X restored from its 8-bit checkpoint (see include/sgemm.h)."""
+    dt = _dtype_code(dtype)
+    _check(lib().sgemm_restore8(dt, M, N, _ptr_as(Q, _INT8), ldq, _ptr_as(S, _FLOAT), lds,
+                                _ptr_as(X, _NAMES16.get(dt, ())), ldx, _stream(stream)))
+
+
+def sgemm_linear_checkpoint8(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Zq, ldzq,
+                             Zs, ldzs, stream=None) -> None:
+    """sgemm_linear with the pre-activation kept as an 8-bit checkpoint (see include/sgemm.h)."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_linear_checkpoint8(dt, _op(transw), M, N, K, _ptr_as(X, names), ldx,
+                                          _ptr_as(W, names), ldw, _ptr_as(bias, names), _act_code(act),
+                                          _ptr_as(R, names), ldr, _ptr_as(Y, names), ldy,
+                                          _ptr_as(Zq, _INT8), ldzq, _ptr_as(Zs, _FLOAT), ldzs,
+                                          _stream(stream)))
+
+
+def sgemm_linear_backward_checkpoint8(dtype, transw, M, N, K, dY, lddy, Zq, ldzq, Zs, ldzs, act, Xq, ldxq,
+                                      Xs, ldxs, W, ldw, dX, lddx, dW, lddw, db, stream=None) -> None:
+    """The gradients of sgemm_linear from 8-bit checkpoints of X and Z (see include/sgemm.h)."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_linear_backward_checkpoint8(
+        dt, _op(transw), M, N, K, _ptr_as(dY, names), lddy, _ptr_as(Zq, _INT8), ldzq, _ptr_as(Zs, _FLOAT),
+        ldzs, _act_code(act), _ptr_as(Xq, _INT8), ldxq, _ptr_as(Xs, _FLOAT), ldxs, _ptr_as(W, names), ldw,
+        _ptr_as(dX, names), lddx, _ptr_as(dW, names), lddw, _ptr(db), _stream(stream)))
+
+
+def sgemm_cross_entropy(dtype, transw, T, V, D, X, ldx, W, ldw, labels, loss, lse, stream=None) -> None:
+    """Softmax cross entropy of a vocabulary head (see include/sgemm.h); loss or lse may be None."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_cross_entropy(dt, _op(transw), T, V, D, _ptr_as(X, names), ldx, _ptr_as(W, names), ldw,
+                                     _ptr_as(labels, _LABELS), _ptr_as(loss, _FLOAT), _ptr_as(lse, _FLOAT),
+                                     _stream(stream)))
+
+
+def sgemm_cross_entropy_backward(dtype, transw, T, V, D, dloss, incd, X, ldx, W, ldw, labels, lse, dX, lddx,
+                                 dW, lddw, stream=None) -> None:
+    """The gradients of sgemm_cross_entropy (see include/sgemm.h); dX or dW may be None."""
+    dt = _dtype_code(dtype)
+    names = _NAMES16.get(dt, ())
+    _check(lib().sgemm_cross_entropy_backward(dt, _op(transw), T, V, D, _ptr_as(dloss, _FLOAT), incd,
+                                              _ptr_as(X, names), ldx, _ptr_as(W, names), ldw,
+                                              _ptr_as(labels, _LABELS), _ptr_as(lse, _FLOAT),
+                                              _ptr_as(dX, names), lddx, _ptr_as(dW, names), lddw,
+                                              _stream(stream)))
+
+
 _torch = None
 _CODES: dict = {}
 
@@ -505,14 +585,94 @@ def _weight_shape(weight, transw):
     return (a, b, op) if op == SGEMM_OP_T else (b, a, op)
 
 
+class Checkpoint8(NamedTuple):
+    """A matrix of 16-bit values kept in 8 bits: int8 codes, a float32 scale for each 64 columns of a
+    row, and the type that it is restored to (include/sgemm.h has the format)."""
+    codes: Any
+    scale: Any
+    dtype: Any
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _new_checkpoint(torch, side, rows, cols, dtype, device):
+    """Codes in rows of whole 16 bytes."""
+    codes = _empty(torch, side, (rows, -(-cols // 16) * 16), torch.int8, device)[:, :cols]
+    return Checkpoint8(codes, _empty(torch, side, (rows, -(-cols // 64)), torch.float32, device), dtype)
+
+
+def _saved(c):
+    """(codes, ldq, scale, lds) of a checkpoint made by ``_new_checkpoint``."""
+    return (c.codes.data_ptr(), max(c.codes.stride(0), 1), c.scale.data_ptr(), max(c.scale.shape[1], 1))
+
+
+def _codes(c, rows, cols, dtype, device, what):
+    """(codes, ldq, scale, lds) of a rows x cols checkpoint of the call's type and device."""
+    blocks = -(-cols // 64)
+    if c.codes.shape != (rows, cols) or c.scale.shape != (rows, blocks):
+        raise ValueError(f"{what} must be a checkpoint of shape {(rows, cols)}, got codes "
+                         f"{tuple(c.codes.shape)} and scales {tuple(c.scale.shape)}")
+    if c.dtype is not dtype:
+        raise TypeError(f"{what} is a checkpoint of {c.dtype}: every matrix of a call has one 16-bit type")
+    if c.codes.dtype is not _torch.int8 or c.scale.dtype is not _torch.float32:
+        raise TypeError(f"{what}: a checkpoint has int8 codes and float32 scales")
+    if c.codes.device != device or c.scale.device != device:
+        raise ValueError("the tensors of a call must be on one device")
+    (ldq, inner_q), (lds, inner_s) = c.codes.stride(), c.scale.stride()
+    if (inner_q != 1 and cols > 1) or (inner_s != 1 and blocks > 1):
+        raise ValueError(f"{what}: rows must be contiguous")
+    if rows <= 1:
+        ldq, lds = max(ldq, cols, 1), max(lds, blocks, 1)
+    return c.codes.data_ptr(), ldq, c.scale.data_ptr(), lds
+
+
+def checkpoint8(x, stream=None):
+    """torch convenience: the ``Checkpoint8`` of a 2-D bfloat16 or half CUDA tensor with contiguous
+    rows: 1.06 bytes a value, each within a 254th of the largest of its 64."""
+    torch, dtype, device, code = _begin(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    M, N = x.shape
+    px, ldx = _matrix(x, M, N, dtype, device, "x")
+    queue, side = _queue(torch, device, stream)
+    c = _new_checkpoint(torch, side, M, N, dtype, device)
+    if side is not None:
+        _in_use(side, x)
+    status = (_lib or lib()).sgemm_checkpoint8(code, M, N, px, max(ldx, 1), *_saved(c), queue)
+    if status:
+        _check(status)
+    return c
+
+
+def restore8(checkpoint, stream=None):
+    """torch convenience: the matrix that a ``Checkpoint8`` stands for, in its 16-bit type."""
+    torch, dtype, device, code = _begin(checkpoint)
+    if checkpoint.codes.dim() != 2 or checkpoint.scale.dim() != 2:
+        raise ValueError("a checkpoint's codes and scales must be 2-D")
+    M, N = checkpoint.codes.shape
+    saved = _codes(checkpoint, M, N, dtype, device, "the argument")
+    queue, side = _queue(torch, device, stream)
+    x = _empty(torch, side, (M, N), dtype, device)
+    if side is not None:
+        _in_use(side, checkpoint.codes, checkpoint.scale)
+    status = (_lib or lib()).sgemm_restore8(code, M, N, *saved, x.data_ptr(), max(N, 1), queue)
+    if status:
+        _check(status)
+    return x
+
+
 def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre=False, out=None,
            stream=None):
     """torch convenience: act(x op(weight) + bias) + residual on 2-D bfloat16 or half CUDA
     tensors with contiguous rows. ``transw='T'`` takes a weight stored out x in (as
     torch.nn.Linear keeps it), 'N' one stored in x out. Returns y, or (y, pre) with the
-    pre-activation that ``linear_backward`` reads when ``save_pre``. ``out`` may be
-    ``residual`` itself. No gradient is recorded, whether or not the inputs require one
+    pre-activation that ``linear_backward`` reads when ``save_pre`` (as a ``Checkpoint8`` for
+    ``save_pre='8bit'``). ``out`` may be ``residual`` itself. No gradient is recorded, whether or not the inputs require one
     (``Linear`` in examples/feed_forward.py does that)."""
+    if isinstance(save_pre, str) and save_pre != "8bit":
+        raise ValueError("save_pre is True, False or '8bit'")
     torch, dtype, device, code = _begin(x)
     N, K, op = _weight_shape(weight, transw)
     M = x.shape[0]
@@ -532,11 +692,19 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
     if out is None:
         out, ldy = _empty(torch, side, (M, N), dtype, device), max(N, 1)
         py = out.data_ptr()
-    if save_pre:
+    if save_pre == "8bit":
+        pre = _new_checkpoint(torch, side, M, N, dtype, device)
+    elif save_pre:
         pre = _empty(torch, side, (M, N), dtype, device)
         pz = pre.data_ptr()
     if side is not None:
         _in_use(side, x, weight, bias, residual, out)
+    if save_pre == "8bit":
+        status = (_lib or lib()).sgemm_linear_checkpoint8(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act),
+                                                          pr, ldr, py, ldy, *_saved(pre), queue)
+        if status:
+            _check(status)
+        return out, pre
     status = (_lib or lib()).sgemm_linear(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act), pr,
                                           ldr, py, ldy, pz, max(N, 1), queue)
     if status:
@@ -547,14 +715,26 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
 def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=True, need_dw=True,
                     need_db=True, stream=None):
     """torch convenience: (dx, dw, db) of ``linear`` from dy and the saved pre-activation
-    (None for those not needed; db is float32). The residual's gradient is dy itself."""
+    (None for those not needed; db is float32). The residual's gradient is dy itself. x and pre
+    may each be a ``Checkpoint8``: the results are those of the restored values."""
+    saved = isinstance(x, Checkpoint8)
+    if saved != isinstance(pre, Checkpoint8) and not (saved and pre is None):
+        if saved:
+            x, saved = restore8(x, stream=stream), False
+        else:
+            pre = restore8(pre, stream=stream)
     torch, dtype, device, code = _begin(x)
     N, K, op = _weight_shape(weight, transw)
-    M = x.shape[0]
-    px, ldx = _matrix(x, M, K, dtype, device, "x")
+    if saved:
+        M = x.codes.shape[0]
+        px8 = _codes(x, M, K, dtype, device, "x")
+        pz8 = (None, max(N, 1), None, max(-(-N // 64), 1)) if pre is None else _codes(pre, M, N, dtype, device, "pre")
+    else:
+        M = x.shape[0]
+        px, ldx = _matrix(x, M, K, dtype, device, "x")
+        pz, ldz = (None, 0) if pre is None else _matrix(pre, M, N, dtype, device, "pre")
     pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
     pg, ldg = _matrix(dy, M, N, dtype, device, "dy")
-    pz, ldz = (None, 0) if pre is None else _matrix(pre, M, N, dtype, device, "pre")
     queue, side = _queue(torch, device, stream)
     dx = dw = db = px_out = pw_out = pb_out = None
     if need_dx:
@@ -567,7 +747,14 @@ def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=Tru
         db = _empty(torch, side, (N,), torch.float32, device)
         pb_out = db.data_ptr()
     if side is not None:
-        _in_use(side, dy, x, weight, pre)
+        _in_use(side, dy, weight, *((*x[:2], *(pre[:2] if pre else ())) if saved else (x, pre)))
+    if saved:
+        status = (_lib or lib()).sgemm_linear_backward_checkpoint8(
+            code, op, M, N, K, pg, ldg, *pz8, _act_code(act), *px8, pw, ldw, px_out, max(K, 1), pw_out,
+            max(weight.shape[1], 1), pb_out, queue)
+        if status:
+            _check(status)
+        return dx, dw, db
     status = (_lib or lib()).sgemm_linear_backward(code, op, M, N, K, pg, ldg, pz, ldz, _act_code(act), px,
                                                    ldx, pw, ldw, px_out, max(K, 1), pw_out,
                                                    max(weight.shape[1], 1), pb_out, queue)
@@ -635,3 +822,67 @@ def moe(x, router, w_gate, w_up, w_down, topk, act="silu", renormalize=True, act
     if status:
         _check(status)
     return out, index, weight
+
+
+def _labels(labels, T, device):
+    if labels.dtype is not _torch.int64:
+        raise TypeError(f"labels must be int64, got {labels.dtype}")
+    return _vector(labels, T, device, "labels")
+
+
+def cross_entropy(x, weight, labels, transw="T", stream=None):
+    """torch convenience: (loss, lse), float32 per token, of the softmax over x op(weight) (x T x D;
+    weight V x D for ``transw='T'``, D x V for 'N') at int64 labels. A label outside [0, V), such as
+    -100, does not count: its loss is 0. The logits are not kept. No gradient is recorded
+    (``cross_entropy_backward`` computes it from lse)."""
+    torch, dtype, device, code = _begin(x)
+    V, D, op = _weight_shape(weight, transw)
+    T = x.shape[0]
+    px, ldx = _matrix(x, T, D, dtype, device, "x")
+    pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
+    pl = _labels(labels, T, device)
+    queue, side = _queue(torch, device, stream)
+    loss = _empty(torch, side, (T,), torch.float32, device)
+    lse = _empty(torch, side, (T,), torch.float32, device)
+    if side is not None:
+        _in_use(side, x, weight, labels)
+    status = (_lib or lib()).sgemm_cross_entropy(code, op, T, V, D, px, ldx, pw, ldw, pl, loss.data_ptr(),
+                                                 lse.data_ptr(), queue)
+    if status:
+        _check(status)
+    return loss, lse
+
+
+def cross_entropy_backward(dloss, x, weight, labels, lse, transw="T", need_dx=True, need_dw=True, stream=None):
+    """torch convenience: (dx, dw) of ``cross_entropy`` from dloss (float32 per token, or one value
+    expanded to that shape) and the lse that it returned; None for those not needed."""
+    torch, dtype, device, code = _begin(x)
+    V, D, op = _weight_shape(weight, transw)
+    T = x.shape[0]
+    px, ldx = _matrix(x, T, D, dtype, device, "x")
+    pw, ldw = _matrix(weight, *weight.shape, dtype, device, "weight")
+    pl = _labels(labels, T, device)
+    for t, what in ((dloss, "dloss"), (lse, "lse")):
+        if t.dtype is not torch.float32:
+            raise TypeError(f"{what} must be float32, got {t.dtype}")
+        if t.shape != (T,):
+            raise ValueError(f"{what} must have shape {(T,)}, got {tuple(t.shape)}")
+        if t.device != device:
+            raise ValueError("the tensors of a call must be on one device")
+    ps = _vector(lse, T, device, "lse")
+    queue, side = _queue(torch, device, stream)
+    dx = dw = pdx = pdw = None
+    if need_dx:
+        dx = _empty(torch, side, (T, D), dtype, device)
+        pdx = dx.data_ptr()
+    if need_dw:
+        dw = _empty(torch, side, weight.shape, dtype, device)
+        pdw = dw.data_ptr()
+    if side is not None:
+        _in_use(side, dloss, x, weight, labels, lse)
+    status = (_lib or lib()).sgemm_cross_entropy_backward(code, op, T, V, D, dloss.data_ptr(), dloss.stride(0), px,
+                                                          ldx, pw, ldw, pl, ps, pdx, D, pdw, weight.shape[1],
+                                                          queue)
+    if status:
+        _check(status)
+    return dx, dw

@@ -1,0 +1,230 @@
+// head16.cu: the softmax cross entropy of a vocabulary head on 16-bit values, and its gradient,
+// without keeping the logits z = X . op(W).
+//
+//   lse_t = log sum_v exp z_tv,   loss_t = lse_t - z_t,label
+//   dz_tv = dloss_t (exp(z_tv - lse_t) - [v = label]),   dX = dz . op(W)^T,   dW = X^T . dz
+//
+// The forward pass is the pair product (pair_gemm16.cu) with an epilogue that reduces each row's 64
+// logits of a warp to their maximum and sum of exponentials; a second kernel joins those. The gradient
+// computes the logits again, a piece of the vocabulary at a time: one product whose epilogue
+// writes the piece's dz in 16 bits to scratch, then dX and dW's rows (or columns) of the piece in one
+// launch. dX adds up over the pieces in fp32.
+#include "activation16.cuh"
+#include "half16.cuh"
+#include "layer16.cuh"
+#include "pair_gemm16.cuh"
+
+#include <algorithm>
+
+namespace sg {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
+constexpr int kJoinThreads = 1024;
+
+// Joins the parts of 32 rows: lane = row, a warp every 32nd part, then the warps through shared memory.
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const float2 *parts, long long ld, int n_parts,
+                                                            const float *at, const int64_t *labels, int T, int V,
+                                                            float *loss, float *lse) {
+    __shared__ float2 shared[32][33];
+    grid_dependents();
+    grid_dependency();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x * 32 + lane;
+    auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x);
+        const float base = m == -INFINITY ? 0.0f : m;
+        return make_float2(m, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
+    };
+    float2 a = make_float2(-INFINITY, 0.0f);
+    if (row < T) {
+#pragma unroll 4
+        for (int i = warp; i < n_parts; i += 32) a = join(a, __ldcg(parts + i * ld + row));
+    }
+    shared[warp][lane] = a;
+    __syncthreads();
+    // Warp w now joins row w's 32 values.
+    a = shared[lane][warp];
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) {
+        const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, s), __shfl_xor_sync(0xFFFFFFFFu, a.y, s));
+        a = join(a, b);
+    }
+    const int mine = blockIdx.x * 32 + warp;
+    if (lane == 0 && mine < T) {
+        const float l = a.x + logf(a.y);
+        const int64_t label = labels[mine];
+        if (lse) lse[mine] = l;
+        if (loss) loss[mine] = label >= 0 && label < V ? l - at[mine] : 0.0f;
+    }
+}
+
+// factor[0] = 2^s with the largest finite |dloss| of the counted tokens times 2^s in [2^14, 2^15), factor[1] =
+// 2^-s: half then holds probabilities down to 2^-38 of the largest gradient.
+__global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long long incd, const int64_t *labels,
+                                                      int T, int V, float *factor) {
+    __shared__ float top[32];
+    grid_dependents();
+    grid_dependency();
+    float a = 0.0f;
+    for (int t = threadIdx.x; t < T; t += 1024) {
+        const int64_t label = labels[t];
+        const float d = fabsf(dloss[t * incd]);
+        if (label >= 0 && label < V && d < INFINITY) a = fmaxf(a, d);
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, s));
+    if ((threadIdx.x & 31) == 0) top[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        a = top[threadIdx.x];
+#pragma unroll
+        for (int s = 16; s > 0; s /= 2) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, s));
+        if (threadIdx.x == 0) {
+            const int s = a > 0.0f ? max(-100, min(100, 14 - ilogbf(a))) : 0;
+            factor[0] = ldexpf(1.0f, s);
+            factor[1] = ldexpf(1.0f, -s);
+        }
+    }
+}
+
+// The logits of tokens [t0, t0 + T) and vocabulary entries [v0, v0 + n).
+Gemm16 logits(const Head16 &h, int t0, int T, int v0, int n) {
+    Gemm16 g;
+    g.dtype = h.dtype;
+    g.M = T;
+    g.N = n;
+    g.K = h.D;
+    g.A = h.X + static_cast<long long>(t0) * h.ldx;
+    g.lda = h.ldx;
+    g.B = h.w_dv ? h.W + v0 : h.W + static_cast<long long>(v0) * h.ldw;
+    g.ldb = h.ldw;
+    g.b_mn = h.w_dv;
+    return g;
+}
+
+cudaError_t pack(Head16 &h, cudaStream_t stream, const char **detail) {
+    const Pack16 packs[2] = {{&h.X, &h.ldx, h.T, h.D}, {&h.W, &h.ldw, h.w_dv ? h.D : h.V, h.w_dv ? h.V : h.D}};
+    return pack16_launch(packs, 2, stream, detail);
+}
+
+constexpr int kTokens = 32768;  // per piece of the forward pass
+
+}  // namespace
+
+cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **detail) {
+    Head16 h = head;
+    cudaError_t err = pack(h, stream, detail);
+    if (err != cudaSuccess) return err;
+    const int n_parts = static_cast<int>((h.V + 63LL) / 64);
+    for (int t0 = 0; t0 < h.T; t0 += std::min(kTokens, h.T - t0)) {
+        const int T = std::min(kTokens, h.T - t0);
+        const long long ld = (T + 31) / 32 * 32;
+        void *p = nullptr;
+        err = layer_scratch(kScratchHead, stream, static_cast<size_t>(ld) * 4 + static_cast<size_t>(ld) * n_parts * 8, &p, detail);
+        if (err != cudaSuccess) return err;
+        PairExtra extra;
+        PairHead &x = extra.head;
+        x.labels = h.labels + t0;
+        x.V = h.V;
+        x.at = static_cast<float *>(p);
+        x.parts = reinterpret_cast<float2 *>(x.at + ld);
+        x.ld_parts = ld;
+        const Gemm16 g = logits(h, t0, T, 0, h.V);
+        err = pair_gemm16_extra_launch(&g, 1, kPairLogits, extra, stream, detail);
+        if (err != cudaSuccess) return err;
+        err = launch_early(join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), kJoinThreads, 0, stream,
+                           static_cast<const float2 *>(x.parts), ld, n_parts, static_cast<const float *>(x.at),
+                           x.labels, T, h.V, h.loss ? h.loss + t0 : nullptr, h.lse ? h.lse + t0 : nullptr);
+        if (err != cudaSuccess) {
+            *detail = "loss kernel launch failed";
+            return err;
+        }
+    }
+    return cudaSuccess;
+}
+
+cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const char **detail) {
+    Head16 h = head;
+    cudaError_t err = pack(h, stream, detail);
+    if (err != cudaSuccess) return err;
+    // Pieces of up to 512 MB of dz, of 4096 entries or more, all of about the same size.
+    const long long most = std::max<long long>(4096, (512LL << 20) / 2 / h.T / 256 * 256);
+    const long long pieces = (h.V + most - 1) / most;
+    const int width = static_cast<int>(((h.V + pieces - 1) / pieces + 255) / 256 * 256);
+    const long long ldz = std::min<long long>(width, (h.V + 7LL) / 8 * 8);
+    void *dz = nullptr, *p = nullptr;
+    err = layer_scratch(kScratchHeadDz, stream, static_cast<size_t>(h.T) * ldz * 2, &dz, detail);
+    if (err != cudaSuccess) return err;
+    PairExtra extra;
+    PairHead &x = extra.head;
+    x.labels = h.labels;
+    x.V = h.V;
+    x.lse = h.lse_in;
+    x.dloss = h.dloss;
+    x.incd = h.incd;
+    if (h.dtype == kF16) {
+        err = layer_scratch(kScratchHead, stream, 8, &p, detail);
+        if (err != cudaSuccess) return err;
+        float *factor = static_cast<float *>(p);
+        err = launch_early(factor_kernel, dim3(1), 1024, 0, stream, h.dloss, h.incd, h.labels, h.T, h.V, factor);
+        if (err != cudaSuccess) {
+            *detail = "loss gradient kernel launch failed";
+            return err;
+        }
+        x.factor = factor;
+        extra.sum.factor = factor + 1;
+    }
+    if (h.dX && width < h.V) {
+        err = layer_scratch(kScratchHeadSum, stream, pair_sum_bytes(h.T, h.D), &p, detail);
+        if (err != cudaSuccess) return err;
+        extra.sum.sums = static_cast<float *>(p);
+    }
+    for (int v0 = 0; v0 < h.V; v0 += std::min(width, h.V - v0)) {
+        const int n = std::min(width, h.V - v0);
+        Gemm16 g = logits(h, 0, h.T, v0, n);
+        g.D = static_cast<uint16_t *>(dz);
+        g.ldd = ldz;
+        x.v0 = v0;
+        err = pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
+        if (err != cudaSuccess) return err;
+        Gemm16 list[2];
+        int count = 0;
+        if (h.dX) {
+            Gemm16 &q = list[count++];
+            q.dtype = h.dtype;
+            q.M = h.T;
+            q.N = h.D;
+            q.K = n;
+            q.A = g.D;
+            q.lda = ldz;
+            q.B = g.B;
+            q.ldb = h.ldw;
+            q.b_mn = !h.w_dv;
+            q.D = h.dX;
+            q.ldd = h.lddx;
+        }
+        if (h.dW) {
+            Gemm16 &q = list[count++];
+            q.dtype = h.dtype;
+            q.M = h.w_dv ? h.D : n;
+            q.N = h.w_dv ? n : h.D;
+            q.K = h.T;
+            q.A = h.w_dv ? h.X : g.D;
+            q.lda = h.w_dv ? h.ldx : ldz;
+            q.a_mn = true;
+            q.B = h.w_dv ? g.D : h.X;
+            q.ldb = h.w_dv ? ldz : h.ldx;
+            q.b_mn = true;
+            q.D = h.w_dv ? h.dW + v0 : h.dW + static_cast<long long>(v0) * h.lddw;
+            q.ldd = h.lddw;
+        }
+        extra.sum.first = v0 == 0;
+        extra.sum.last = v0 + n == h.V;
+        err = pair_gemm16_extra_launch(list, count, kPairSum, extra, stream, detail);
+        if (err != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace sg

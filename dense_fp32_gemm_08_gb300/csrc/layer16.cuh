@@ -1,5 +1,6 @@
 // layer16.cuh: host-visible description of the 16-bit layer operators (linear layer, its
-// gradients, mixture-of-experts layer), used by the C ABI in sgemm_api.cu.
+// gradients, mixture-of-experts layer, 8-bit checkpoints, the vocabulary head's loss), used by the C ABI
+// in sgemm_api.cu.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -66,6 +67,67 @@ cudaError_t launch_early(void (*kernel)(Params...), dim3 grid, unsigned threads,
 constexpr int kMaxProducts = 2;
 cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail);
 
+// A matrix to its 8-bit checkpoint (checkpoint8.cuh) and back.
+struct Checkpoint8 {
+    int dtype = 0;
+    int M = 0, N = 0;
+    const uint16_t *X = nullptr;
+    long long ldx = 0;
+    int8_t *Q = nullptr;
+    long long ldq = 0;
+    float *S = nullptr;  // ceil(N / 64) scales per row
+    long long lds = 0;
+};
+struct Restore8 {
+    int dtype = 0;
+    int M = 0, N = 0;
+    const int8_t *Q = nullptr;
+    long long ldq = 0;
+    const float *S = nullptr;
+    long long lds = 0;
+    uint16_t *X = nullptr;
+    long long ldx = 0;
+};
+cudaError_t save8_launch(const Checkpoint8 &c, cudaStream_t stream, const char **detail);
+cudaError_t restore8_launch(const Restore8 &c, cudaStream_t stream, const char **detail);
+
+// The product with its pre-activation kept as an 8-bit checkpoint (of the 16-bit values that `pre` would
+// hold; c.X is not used).
+cudaError_t gemm16_save8_launch(const Gemm16 &g, const Checkpoint8 &c, cudaStream_t stream, const char **detail);
+
+// The vocabulary head's softmax cross entropy: logits z = X . op(W) of T tokens.
+struct Head16 {
+    int dtype = 0;
+    int T = 0, V = 0, D = 0;
+    const uint16_t *X = nullptr;
+    long long ldx = 0;
+    const uint16_t *W = nullptr;
+    long long ldw = 0;
+    bool w_dv = false;  // false: W stored V x D; true: D x V
+    const int64_t *labels = nullptr;  // outside [0, V): the token does not count
+    float *loss = nullptr, *lse = nullptr;  // of the forward pass, either may be null
+    // the gradient's
+    const float *dloss = nullptr;
+    long long incd = 0;
+    const float *lse_in = nullptr;
+    uint16_t *dX = nullptr;
+    long long lddx = 0;
+    uint16_t *dW = nullptr;
+    long long lddw = 0;
+};
+cudaError_t head16_launch(const Head16 &h, cudaStream_t stream, const char **detail);
+cudaError_t head16_grad_launch(const Head16 &h, cudaStream_t stream, const char **detail);
+
+// Aligned copies, in one launch per two, of matrices that TMA cannot address (of rows x cols values):
+// pointer and leading dimension then name the copy. One call's copies share a scratch buffer.
+struct Pack16 {
+    const uint16_t **ptr;
+    long long *ld;
+    int rows, cols;
+};
+constexpr int kMaxPacks = 2 * kMaxProducts;
+cudaError_t pack16_launch(const Pack16 *list, int n, cudaStream_t stream, const char **detail);
+
 // The elementwise part of the linear layer's gradient: dz = dy * act'(z), M x N, and its
 // column sums db (fp32), either of them optional. dz == nullptr: only the sums.
 struct ActGrad {
@@ -123,6 +185,11 @@ enum LayerScratch : int {
     kScratchSumSync = 6,  // arrival counters of the column sums
     kScratchPair = 7,      // pieces of the pair product's cut tiles
     kScratchPairSync = 8,  // their arrival counters
+    kScratchRestoreX = 9,  // restored checkpoints
+    kScratchRestoreZ = 10,
+    kScratchHead = 11,     // the head's partial sums, label logits and factor
+    kScratchHeadDz = 12,   // a piece of the logits' gradient
+    kScratchHeadSum = 13,  // dX over the pieces so far
     kScratchUses
 };
 cudaError_t layer_scratch(LayerScratch use, cudaStream_t stream, size_t bytes, void **out,

@@ -221,6 +221,39 @@ __global__ void zero_kernel(float *p, int n) {
 
 }  // namespace
 
+cudaError_t pack16_launch(const Pack16 *list, int n, cudaStream_t stream, const char **detail) {
+    PackJob jobs[kMaxPacks + 1] = {};
+    const Pack16 *from[kMaxPacks];
+    size_t at[kMaxPacks], elems = 0;
+    int n_jobs = 0;
+    for (int i = 0; i < n; ++i) {
+        const Pack16 &p = list[i];
+        if (tma_rows(*p.ptr, *p.ld)) continue;
+        jobs[n_jobs] = pack_job(*p.ptr, *p.ld, p.rows, p.cols);
+        from[n_jobs] = &p;
+        at[n_jobs++] = elems;
+        elems += static_cast<size_t>(p.rows) * static_cast<size_t>((p.cols + 7LL) / 8 * 8);
+    }
+    if (n_jobs == 0) return cudaSuccess;
+    void *ptr = nullptr;
+    cudaError_t err = layer_scratch(kScratchPack, stream, elems * 2, &ptr, detail);
+    if (err != cudaSuccess) return err;
+    for (int i = 0; i < n_jobs; ++i) {
+        jobs[i].dst = static_cast<uint16_t *>(ptr) + at[i];
+        *from[i]->ptr = jobs[i].dst;
+        *from[i]->ld = jobs[i].ldd;
+    }
+    for (int i = 0; i < n_jobs; i += 2) {
+        const int blocks = jobs[i].gx * jobs[i].gy + jobs[i + 1].gx * jobs[i + 1].gy;
+        err = launch_early(pack16_kernel, dim3(blocks), 256, 0, stream, jobs[i], jobs[i + 1]);
+        if (err != cudaSuccess) {
+            *detail = "repacking kernel launch failed";
+            return err;
+        }
+    }
+    return cudaSuccess;
+}
+
 cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
     cudaError_t err = cudaSuccess;
     Gemm16 q[kMaxProducts];
@@ -240,40 +273,13 @@ cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const 
             return err;
         }
     }
-    // Aligned copies of the operands TMA cannot address, in one launch.
-    PackJob jobs[2 * kMaxProducts] = {};
-    const uint16_t **base[2 * kMaxProducts];
-    size_t at[2 * kMaxProducts], elems = 0;
-    int n_jobs = 0;
-    auto pack = [&](const uint16_t *&ptr, long long &ld, int rows, int cols) {
-        if (tma_rows(ptr, ld)) return;
-        jobs[n_jobs] = pack_job(ptr, ld, rows, cols);
-        base[n_jobs] = &ptr;
-        at[n_jobs++] = elems;
-        ld = (cols + 7LL) / 8 * 8;
-        elems += static_cast<size_t>(rows) * ld;
-    };
+    Pack16 packs[kMaxPacks];
     for (int i = 0; i < products; ++i) {
-        pack(q[i].A, q[i].lda, q[i].a_mn ? q[i].K : q[i].M, q[i].a_mn ? q[i].M : q[i].K);
-        pack(q[i].B, q[i].ldb, q[i].b_mn ? q[i].K : q[i].N, q[i].b_mn ? q[i].N : q[i].K);
+        packs[2 * i] = {&q[i].A, &q[i].lda, q[i].a_mn ? q[i].K : q[i].M, q[i].a_mn ? q[i].M : q[i].K};
+        packs[2 * i + 1] = {&q[i].B, &q[i].ldb, q[i].b_mn ? q[i].K : q[i].N, q[i].b_mn ? q[i].N : q[i].K};
     }
-    if (n_jobs > 0) {
-        void *ptr = nullptr;
-        err = layer_scratch(kScratchPack, stream, elems * 2, &ptr, detail);
-        if (err != cudaSuccess) return err;
-        for (int i = 0; i < n_jobs; ++i) {
-            jobs[i].dst = static_cast<uint16_t *>(ptr) + at[i];
-            *base[i] = jobs[i].dst;
-        }
-        for (int i = 0; i < n_jobs; i += 2) {
-            const int blocks = jobs[i].gx * jobs[i].gy + jobs[i + 1].gx * jobs[i + 1].gy;
-            err = launch_early(pack16_kernel, dim3(blocks), 256, 0, stream, jobs[i], jobs[i + 1]);
-            if (err != cudaSuccess) {
-                *detail = "repacking kernel launch failed";
-                return err;
-            }
-        }
-    }
+    err = pack16_launch(packs, 2 * products, stream, detail);
+    if (err != cudaSuccess) return err;
     // Products that stream weights for a few rows go alone; the others share one launch (and a
     // gradient's two always do when there are more rows: 256 rows 1024 -> 1024 15.4 us, apart 22.5;
     // 4095 x 3001 x 1537 f16 108 us, apart 130).
@@ -287,6 +293,21 @@ cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const 
         }
     }
     return together > 0 ? pair_gemm16_launch(q, together, stream, detail) : cudaSuccess;
+}
+
+cudaError_t gemm16_save8_launch(const Gemm16 &g, const Checkpoint8 &c, cudaStream_t stream, const char **detail) {
+    // The pre-activation goes through scratch in 16 bits.
+    Gemm16 q = g;
+    Checkpoint8 save = c;
+    q.ldz = (g.N + 7LL) / 8 * 8;
+    void *z = nullptr;
+    cudaError_t err = layer_scratch(kScratchRestoreZ, stream, static_cast<size_t>(g.M) * q.ldz * 2, &z, detail);
+    if (err != cudaSuccess) return err;
+    q.pre = static_cast<uint16_t *>(z);
+    save.X = q.pre;
+    save.ldx = q.ldz;
+    err = gemm16_launch(&q, 1, stream, detail);
+    return err == cudaSuccess ? save8_launch(save, stream, detail) : err;
 }
 
 cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **detail) {

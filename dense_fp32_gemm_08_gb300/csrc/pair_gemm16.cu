@@ -87,6 +87,9 @@ struct PairParams {
     uint16_t *pre;
     long long ldz;
     int z_tma;
+    PairExtra extra;
+    int sum_product;  // the product that adds to the sums (-1: none)
+    int q_vec;        // the codes' rows allow 16-byte stores
 };
 struct PairMaps {
     CUtensorMap a[kMaxProducts], b[kMaxProducts], d[kMaxProducts], z;
@@ -255,7 +258,22 @@ __device__ __forceinline__ void add_residual(float (&v)[32], uint32_t (&raw)[20]
     __syncwarp();
 }
 
-template <typename T>
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMinusInf = -__builtin_huge_valf();
+
+// Where the row's label is among the columns from col0 on (outside them: some other number). The
+// token counts if its label is an entry of the vocabulary.
+struct RowLabel {
+    long long at;
+    bool counts;
+    __device__ __forceinline__ RowLabel(const PairHead &h, int row, int M, int col0) {
+        const long long label = row < M ? h.labels[row] : -1;
+        counts = label >= 0 && label < h.V;
+        at = counts ? label - h.v0 - col0 : -1;
+    }
+};
+
+template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     pair_gemm16_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -381,6 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         int j = 0;
         uint32_t raw[20];  // the next block's residual
         float bias[2] = {0.0f, 0.0f};  // of columns col0 + lane and col0 + 32 + lane
+        float factor = 1.0f;
+        if (MODE == kPairSum && p.extra.sum.factor) factor = *p.extra.sum.factor;
+        if (MODE == kPairLogitGrad && p.extra.head.factor) factor = *p.extra.head.factor;
         for (int t = pair; t < p.total_items; t += pairs, ++j) {
             const int set = j & 1;
             const Item item(p, t);
@@ -395,6 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     bias[0] = col0 + lane < g.N ? Half16<T>::widen(p.bias[col0 + lane]) : 0.0f;
                     bias[1] = g.N - col0 - 32 > lane ? Half16<T>::widen(p.bias[col0 + 32 + lane]) : 0.0f;
                 }
+            }
+            RowLabel label(p.extra.head, MODE == kPairLogits || MODE == kPairLogitGrad ? row0 + lane : g.M,
+                           g.M, col0);
+            float lse = 0.0f, dloss = 0.0f;
+            if (MODE == kPairLogitGrad && label.counts) {
+                lse = p.extra.head.lse[row0 + lane];
+                dloss = factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd];
             }
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
             tc_after_sync();
@@ -446,6 +474,91 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     tmem_ld_wait();
                 }
             };
+            if constexpr (MODE == kPairLogits) {
+                float m = kMinusInf, s = 0.0f;
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    float v[32];
+                    values(b, v);
+                    if (b == blocks - 1 && !pieces) release();
+                    const int at = static_cast<int>(label.at) - 32 * b;
+                    const bool mine = label.at >= 32 * b && label.at < 32 * b + 32;
+                    if (__any_sync(0xFFFFFFFFu, mine)) {
+                        float z = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) z = i == at ? v[i] : z;
+                        if (mine) p.extra.head.at[row0 + lane] = z;
+                    }
+                    const int cols = g.N - col0 - 32 * b;
+                    if (cols < 32) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = i < cols ? v[i] : kMinusInf;
+                    }
+                    float top = m;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
+                    const float base = top == kMinusInf ? 0.0f : top;
+                    s *= exp2_approx((m - base) * kLog2e);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) s += exp2_approx((v[i] - base) * kLog2e);
+                    m = top;
+                }
+                if (row0 + lane < g.M)
+                    p.extra.head.parts[static_cast<size_t>(col0 / 64) * p.extra.head.ld_parts + row0 + lane] =
+                        make_float2(m, s);
+                continue;
+            }
+            if constexpr (MODE == kPairLogitGrad) {
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    float v[32];
+                    values(b, v);
+                    if (b == blocks - 1 && !pieces) release();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = exp2_approx((v[i] - lse) * kLog2e);
+                    const int at = static_cast<int>(label.at) - 32 * b;
+                    const bool mine = label.at >= 32 * b && label.at < 32 * b + 32;
+                    if (__any_sync(0xFFFFFFFFu, mine)) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] -= mine && i == at ? 1.0f : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = label.counts ? v[i] * dloss : 0.0f;
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                    store_block<T>(v, buf, &maps.d[0], 1, g.D, g.ldd, g.M, g.N, row0, col0 + 32 * b, lane);
+                }
+                continue;
+            }
+            if constexpr (MODE == kPairSum) {
+                const bool summed = item.product == p.sum_product;
+                float *sums = p.extra.sum.sums + (2 * static_cast<size_t>(item.tile) + rank) * kBN * kBM +
+                              c0 * kBM + quarter * 32 + lane;
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    float v[32];
+                    values(b, v);
+                    if (b == blocks - 1 && !pieces) release();
+                    if (summed) {
+                        if (!p.extra.sum.first) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] += __ldcg(sums + (32 * b + i) * kBM);
+                        }
+                        if (!p.extra.sum.last) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) __stcg(sums + (32 * b + i) * kBM, v[i]);
+                            continue;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] *= factor;
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+                    store_block<T>(v, buf, &maps.d[item.product], g.d_tma, g.D, g.ldd, g.M, g.N, row0,
+                                   col0 + 32 * b, lane);
+                }
+                continue;
+            }
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b) {
                 const int col = col0 + 32 * b;
@@ -489,13 +602,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 constexpr int kMaxDevices = 64;
 
 // Pairs that can run at once (an odd SM of a cluster group stays idle), found once per device.
-template <typename T>
+template <typename T, int MODE>
 cudaError_t prepare(int dev, int *pairs) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t setup[kMaxDevices];
     static int max_pairs[kMaxDevices];
     std::call_once(once[dev], [&] {
-        auto kernel = pair_gemm16_kernel<T>;
+        auto kernel = pair_gemm16_kernel<T, MODE>;
         setup[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           static_cast<int>(kSmem));
         if (setup[dev] != cudaSuccess) return;
@@ -553,15 +666,15 @@ void cut_along_k(PairParams &p, int n, int pairs) {
     }
 }
 
-template <typename T>
-cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
+template <typename T, int MODE>
+cudaError_t launch(const Gemm16 *list, int n, const PairExtra &extra, cudaStream_t stream, const char **detail) {
     int dev = 0, max_pairs = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         *detail = "cudaGetDevice failed";
         return err != cudaSuccess ? err : cudaErrorInvalidDevice;
     }
-    err = prepare<T>(dev, &max_pairs);
+    err = prepare<T, MODE>(dev, &max_pairs);
     if (err != cudaSuccess) {
         *detail = "linear layer kernel set-up failed";
         return err;
@@ -592,12 +705,14 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
         q.ldd = g.ldd;
         // A TMA store also writes zeros into the rest of a row's last 16 bytes, which may belong to
         // the caller's wider matrix: only rows that end on that boundary are stored so.
-        q.d_tma = tma_rows(g.D, g.ldd) && g.N % 8 == 0;
+        // (The logits' gradient goes to scratch whose rows all end on it.)
+        const int n_out = MODE == kPairLogitGrad ? static_cast<int>(std::min(g.ldd, (g.N + 7LL) / 8 * 8)) : g.N;
+        q.d_tma = MODE != kPairLogits && tma_rows(g.D, g.ldd) && n_out % 8 == 0;
         if (!(g.a_mn ? tensor_map_16(&maps.a[i], g.A, g.dtype, g.M, g.K, g.lda, 64, kBK)
                      : tensor_map_16(&maps.a[i], g.A, g.dtype, g.K, g.M, g.lda, kBK, kBM)) ||
             !(g.b_mn ? tensor_map_16(&maps.b[i], g.B, g.dtype, g.N, g.K, g.ldb, 64, kBK)
                      : tensor_map_16(&maps.b[i], g.B, g.dtype, g.K, g.N, g.ldb, kBK, kBN / 2)) ||
-            (q.d_tma && !tensor_map_16(&maps.d[i], g.D, g.dtype, g.N, g.M, g.ldd, 32, 32, true))) {
+            (q.d_tma && !tensor_map_16(&maps.d[i], g.D, g.dtype, n_out, g.M, g.ldd, 32, 32, true))) {
             *detail = "cuTensorMapEncodeTiled rejected a matrix";
             return cudaErrorInvalidValue;
         }
@@ -623,6 +738,8 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
         p.pieces = static_cast<float *>(data);
         p.counters = static_cast<unsigned int *>(sync);
     }
+    p.extra = extra;
+    p.sum_product = MODE == kPairSum && extra.sum.sums ? order[0] : -1;  // list[0]
     if (n == 1) {
         const Gemm16 &g = list[0];
         p.bias = g.bias;
@@ -639,7 +756,7 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
         }
     }
     const int pairs = std::min(p.total_items, max_pairs);
-    err = launch_early(pair_gemm16_kernel<T>, dim3(2u * static_cast<unsigned>(pairs)), kThreads, kSmem,
+    err = launch_early(pair_gemm16_kernel<T, MODE>, dim3(2u * static_cast<unsigned>(pairs)), kThreads, kSmem,
                        stream, maps, p);
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
     return err;
@@ -648,8 +765,31 @@ cudaError_t launch(const Gemm16 *list, int n, cudaStream_t stream, const char **
 }  // namespace
 
 cudaError_t pair_gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail) {
-    return list[0].dtype == kBf16 ? launch<__nv_bfloat16>(list, n, stream, detail)
-                                  : launch<__half>(list, n, stream, detail);
+    return pair_gemm16_extra_launch(list, n, kPairLayer, PairExtra(), stream, detail);
+}
+
+// Room for the sums of an M x N product.
+size_t pair_sum_bytes(int M, int N) {
+    return static_cast<size_t>((M + 255LL) / 256) * static_cast<size_t>((N + 255LL) / 256) * 2 * kBN * kBM * 4;
+}
+
+cudaError_t pair_gemm16_extra_launch(const Gemm16 *list, int n, int mode, const PairExtra &extra,
+                                     cudaStream_t stream, const char **detail) {
+    const bool bf16 = list[0].dtype == kBf16;
+    switch (mode) {
+        case kPairLogits:
+            return bf16 ? launch<__nv_bfloat16, kPairLogits>(list, n, extra, stream, detail)
+                        : launch<__half, kPairLogits>(list, n, extra, stream, detail);
+        case kPairLogitGrad:
+            return bf16 ? launch<__nv_bfloat16, kPairLogitGrad>(list, n, extra, stream, detail)
+                        : launch<__half, kPairLogitGrad>(list, n, extra, stream, detail);
+        case kPairSum:
+            return bf16 ? launch<__nv_bfloat16, kPairSum>(list, n, extra, stream, detail)
+                        : launch<__half, kPairSum>(list, n, extra, stream, detail);
+        default:
+            return bf16 ? launch<__nv_bfloat16, kPairLayer>(list, n, extra, stream, detail)
+                        : launch<__half, kPairLayer>(list, n, extra, stream, detail);
+    }
 }
 
 // ---- tensor maps ------------------------------------------------------------------------------------

@@ -19,6 +19,49 @@ bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols
 // matrices may have any alignment.
 cudaError_t pair_gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail);
 
+// What the epilogue does with a product, besides Gemm16's own parts.
+enum PairMode : int {
+    kPairLayer = 0,  // bias, activation, residual, pre-activation
+    kPairSave8,      // the same, the pre-activation as an 8-bit checkpoint
+    kPairLogits,     // logits of the head: their sums of exponentials and the labels' values; no output
+    kPairLogitGrad,  // the logits' gradient
+    kPairSum,        // products that add to fp32 sums of earlier ones, and a factor from memory
+};
+struct PairSave8 {
+    int8_t *codes = nullptr;
+    long long ldq = 0;
+    float *scales = nullptr;
+    long long lds = 0;
+};
+// The product's columns are the vocabulary's entries from v0 on.
+struct PairHead {
+    const int64_t *labels = nullptr;
+    int V = 0, v0 = 0;
+    // kPairLogits: of 64 columns' logits of a row, the largest m and the sum of exp(z - m), at
+    // parts[(column / 64) * ld_parts + row]; and the row's logit at its label.
+    float2 *parts = nullptr;
+    long long ld_parts = 0;
+    float *at = nullptr;
+    // kPairLogitGrad
+    const float *lse = nullptr, *dloss = nullptr;
+    long long incd = 0;
+    const float *factor = nullptr;  // multiplies dloss
+};
+// The first product's sums, in the kernel's own order; a piece that is not the last writes no output.
+struct PairSum {
+    float *sums = nullptr;
+    int first = 1, last = 1;
+    const float *factor = nullptr;  // multiplies both products' outputs
+};
+struct PairExtra {
+    PairSave8 save;
+    PairHead head;
+    PairSum sum;
+};
+size_t pair_sum_bytes(int M, int N);
+cudaError_t pair_gemm16_extra_launch(const Gemm16 *list, int n, int mode, const PairExtra &extra,
+                                     cudaStream_t stream, const char **detail);
+
 // The product for few rows of A, streaming B's blocks once over all SMs: up to 64 rows, and more
 // where the 128 x 64 tiles number at most 128. A and B must satisfy tma_rows; K > 0.
 bool stream_gemm16_supports(const Gemm16 &g);

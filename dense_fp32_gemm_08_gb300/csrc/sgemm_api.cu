@@ -2,6 +2,7 @@
 // status reporting. Every compute step runs in the CUDA kernels of this library.
 #include "sgemm.h"
 
+#include <algorithm>
 #include <atomic>
 #include <cstdio>
 #include <cstdlib>
@@ -286,11 +287,77 @@ sgemm_status_t check_layer_limits(int64_t M, int64_t N, int64_t K) {
     return SGEMM_OK;
 }
 
+const uint64_t kStandIn = 0;  // an aligned address
+
+// The two arrays of an 8-bit checkpoint.
+struct Codes8 {
+    const int8_t *Q;
+    int64_t ldq;
+    const float *S;
+    int64_t lds;
+};
+
+sgemm_status_t check_dtype(sgemm_dtype_t dtype) {
+    return dtype == SGEMM_DTYPE_BF16 || dtype == SGEMM_DTYPE_F16 ? SGEMM_OK
+                                                                 : fail(SGEMM_ERR_INVALID_VALUE, "unknown dtype");
+}
+
+// Of an M x N matrix, M and N >= 0.
+sgemm_status_t check_codes(const Codes8 &c, int64_t M, int64_t N) {
+    if (short_ld(c.ldq, N)) return fail(SGEMM_ERR_INVALID_VALUE, "a checkpoint's ldq < max(1, columns)");
+    if (short_ld(c.lds, N / 64 + (N % 64 != 0)))
+        return fail(SGEMM_ERR_INVALID_VALUE, "a checkpoint's lds < max(1, ceil(columns / 64))");
+    if (M > 0 && N > 0 && (!c.Q || !c.S)) return fail(SGEMM_ERR_INVALID_VALUE, "a checkpoint's Q or S is NULL");
+    if (reinterpret_cast<uintptr_t>(c.S) & 3u)
+        return fail(SGEMM_ERR_INVALID_VALUE, "a checkpoint's S is not aligned to its type");
+    return SGEMM_OK;
+}
+
+sg::Checkpoint8 to_checkpoint(const Codes8 &c, sgemm_dtype_t dtype, int64_t M, int64_t N) {
+    sg::Checkpoint8 q;
+    q.dtype = dtype;
+    q.M = static_cast<int>(M);
+    q.N = static_cast<int>(N);
+    q.Q = const_cast<int8_t *>(c.Q);
+    q.ldq = c.ldq;
+    q.S = const_cast<float *>(c.S);
+    q.lds = c.lds;
+    return q;
+}
+
+sgemm_status_t checkpoint8(sgemm_dtype_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx, const Codes8 &c,
+                           bool save, cudaStream_t stream) {
+    sgemm_status_t st = check_dtype(dtype);
+    if (st != SGEMM_OK) return st;
+    if (M < 0 || N < 0) return fail(SGEMM_ERR_INVALID_VALUE, "M and N must be >= 0");
+    if (short_ld(ldx, N)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < max(1, N)");
+    st = check_codes(c, M, N);
+    if (st != SGEMM_OK) return st;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (!X) return fail(SGEMM_ERR_INVALID_VALUE, "X is NULL");
+    if (odd(X)) return fail(SGEMM_ERR_INVALID_VALUE, "X is not aligned to its 2-byte type");
+    st = check_layer_limits(M, N, 0);
+    if (st != SGEMM_OK) return st;
+    sg::Checkpoint8 q = to_checkpoint(c, dtype, M, N);
+    const char *detail = "";
+    cudaError_t err;
+    if (save) {
+        q.X = in16(X);
+        q.ldx = ldx;
+        err = sg::save8_launch(q, stream, &detail);
+    } else {
+        const sg::Restore8 r{q.dtype, q.M, q.N, q.Q, q.ldq, q.S, q.lds, const_cast<uint16_t *>(in16(X)), ldx};
+        err = sg::restore8_launch(r, stream, &detail);
+    }
+    return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
+}
+
 sgemm_status_t linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
                       const void *X, int64_t ldx, const void *W, int64_t ldw, const void *bias,
                       sgemm_activation_t act, const void *R, int64_t ldr, void *Y, int64_t ldy,
-                      void *Z, int64_t ldz, cudaStream_t stream) {
+                      void *Z, int64_t ldz, const Codes8 *saved, cudaStream_t stream) {
     sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
+    if (st == SGEMM_OK && saved) st = check_codes(*saved, M, N);
     if (st != SGEMM_OK) return st;
     if (short_ld(ldx, K)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < max(1, K)");
     if (short_ld(ldw, transw == SGEMM_OP_T ? K : N))
@@ -328,7 +395,11 @@ sgemm_status_t linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t
     g.pre = out16(Z);
     g.ldz = ldz;
     const char *detail = "";
-    const cudaError_t err = sg::gemm16_launch(&g, 1, stream, &detail);
+    cudaError_t err;
+    if (saved)
+        err = sg::gemm16_save8_launch(g, to_checkpoint(*saved, dtype, M, N), stream, &detail);
+    else
+        err = sg::gemm16_launch(&g, 1, stream, &detail);
     return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
 }
 
@@ -336,7 +407,7 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
                                int64_t K, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
                                sgemm_activation_t act, const void *X, int64_t ldx, const void *W,
                                int64_t ldw, void *dX, int64_t lddx, void *dW, int64_t lddw,
-                               float *db, cudaStream_t stream) {
+                               float *db, cudaStream_t stream, bool only_check = false) {
     sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
     if (st != SGEMM_OK) return st;
     const bool t = transw == SGEMM_OP_T;
@@ -361,7 +432,7 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         (reinterpret_cast<uintptr_t>(db) & 3u))
         return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its type");
     st = check_layer_limits(M, N, K);
-    if (st != SGEMM_OK) return st;
+    if (st != SGEMM_OK || only_check) return st;
 
     const char *detail = "";
     const uint16_t *dz = in16(dY);
@@ -432,6 +503,117 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
     return SGEMM_OK;
 }
 
+// A checkpoint restored to scratch: *out and *ld then name an aligned 16-bit matrix.
+cudaError_t restore_to_scratch(const Codes8 &c, sgemm_dtype_t dtype, int64_t M, int64_t N, sg::LayerScratch use,
+                               cudaStream_t stream, const void **out, int64_t *ld, const char **detail) {
+    const sg::Checkpoint8 q = to_checkpoint(c, dtype, M, N);
+    sg::Restore8 r{q.dtype, q.M, q.N, q.Q, q.ldq, q.S, q.lds, nullptr, (N + 7) / 8 * 8};
+    void *p = nullptr;
+    const cudaError_t err = sg::layer_scratch(use, stream, static_cast<size_t>(M) * r.ldx * 2, &p, detail);
+    if (err != cudaSuccess) return err;
+    r.X = static_cast<uint16_t *>(p);
+    *out = p;
+    *ld = r.ldx;
+    return sg::restore8_launch(r, stream, detail);
+}
+
+sgemm_status_t linear_backward8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
+                                const void *dY, int64_t lddy, const Codes8 &z, sgemm_activation_t act,
+                                const Codes8 &x, const void *W, int64_t ldw, void *dX, int64_t lddx, void *dW,
+                                int64_t lddw, float *db, cudaStream_t stream) {
+    sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
+    const bool want_dx = dX && M > 0 && N > 0 && K > 0, want_dw = dW && N > 0 && K > 0;
+    const bool use_z = act != SGEMM_ACT_NONE && (want_dx || want_dw || (db && N > 0)) && M > 0;
+    const bool use_x = want_dw && M > 0;
+    if (st == SGEMM_OK && act != SGEMM_ACT_NONE) st = check_codes(z, use_z ? M : 0, N);
+    if (st == SGEMM_OK && dW) st = check_codes(x, use_x ? M : 0, K);
+    if (st != SGEMM_OK) return st;
+    // The checks of linear_backward on the rest, with nothing queued, come first: a stand-in for what
+    // is restored.
+    const void *X = x.Q ? &kStandIn : nullptr, *Z = z.Q ? &kStandIn : nullptr;
+    int64_t ldx = std::max<int64_t>(1, K), ldz = std::max<int64_t>(1, N);
+    st = linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db,
+                         stream, true);
+    if (st != SGEMM_OK) return st;
+    const char *detail = "";
+    cudaError_t err = cudaSuccess;
+    if (use_x) err = restore_to_scratch(x, dtype, M, K, sg::kScratchRestoreX, stream, &X, &ldx, &detail);
+    if (err == cudaSuccess && use_z)
+        err = restore_to_scratch(z, dtype, M, N, sg::kScratchRestoreZ, stream, &Z, &ldz, &detail);
+    if (err != cudaSuccess) return fail_cuda(detail, err);
+    return linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db,
+                           stream, false);
+}
+
+// Checks what the loss and its gradient share.
+sgemm_status_t check_head(const sg::Head16 &h, sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V,
+                          int64_t D) {
+    const sgemm_status_t st = check_dtype(dtype);
+    if (st != SGEMM_OK) return st;
+    if (transw != SGEMM_OP_N && transw != SGEMM_OP_T)
+        return fail(SGEMM_ERR_INVALID_VALUE, "transw must be SGEMM_OP_N or SGEMM_OP_T");
+    if (T < 0) return fail(SGEMM_ERR_INVALID_VALUE, "T must be >= 0");
+    if (V < 1 || D < 1) return fail(SGEMM_ERR_INVALID_VALUE, "V and D must be >= 1");
+    if (short_ld(h.ldx, D)) return fail(SGEMM_ERR_INVALID_VALUE, "ldx < D");
+    if (short_ld(h.ldw, h.w_dv ? V : D)) return fail(SGEMM_ERR_INVALID_VALUE, h.w_dv ? "ldw < V" : "ldw < D (W transposed)");
+    return SGEMM_OK;
+}
+
+sgemm_status_t check_head_pointers(const sg::Head16 &h) {
+    if (!h.X || !h.W) return fail(SGEMM_ERR_INVALID_VALUE, "X or W is NULL");
+    if (!h.labels) return fail(SGEMM_ERR_INVALID_VALUE, "labels is NULL");
+    auto off = [](const void *p, unsigned mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
+    if (odd(h.X) || odd(h.W) || odd(h.dX) || odd(h.dW) || off(h.labels, 7u) || off(h.loss, 3u) || off(h.lse, 3u) ||
+        off(h.dloss, 3u) || off(h.lse_in, 3u))
+        return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its type");
+    return SGEMM_OK;
+}
+
+sgemm_status_t head(sg::Head16 h, bool gradient, sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V,
+                    int64_t D, cudaStream_t stream) {
+    h.w_dv = transw == SGEMM_OP_N;
+    sgemm_status_t st = check_head(h, dtype, transw, T, V, D);
+    if (st != SGEMM_OK) return st;
+    if (gradient) {
+        if (h.incd < 0) return fail(SGEMM_ERR_INVALID_VALUE, "incd must be >= 0");
+        if (h.dX && short_ld(h.lddx, D)) return fail(SGEMM_ERR_INVALID_VALUE, "lddx < D");
+        if (h.dW && short_ld(h.lddw, h.w_dv ? V : D))
+            return fail(SGEMM_ERR_INVALID_VALUE, h.w_dv ? "lddw < V" : "lddw < D (W transposed)");
+        if (!h.dX && !h.dW) return SGEMM_OK;
+        if (T == 0 && !h.dW) return SGEMM_OK;
+    } else if (T == 0 || (!h.loss && !h.lse)) {
+        return SGEMM_OK;
+    }
+    if (T > 0) {
+        st = check_head_pointers(h);
+        if (st != SGEMM_OK) return st;
+        if (gradient && (!h.dloss || !h.lse_in)) return fail(SGEMM_ERR_INVALID_VALUE, "dloss or lse is NULL");
+        if (h.loss && h.loss == h.lse) return fail(SGEMM_ERR_INVALID_VALUE, "loss and lse are the same array");
+    } else if (odd(h.dW)) {
+        return fail(SGEMM_ERR_INVALID_VALUE, "a pointer is not aligned to its type");
+    }
+    st = check_layer_limits(T, V, D);
+    if (st != SGEMM_OK) return st;
+    h.dtype = static_cast<int>(dtype);
+    h.T = static_cast<int>(T);
+    h.V = static_cast<int>(V);
+    h.D = static_cast<int>(D);
+    const char *detail = "";
+    cudaError_t err;
+    if (T == 0) {  // a gradient without tokens: a product over no k writes zeros
+        sg::Gemm16 g;
+        g.dtype = h.dtype;
+        g.M = h.w_dv ? h.D : h.V;
+        g.N = h.w_dv ? h.V : h.D;
+        g.D = h.dW;
+        g.ldd = h.lddw;
+        err = sg::gemm16_launch(&g, 1, stream, &detail);
+    } else {
+        err = gradient ? sg::head16_grad_launch(h, stream, &detail) : sg::head16_launch(h, stream, &detail);
+    }
+    return err == cudaSuccess ? SGEMM_OK : fail_cuda(detail, err);
+}
+
 sgemm_status_t moe(const sg::Moe16 &m, int64_t T, int64_t E, int64_t topk, int64_t D, int64_t F,
                    cudaStream_t stream) {
     if (m.dtype != SGEMM_DTYPE_BF16 && m.dtype != SGEMM_DTYPE_F16)
@@ -500,7 +682,7 @@ sgemm_status_t sgemm_linear(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, i
                             void *Y, int64_t ldy, void *Z, int64_t ldz, void *stream) {
     return guarded([&] {
         return linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, Z, ldz,
-                      static_cast<cudaStream_t>(stream));
+                      nullptr, static_cast<cudaStream_t>(stream));
     });
 }
 
@@ -513,6 +695,81 @@ sgemm_status_t sgemm_linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int
     return guarded([&] {
         return linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX,
                                lddx, dW, lddw, db, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_checkpoint8(sgemm_dtype_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx, int8_t *Q,
+                                 int64_t ldq, float *S, int64_t lds, void *stream) {
+    return guarded([&] {
+        return checkpoint8(dtype, M, N, X, ldx, {Q, ldq, S, lds}, true, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_restore8(sgemm_dtype_t dtype, int64_t M, int64_t N, const int8_t *Q, int64_t ldq, const float *S,
+                              int64_t lds, void *X, int64_t ldx, void *stream) {
+    return guarded([&] {
+        return checkpoint8(dtype, M, N, X, ldx, {Q, ldq, S, lds}, false, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_linear_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
+                                        const void *X, int64_t ldx, const void *W, int64_t ldw, const void *bias,
+                                        sgemm_activation_t act, const void *R, int64_t ldr, void *Y, int64_t ldy,
+                                        int8_t *Zq, int64_t ldzq, float *Zs, int64_t ldzs, void *stream) {
+    return guarded([&] {
+        const Codes8 saved{Zq, ldzq, Zs, ldzs};
+        return linear(dtype, transw, M, N, K, X, ldx, W, ldw, bias, act, R, ldr, Y, ldy, nullptr, 0, &saved,
+                      static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                                                 int64_t K, const void *dY, int64_t lddy, const int8_t *Zq,
+                                                 int64_t ldzq, const float *Zs, int64_t ldzs, sgemm_activation_t act,
+                                                 const int8_t *Xq, int64_t ldxq, const float *Xs, int64_t ldxs,
+                                                 const void *W, int64_t ldw, void *dX, int64_t lddx, void *dW,
+                                                 int64_t lddw, float *db, void *stream) {
+    return guarded([&] {
+        return linear_backward8(dtype, transw, M, N, K, dY, lddy, {Zq, ldzq, Zs, ldzs}, act, {Xq, ldxq, Xs, ldxs}, W,
+                                ldw, dX, lddx, dW, lddw, db, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
+                                   const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *labels,
+                                   float *loss, float *lse, void *stream) {
+    return guarded([&] {
+        sg::Head16 h;
+        h.X = in16(X);
+        h.ldx = ldx;
+        h.W = in16(W);
+        h.ldw = ldw;
+        h.labels = labels;
+        h.loss = loss;
+        h.lse = lse;
+        return head(h, false, dtype, transw, T, V, D, static_cast<cudaStream_t>(stream));
+    });
+}
+
+sgemm_status_t sgemm_cross_entropy_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
+                                            const float *dloss, int64_t incd, const void *X, int64_t ldx,
+                                            const void *W, int64_t ldw, const int64_t *labels, const float *lse,
+                                            void *dX, int64_t lddx, void *dW, int64_t lddw, void *stream) {
+    return guarded([&] {
+        sg::Head16 h;
+        h.X = in16(X);
+        h.ldx = ldx;
+        h.W = in16(W);
+        h.ldw = ldw;
+        h.labels = labels;
+        h.dloss = dloss;
+        h.incd = incd;
+        h.lse_in = lse;
+        h.dX = out16(dX);
+        h.lddx = lddx;
+        h.dW = out16(dW);
+        h.lddw = lddw;
+        return head(h, true, dtype, transw, T, V, D, static_cast<cudaStream_t>(stream));
     });
 }
 

@@ -364,6 +364,86 @@ sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T,
                          int64_t ldr, void *Y, int64_t ldy, int32_t *topk_index,
                          float *topk_weight, void *stream);
 
+/*
+ * What a training step keeps
+ * --------------------------
+ * Activations in 8 bits for the backward pass (checkpoints), and a vocabulary head's loss without its logits.
+ *
+ * A checkpoint of an M x N matrix of 16-bit values has two arrays: codes Q, M x N int8 (ldq >= max(1, N)), and
+ * scales S, M x ceil(N / 64) fp32 (lds >= max(1, ceil(N / 64))). The values of a row in columns 64 b .. 64 b + 63 share
+ * a scale: with a their largest magnitude,
+ *
+ *     S = a / 127,   Q = 127 x / a rounded to the nearest integer, ties to even,   restored value: Q * S rounded
+ *     to the matrix's type
+ *
+ * so a restored value is within a / 254 (and its rounding) of x, and a itself comes back as it was. A block of zeros
+ * has S = 0; one that holds an infinity or a NaN restores to NaN throughout. Q in rows of a multiple of 16 bytes at a
+ * 16-byte aligned base is read and written fastest; any other is taken too.
+ */
+/* The checkpoint (Q, S) of X (M x N, ldx >= max(1, N)). M == 0 or N == 0 is a no-op. */
+sgemm_status_t sgemm_checkpoint8(sgemm_dtype_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx, int8_t *Q,
+                                 int64_t ldq, float *S, int64_t lds, void *stream);
+
+/* X (M x N, ldx >= max(1, N)) restored from the checkpoint (Q, S). M == 0 or N == 0 is a no-op. */
+sgemm_status_t sgemm_restore8(sgemm_dtype_t dtype, int64_t M, int64_t N, const int8_t *Q, int64_t ldq, const float *S,
+                              int64_t lds, void *X, int64_t ldx, void *stream);
+
+/*
+ * sgemm_linear with the pre-activation kept as a checkpoint (Zq, Zs) of the M x N values that Z would hold there. Y
+ * is computed from the unrounded pre-activation, as there. Neither array may be NULL or overlap another matrix.
+ */
+sgemm_status_t sgemm_linear_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
+                                        const void *X, int64_t ldx, const void *W, int64_t ldw, const void *bias,
+                                        sgemm_activation_t act, const void *R, int64_t ldr, void *Y, int64_t ldy,
+                                        int8_t *Zq, int64_t ldzq, float *Zs, int64_t ldzs, void *stream);
+
+/*
+ * sgemm_linear_backward from checkpoints of X (M x K) and of the pre-activation Z (M x N): its results are those of
+ * sgemm_linear_backward on the restored values. (Zq, Zs) are read unless act is none, (Xq, Xs) only for dW (NULL
+ * otherwise).
+ */
+sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
+                                                 int64_t K, const void *dY, int64_t lddy, const int8_t *Zq,
+                                                 int64_t ldzq, const float *Zs, int64_t ldzs, sgemm_activation_t act,
+                                                 const int8_t *Xq, int64_t ldxq, const float *Xs, int64_t ldxs,
+                                                 const void *W, int64_t ldw, void *dX, int64_t lddx, void *dW,
+                                                 int64_t lddw, float *db, void *stream);
+
+/*
+ * Softmax cross entropy of a vocabulary head, without keeping its logits:
+ *
+ *     z = X . op(W),   lse[t] = log(sum over v of exp(z[t, v])),   loss[t] = lse[t] - z[t, labels[t]]
+ *
+ *   T tokens, V >= 1 entries of the vocabulary, D >= 1 model width.   X  T x D, ldx >= D.
+ *   W       SGEMM_OP_T: V x D, ldw >= D. SGEMM_OP_N: D x V, ldw >= V.
+ *   labels  T int64 values. A token whose label is outside [0, V) (such as -100) does not count: its loss is 0.
+ *   loss, lse  T fp32 values each; either may be NULL (not computed). lse is what the gradient reads.
+ * T == 0 is a no-op. Sums are fp32, in an order that does not depend on timing. A logit of minus infinity has
+ * probability 0; a logit of plus infinity or NaN makes its token's lse and loss NaN.
+ */
+sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
+                                   const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *labels,
+                                   float *loss, float *lse, void *stream);
+
+/*
+ * Its gradients, from dloss[t * incd] = dLoss / dloss[t] (incd >= 0; 0: one value for every token) and the forward
+ * pass's lse:
+ *
+ *     dz[t, v] = dloss[t] * (exp(z[t, v] - lse[t]) - (v == labels[t])),  0 for tokens that do not count
+ *     dX = dz . op(W)^T (T x D, lddx >= D),   dW = X^T . dz in W's layout (lddw as ldw)
+ *
+ * dX and dW may each be NULL (not computed). With T == 0, dW is set to zero. The logits are computed again, a piece
+ * of the vocabulary at a time; a piece's dz lives in a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
+ * sums over the pieces in another of 4 * T' * D' (T and D rounded up to multiples of 256). The products read dz in the
+ * call's dtype, in half times a power of two that brings the largest counted |dloss| to 2^14 and that the outputs are
+ * divided by again. X of a token that does not count is multiplied by 0 for dW, so it must be finite. Outputs must
+ * not overlap inputs or each other.
+ */
+sgemm_status_t sgemm_cross_entropy_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
+                                            const float *dloss, int64_t incd, const void *X, int64_t ldx,
+                                            const void *W, int64_t ldw, const int64_t *labels, const float *lse,
+                                            void *dX, int64_t lddx, void *dW, int64_t lddw, void *stream);
+
 /* Static text for a status code (never NULL). */
 const char *sgemm_status_string(sgemm_status_t status);
 
