@@ -337,13 +337,16 @@ def _side_stream(torch, device, queue):
     return torch.cuda.ExternalStream(queue, device=device)
 
 
-def _empty(torch, side, shape, dtype, device):
+def _empty(torch, side, shape, dtype, device, ld=None):
     """An output. On a side stream its memory comes from that stream's pool, so that no pending work
-    of the current stream still uses it, and is kept while the current stream may use it."""
+    of the current stream still uses it, and is kept while the current stream may use it. With `ld` its
+    rows are that far apart."""
     if side is None:
+        if ld is not None:
+            return torch.empty_strided(shape, (ld, 1), dtype=dtype, device=device)
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(side):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = _empty(torch, None, shape, dtype, device, ld)
     t.record_stream(torch.cuda.current_stream(device))
     return t
 
@@ -598,14 +601,11 @@ class Checkpoint8(NamedTuple):
 
 
 def _new_checkpoint(torch, side, rows, cols, dtype, device):
-    """Codes in rows of whole 16 bytes."""
-    codes = _empty(torch, side, (rows, -(-cols // 16) * 16), torch.int8, device)[:, :cols]
-    return Checkpoint8(codes, _empty(torch, side, (rows, -(-cols // 64)), torch.float32, device), dtype)
-
-
-def _saved(c):
-    """(codes, ldq, scale, lds) of a checkpoint made by ``_new_checkpoint``."""
-    return (c.codes.data_ptr(), max(c.codes.stride(0), 1), c.scale.data_ptr(), max(c.scale.shape[1], 1))
+    """A checkpoint with codes in rows of whole 16 bytes, and its (codes, ldq, scale, lds)."""
+    ldq, blocks = (cols + 15) // 16 * 16 or 1, (cols + 63) // 64
+    codes = _empty(torch, side, (rows, cols), torch.int8, device, ldq)
+    scale = _empty(torch, side, (rows, blocks), torch.float32, device)
+    return Checkpoint8(codes, scale, dtype), (codes.data_ptr(), ldq, scale.data_ptr(), blocks or 1)
 
 
 def _codes(c, rows, cols, dtype, device, what):
@@ -637,10 +637,10 @@ def checkpoint8(x, stream=None):
     M, N = x.shape
     px, ldx = _matrix(x, M, N, dtype, device, "x")
     queue, side = _queue(torch, device, stream)
-    c = _new_checkpoint(torch, side, M, N, dtype, device)
+    c, saved = _new_checkpoint(torch, side, M, N, dtype, device)
     if side is not None:
         _in_use(side, x)
-    status = (_lib or lib()).sgemm_checkpoint8(code, M, N, px, max(ldx, 1), *_saved(c), queue)
+    status = (_lib or lib()).sgemm_checkpoint8(code, M, N, px, ldx, *saved, queue)
     if status:
         _check(status)
     return c
@@ -693,7 +693,7 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
         out, ldy = _empty(torch, side, (M, N), dtype, device), max(N, 1)
         py = out.data_ptr()
     if save_pre == "8bit":
-        pre = _new_checkpoint(torch, side, M, N, dtype, device)
+        pre, saved = _new_checkpoint(torch, side, M, N, dtype, device)
     elif save_pre:
         pre = _empty(torch, side, (M, N), dtype, device)
         pz = pre.data_ptr()
@@ -701,7 +701,7 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
         _in_use(side, x, weight, bias, residual, out)
     if save_pre == "8bit":
         status = (_lib or lib()).sgemm_linear_checkpoint8(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act),
-                                                          pr, ldr, py, ldy, *_saved(pre), queue)
+                                                          pr, ldr, py, ldy, *saved, queue)
         if status:
             _check(status)
         return out, pre

@@ -13,29 +13,85 @@ namespace sg {
 
 constexpr int kCheckpointBlock = 64;
 
-// The codes of a block whose largest magnitude is `a` (of the type T's values).
-struct Coder8 {
-    float scale;  // what is stored
-    float top;    // a, or what keeps the codes of a block without a magnitude at 0
-    float c;      // keeps 127 x finite
-    bool finite;
-    __device__ __forceinline__ explicit Coder8(float a) {
-        finite = a < __int_as_float(0x7f800000);  // false for NaN
-        scale = finite ? __fdiv_rn(a, 127.0f) : __int_as_float(0x7fc00000);
-        c = a > 1e30f ? 0.0009765625f : 1.0f;
-        top = finite && a > 0.0f ? a * c : 1.0f;
+// The largest magnitude among 16-bit values, as bits without the sign: they order as integers, with
+// infinity and then NaN above every finite value. `acc` holds two candidates, `w` two values.
+template <typename T>
+__device__ __forceinline__ uint32_t magnitude2(uint32_t acc, uint32_t w) {
+    w &= 0x7FFF7FFFu;
+    if constexpr (Half16<T>::kind == kBf16) {
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&acc),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&w));
+        return *reinterpret_cast<const uint32_t *>(&m);
+    } else {
+        const __half2 m = __hmax2_nan(*reinterpret_cast<const __half2 *>(&acc), *reinterpret_cast<const __half2 *>(&w));
+        return *reinterpret_cast<const uint32_t *>(&m);
     }
-    // The code's two's complement in the low 8 bits. 127 x has at most 18 significant bits, so it is exact,
-    // and the quotient's rounding moves no value onto or over a tie: 127 x / a is (k + 1/2) exactly or
-    // differs from it by at least 2^-21, which exceeds its fp32 rounding error where |q| < 128 asks for it.
-    __device__ __forceinline__ uint32_t code(float x) const {
-        const float q = finite ? __fdiv_rn(x * c * 127.0f, top) : 0.0f;
-        return __float_as_uint(q + 12582912.0f) & 0xFFu;  // 1.5 2^23: the integer in the low bits
+}
+__device__ __forceinline__ uint32_t magnitude(uint32_t acc) { return max(acc & 0xFFFFu, acc >> 16); }
+
+template <typename T>
+__device__ __forceinline__ bool is_finite(uint32_t magnitude_bits) {
+    return magnitude_bits < (Half16<T>::kind == kBf16 ? 0x7F80u : 0x7C00u);
+}
+// What is stored for a block whose largest magnitude has the bits `top`.
+template <typename T>
+__device__ __forceinline__ float scale8(uint32_t top) {
+    return is_finite<T>(top) ? __fdiv_rn(Half16<T>::widen(static_cast<uint16_t>(top)), 127.0f)
+                             : __int_as_float(0x7fc00000);
+}
+
+// The codes of such a block, from its inverse 127 / a in two fp32 parts. x (hi + lo) is then within 2^-36 of the
+// quotient, and its one rounding to fp32 moves no value onto or over a tie: with x in [a 2^-s-1, a 2^-s] the
+// quotient is (k + 1/2) exactly, which fp32 holds, or differs from it by at least 2^-12-s (both have at most 11
+// significant bits), 16 times its fp32 spacing. (A product with a rounded inverse is off at ties, which are
+// not rare: every 300th normal bfloat16 value is one.)
+template <typename T>
+struct Coder8 {
+    float hi, lo, lift;
+    bool finite;
+    __device__ __forceinline__ explicit Coder8(uint32_t top) {
+        float a = Half16<T>::widen(static_cast<uint16_t>(top));
+        finite = is_finite<T>(top);
+        // 127 / a could overflow, or leave the range of the approximate division
+        lift = a < 1e-30f ? 18446744073709551616.0f : a > 1e30f ? 5.42101086e-20f : 1.0f;  // 2^64, 2^-64
+        a *= lift;
+        hi = __fdividef(127.0f, a);
+        lo = __fdividef(fmaf(-hi, a, 127.0f), a);
+        if (!(a > 0.0f)) hi = lo = 0.0f;
+    }
+    // Eight codes, two's complement, lowest byte first.
+    __device__ __forceinline__ uint2 eight(const uint32_t (&w)[4]) const {
+        uint32_t bits[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f = Half16<T>::widen2(w[i]);
+            if (lift != 1.0f) {
+                f.x *= lift;
+                f.y *= lift;
+            }
+            // 1.5 2^23: the sum's low bits are the nearest integer, ties to even
+            bits[2 * i] = __float_as_uint(fmaf(f.x, hi, f.x * lo) + 12582912.0f);
+            bits[2 * i + 1] = __float_as_uint(fmaf(f.y, hi, f.y * lo) + 12582912.0f);
+        }
+        auto four = [](const uint32_t *b) {
+            return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+        };
+        return finite ? make_uint2(four(bits), four(bits + 4)) : make_uint2(0, 0);
     }
 };
 
-__device__ __forceinline__ float decode8(uint32_t byte, float scale) {
-    return static_cast<float>(static_cast<int8_t>(byte)) * scale;
+// The value of code k (0..3) of a word, times the scale. (The bytes, made unsigned, become the low bits of
+// 2^23 + byte; the difference is exact.)
+template <int K>
+__device__ __forceinline__ float decode8(uint32_t word_biased, float scale) {
+    return (__uint_as_float(__byte_perm(word_biased, 0x4B000000u, 0x7540 + K)) - 8388736.0f) * scale;
+}
+// The restored values of four codes, in 16 bits.
+template <typename T>
+__device__ __forceinline__ uint2 restore4(uint32_t word, float s0, float s1, float s2, float s3) {
+    const uint32_t b = word ^ 0x80808080u;
+    return make_uint2(Half16<T>::narrow2(decode8<0>(b, s0), decode8<1>(b, s1)),
+                      Half16<T>::narrow2(decode8<2>(b, s2), decode8<3>(b, s3)));
 }
 
 }  // namespace sg
