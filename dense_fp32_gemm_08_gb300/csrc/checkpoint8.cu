@@ -1,8 +1,9 @@
 // checkpoint8.cu: 16-bit matrices to 8-bit checkpoints and back (checkpoint8.cuh has the form).
 //
-// Bound by memory: 2 + 1.06 bytes a value each way. A lane has 8 consecutive columns of a row, so that a
-// block's maximum is three exchanges among 8 lanes; 8 to 32 lanes share a row, and a warp has several rows under
-// way, so that its loads are out before the first is used.
+// Bound by memory: 2 + 1.06 bytes a value each way (16384 x 14336 bf16: saved in 108 us, 6.5 TB/s; restored in
+// 103 us, 6.9 TB/s). Saving is near the issue rate too: a lane has 16 consecutive columns of a row, so that a
+// block's maximum is two exchanges among 4 lanes and what a block costs besides its values is paid by 16 of them
+// (with 8 columns: 137 us). Several rows are under way per lane, so that its loads are out before the first is used.
 #include "checkpoint8.cuh"
 #include "layer16.cuh"
 
@@ -11,136 +12,159 @@
 namespace sg {
 namespace {
 
-constexpr int kRowsInFlight = 4;
+// Rows under way per lane. (16384 x 14336 saved with 2, 3, 4 at their best occupancy: 121, 111, 108 us, restored:
+// 107, 103, 103 us. 4095 x 3001 in unaligned rows, saved: 11.3, 13.0, 12.7 us.)
+__host__ __device__ constexpr int save_rows(bool vec) { return vec ? 4 : 2; }
+constexpr int kRestoreRows = 4;
 
-// Lanes per row (8, 16 or 32) and the warps' tasks: 256 columns or less of kRowsInFlight steps of rows.
+// A row's chunks of 16 (saving) or 8 columns over lanes (4, 8, 16 or 32 to a row), groups of 32 lanes over warps. A CTA's eight
+// warps cover `wide` neighbouring groups (a power of two) of 8 / wide row tasks; a row task is
+// 4 steps of 32 / lanes rows. (Powers of two: a division per task cost as much as its rows.)
 struct Split8 {
-    int lanes, groups;  // groups: of 8 * lanes columns, per row
-    long long row_tasks;
-    __host__ __device__ int rows() const { return 32 / lanes * kRowsInFlight; }
+    int lane_bits, wide_bits, groups, row_tasks;
+    dim3 grid() const {
+        return dim3(static_cast<unsigned>((groups + (1 << wide_bits) - 1) >> wide_bits),
+                    static_cast<unsigned>(std::min((row_tasks + (8LL >> wide_bits) - 1) >> (3 - wide_bits), 65535LL)));
+    }
 };
-Split8 split8(int M, long long chunks) {
+Split8 split8(int M, long long chunks, int rows) {
     Split8 s;
-    s.lanes = chunks <= 8 ? 8 : chunks <= 16 ? 16 : 32;
-    s.groups = static_cast<int>((chunks + s.lanes - 1) / s.lanes);
-    s.row_tasks = (M + s.rows() - 1LL) / s.rows();
+    s.lane_bits = chunks <= 4 ? 2 : chunks <= 8 ? 3 : chunks <= 16 ? 4 : 5;
+    s.groups = static_cast<int>((chunks + (1 << s.lane_bits) - 1) >> s.lane_bits);
+    s.wide_bits = s.groups > 4 ? 3 : s.groups > 2 ? 2 : s.groups > 1 ? 1 : 0;
+    s.row_tasks = static_cast<int>((M + (32LL >> s.lane_bits) * rows - 1) / ((32 >> s.lane_bits) * rows));
     return s;
 }
-long long blocks8(const Split8 &s) { return (s.row_tasks * s.groups + 7) / 8; }
+// This warp's group and first row task, and how far apart its row tasks are.
+struct Tasks8 {
+    int group, task, apart;
+    __device__ __forceinline__ explicit Tasks8(const Split8 &s) {
+        const int warp = threadIdx.x >> 5;
+        group = (blockIdx.x << s.wide_bits) + (warp & ((1 << s.wide_bits) - 1));
+        task = (blockIdx.y << (3 - s.wide_bits)) + (warp >> s.wide_bits);
+        apart = gridDim.y << (3 - s.wide_bits);
+    }
+};
 
-// VEC: X allows 16-byte loads (and N is a multiple of 8).
+// How many of the rows row0 + i * step, i < ROWS, exist.
+template <int ROWS>
+__device__ __forceinline__ int rows_left(int M, int row0, int step) {
+    const long long left = static_cast<long long>(M) - row0;
+    int rows = 0;
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) rows += static_cast<long long>(i) * step < left;
+    return rows;
+}
+
+// VEC: X allows 16-byte loads (and N is a multiple of 8). A lane has 16 columns of a row, four lanes a block.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 5) save8_kernel(const Checkpoint8 c, const Split8 split, int q_vec) {
-    grid_dependents();
-    grid_dependency();
-    const int lane = threadIdx.x & 31;
-    const long long task = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    if (task >= split.row_tasks * split.groups) return;
-    const long long row_task = task / split.groups;
-    const int group = static_cast<int>(task - row_task * split.groups);
-    const int step = 32 / split.lanes;
-    const long long row0 = row_task * split.rows() + lane / split.lanes;
-    const long long col = 8LL * (group * split.lanes + lane % split.lanes);
-    const int count = static_cast<int>(max(0LL, min(8LL, c.N - col)));
-    // Rows row0 + i * step with i < rows exist.
-    const int rows = static_cast<int>(min(static_cast<long long>(kRowsInFlight), (c.M - row0 + step - 1) / step));
+__device__ __forceinline__ void save8_rows(const Checkpoint8 &c, int lane, int row0, long long col, int step,
+                                           bool q_vec) {
+    constexpr int ROWS = save_rows(VEC);
+    const int count = static_cast<int>(max(0LL, min(16LL, c.N - col)));
+    const int rows = rows_left<ROWS>(c.M, row0, step);
     constexpr int W = VEC ? 4 : 5;
-    uint32_t raw[kRowsInFlight][W], top[kRowsInFlight];
-    const uint16_t *src = c.X + row0 * c.ldx + col;
+    uint32_t raw[ROWS][2][W], top[ROWS];
+    const uint16_t *src = c.X + static_cast<long long>(row0) * c.ldx + col;
     const long long src_step = step * c.ldx;
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
+    for (int i = 0; i < ROWS; ++i)
 #pragma unroll
-        for (int k = 0; k < W; ++k) raw[i][k] = 0;
-        if (i < rows && count > 0) {
-            if constexpr (VEC) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src + i * src_step));
-                raw[i][0] = q.x;
-                raw[i][1] = q.y;
-                raw[i][2] = q.z;
-                raw[i][3] = q.w;
-            } else {
-                load8_words(raw[i], src + i * src_step, count);
-            }
-        }
-    }
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
-        if constexpr (!VEC) {
-            const uint4 q = align8(raw[i], src + i * src_step);
-            raw[i][0] = q.x;
-            raw[i][1] = q.y;
-            raw[i][2] = q.z;
-            raw[i][3] = q.w;
-            if (count < 8) {  // what follows the row is not part of it
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (2 * k >= count) raw[i][k] = 0;
-                    if (2 * k + 1 == count) raw[i][k] &= 0xFFFFu;
+            for (int k = 0; k < W; ++k) raw[i][h][k] = 0;
+            if (i < rows && count > 8 * h) {
+                const uint16_t *p = src + i * src_step + 8 * h;
+                if constexpr (VEC) {
+                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(p));
+                    raw[i][h][0] = q.x;
+                    raw[i][h][1] = q.y;
+                    raw[i][h][2] = q.z;
+                    raw[i][h][3] = q.w;
+                } else {
+                    load8_words(raw[i][h], p, min(8, count - 8 * h));
                 }
             }
         }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
         top[i] = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top[i] = magnitude2<T>(top[i], raw[i][k]);
+        for (int h = 0; h < 2; ++h) {
+            if constexpr (!VEC) {
+                const uint4 q = align8(raw[i][h], src + i * src_step + 8 * h);
+                raw[i][h][0] = q.x;
+                raw[i][h][1] = q.y;
+                raw[i][h][2] = q.z;
+                raw[i][h][3] = q.w;
+                if (count < 8 * h + 8) {  // what follows the row is not part of it
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (8 * h + 2 * k >= count) raw[i][h][k] = 0;
+                        if (8 * h + 2 * k + 1 == count) raw[i][h][k] &= 0xFFFFu;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top[i] = magnitude2<T>(top[i], raw[i][h][k]);
+        }
         top[i] = magnitude(top[i]);
 #pragma unroll
-        for (int s = 1; s < 8; s *= 2) top[i] = max(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], s));
+        for (int s = 1; s < 4; s *= 2) top[i] = max(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], s));
     }
-    // Lane i of a block's eight has the scale of row i.
-    const int mine = lane & 7;
+    // Lane i of a block's four has the scale of row i.
+    const int mine = lane & 3;
     if (mine < rows && col / kCheckpointBlock * kCheckpointBlock < c.N) {
         uint32_t bits = top[0];
 #pragma unroll
-        for (int i = 1; i < kRowsInFlight; ++i) bits = mine == i ? top[i] : bits;
-        c.S[(row0 + mine * step) * c.lds + col / kCheckpointBlock] = scale8<T>(bits);
+        for (int i = 1; i < ROWS; ++i) bits = mine == i ? top[i] : bits;
+        c.S[(static_cast<long long>(row0) + mine * step) * c.lds + col / kCheckpointBlock] = scale8<T>(bits);
     }
     if (count <= 0) return;
-    int8_t *q = c.Q + row0 * c.ldq + col;
+    int8_t *q = c.Q + static_cast<long long>(row0) * c.ldq + col;
     const long long q_step = step * c.ldq;
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
         if (i >= rows) break;
-        const uint32_t w[4] = {raw[i][0], raw[i][1], raw[i][2], raw[i][3]};
-        const uint2 codes = Coder8<T>(top[i]).eight(w);
-        if (count == 8 && q_vec) {
-            *reinterpret_cast<uint2 *>(q + i * q_step) = codes;
+        const Coder8<T> coder(top[i]);
+        uint2 codes[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t w[4] = {raw[i][h][0], raw[i][h][1], raw[i][h][2], raw[i][h][3]};
+            codes[h] = coder.eight(w);
+        }
+        if (count == 16 && q_vec) {
+            *reinterpret_cast<uint4 *>(q + i * q_step) = make_uint4(codes[0].x, codes[0].y, codes[1].x, codes[1].y);
         } else {
-            const uint64_t both = static_cast<uint64_t>(codes.y) << 32 | codes.x;
-            for (int k = 0; k < count; ++k) q[i * q_step + k] = static_cast<int8_t>(both >> (8 * k));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint64_t both = static_cast<uint64_t>(codes[h].y) << 32 | codes[h].x;
+                for (int k = 0; k < min(8, count - 8 * h); ++k)
+                    q[i * q_step + 8 * h + k] = static_cast<int8_t>(both >> (8 * k));
+            }
         }
     }
 }
 
 // Aligned rows: X as VEC above, the codes in 8-byte words.
 template <typename T>
-__global__ void __launch_bounds__(256) restore8_aligned_kernel(const Restore8 c, const Split8 split) {
-    grid_dependents();
-    grid_dependency();
-    const int lane = threadIdx.x & 31;
-    const long long task = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    if (task >= split.row_tasks * split.groups) return;
-    const long long row_task = task / split.groups;
-    const int group = static_cast<int>(task - row_task * split.groups);
-    const int step = 32 / split.lanes;
-    const long long row0 = row_task * split.rows() + lane / split.lanes;
-    const long long col = 8LL * (group * split.lanes + lane % split.lanes);
+__device__ __forceinline__ void restore8_aligned_rows(const Restore8 &c, int row0, long long col, int step) {
     if (col >= c.N || row0 >= c.M) return;
-    const int rows = static_cast<int>(min(static_cast<long long>(kRowsInFlight), (c.M - row0 + step - 1) / step));
-    const int8_t *q = c.Q + row0 * c.ldq + col;
-    const float *s = c.S + row0 * c.lds + col / kCheckpointBlock;
-    uint16_t *x = c.X + row0 * c.ldx + col;
+    const int rows = rows_left<kRestoreRows>(c.M, row0, step);
+    const int8_t *q = c.Q + static_cast<long long>(row0) * c.ldq + col;
+    const float *s = c.S + static_cast<long long>(row0) * c.lds + col / kCheckpointBlock;
+    uint16_t *x = c.X + static_cast<long long>(row0) * c.ldx + col;
     const long long q_step = step * c.ldq, s_step = step * c.lds, x_step = step * c.ldx;
-    uint2 codes[kRowsInFlight];
-    float scale[kRowsInFlight];
+    uint2 codes[kRestoreRows];
+    float scale[kRestoreRows];
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i)
+    for (int i = 0; i < kRestoreRows; ++i)
         if (i < rows) {
             codes[i] = __ldg(reinterpret_cast<const uint2 *>(q + i * q_step));
             scale[i] = __ldg(s + i * s_step);
         }
 #pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i)
+    for (int i = 0; i < kRestoreRows; ++i)
         if (i < rows) {
             const uint2 a = restore4<T>(codes[i].x, scale[i], scale[i], scale[i], scale[i]);
             const uint2 b = restore4<T>(codes[i].y, scale[i], scale[i], scale[i], scale[i]);
@@ -149,91 +173,107 @@ __global__ void __launch_bounds__(256) restore8_aligned_kernel(const Restore8 c,
 }
 
 // The output decides the alignment: a lane writes 16 aligned bytes of a row, and reads the codes of those
-// columns, at any address, from the aligned 8-byte words that hold them. A row's first and last values are
-// written one by one where they do not fill 16 bytes.
+// columns, at any address, from the aligned 8-byte words that hold them. A row's first and last values, where
+// they do not fill 16 bytes, go one by one.
 template <typename T>
+__device__ __forceinline__ void restore8_any_rows(const Restore8 &c, int row0, long long chunk, int step) {
+    uint2 raw[kRestoreRows][2];
+    float scale[kRestoreRows][2];
+    const int rows = rows_left<kRestoreRows>(c.M, row0, step);
+    const int8_t *q = c.Q + static_cast<long long>(row0) * c.ldq;
+    const float *s = c.S + static_cast<long long>(row0) * c.lds;
+    uint16_t *x = c.X + static_cast<long long>(row0) * c.ldx;
+    const long long q_step = step * c.ldq, s_step = step * c.lds, x_step = step * c.ldx;
+    auto first_col = [&](int i) {
+        return static_cast<int>(min(chunk, 0x7ffffff0LL)) - (static_cast<int>(reinterpret_cast<uintptr_t>(x + i * x_step) >> 1) & 7);
+    };
+#pragma unroll
+    for (int i = 0; i < kRestoreRows; ++i) {
+        const int col = first_col(i);
+        if (i >= rows || col < 0 || col > c.N - 8) continue;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(q + i * q_step + col);
+        const uint2 *word = reinterpret_cast<const uint2 *>(at & ~static_cast<uintptr_t>(7));
+        raw[i][0] = __ldg(word);
+        if (at & 7) raw[i][1] = __ldg(word + 1);
+        scale[i][0] = __ldg(s + i * s_step + col / kCheckpointBlock);
+        scale[i][1] = __ldg(s + i * s_step + (col + 7) / kCheckpointBlock);
+    }
+#pragma unroll
+    for (int i = 0; i < kRestoreRows; ++i) {
+        if (i >= rows) break;
+        const int col = first_col(i);
+        if (col >= 0 && col <= c.N - 8) {
+            const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q + i * q_step + col));
+            const uint32_t w0 = at & 4 ? raw[i][0].y : raw[i][0].x, w1 = at & 4 ? raw[i][1].x : raw[i][0].y;
+            const uint32_t w2 = at & 4 ? raw[i][1].y : raw[i][1].x;
+            const uint32_t lo = __funnelshift_r(w0, w1, 8 * (at & 3)), hi = __funnelshift_r(w1, w2, 8 * (at & 3));
+            const int border = kCheckpointBlock - (col & (kCheckpointBlock - 1));  // columns of the first scale
+            auto of = [&](int k) { return k < border ? scale[i][0] : scale[i][1]; };
+            const uint2 a = restore4<T>(lo, of(0), of(1), of(2), of(3)), b = restore4<T>(hi, of(4), of(5), of(6), of(7));
+            *reinterpret_cast<uint4 *>(x + i * x_step + col) = make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            for (int k = max(0, -col); k < min(8, c.N - col); ++k) {
+                const uint32_t code = static_cast<uint8_t>(q[i * q_step + col + k]);
+                const float v = s[i * s_step + (col + k) / kCheckpointBlock];
+                x[i * x_step + col + k] = static_cast<uint16_t>(restore4<T>(code, v, v, v, v).x);
+            }
+        }
+    }
+}
+
+// Calls body(lane, first row, chunk's first column, rows between a task's rows) for the warp's tasks. Row
+// tasks past the last row keep their lanes together; their rows are left out by count.
+template <int COLS, int ROWS, typename Body>
+__device__ __forceinline__ void for_tasks(const Split8 &split, Body body) {
+    const Tasks8 mine(split);
+    if (mine.group >= split.groups) return;
+    const int lane = threadIdx.x & 31, step = 32 >> split.lane_bits;
+    const long long col = static_cast<long long>(COLS) * ((static_cast<long long>(mine.group) << split.lane_bits) + (lane & ((1 << split.lane_bits) - 1)));
+    for (long long task = mine.task; task < split.row_tasks; task += mine.apart) {
+        const long long row0 = task * ROWS * step + (lane >> split.lane_bits);
+        body(lane, static_cast<int>(min(row0, 0x7fffffffLL)), col, step);
+    }
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256, VEC ? 4 : 5) save8_kernel(const Checkpoint8 c, const Split8 split, int q_vec) {
+    grid_dependents();
+    grid_dependency();
+    for_tasks<16, save_rows(VEC)>(split, [&](int lane, int row0, long long col, int step) {
+        save8_rows<T, VEC>(c, lane, row0, col, step, q_vec != 0);
+    });
+}
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) restore8_kernel(const Restore8 c, const Split8 split) {
     grid_dependents();
     grid_dependency();
-    const int lane = threadIdx.x & 31;
-    const long long task = blockIdx.x * 8LL + (threadIdx.x >> 5);
-    if (task >= split.row_tasks * split.groups) return;
-    const long long row_task = task / split.groups;
-    const int group = static_cast<int>(task - row_task * split.groups);
-    const int step = 32 / split.lanes;
-    const long long row0 = row_task * split.rows() + lane / split.lanes;
-    const long long chunk = 8LL * (group * split.lanes + lane % split.lanes);
-    uint64_t raw[kRowsInFlight][2];
-    float scale[kRowsInFlight][2];
-#pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
-        const long long row = row0 + i * step;
-        raw[i][0] = raw[i][1] = 0;
-        scale[i][0] = scale[i][1] = 0.0f;
-        if (row >= c.M) continue;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(c.X + row * c.ldx) >> 1) & 7;
-        const long long first = max(0LL, chunk - shift), last = min(static_cast<long long>(c.N), chunk - shift + 8) - 1;
-        if (first > last) continue;
-        // Bytes first .. last lie in one or two aligned words.
-        const uintptr_t at = reinterpret_cast<uintptr_t>(c.Q + row * c.ldq) + (chunk - shift);
-        const uintptr_t word = at & ~static_cast<uintptr_t>(7);
-        const uintptr_t lo = reinterpret_cast<uintptr_t>(c.Q + row * c.ldq + first);
-        const uintptr_t hi = reinterpret_cast<uintptr_t>(c.Q + row * c.ldq + last);
-        if (lo < word + 8) raw[i][0] = __ldg(reinterpret_cast<const unsigned long long *>(word));
-        if (hi >= word + 8) raw[i][1] = __ldg(reinterpret_cast<const unsigned long long *>(word) + 1);
-        const float *s = c.S + row * c.lds;
-        scale[i][0] = __ldg(s + first / kCheckpointBlock);
-        scale[i][1] = first / kCheckpointBlock == last / kCheckpointBlock ? scale[i][0] : __ldg(s + last / kCheckpointBlock);
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsInFlight; ++i) {
-        const long long row = row0 + i * step;
-        if (row >= c.M) continue;
-        const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(c.X + row * c.ldx) >> 1) & 7;
-        const long long col = chunk - shift;
-        if (col >= c.N || col + 8 <= 0) continue;
-        const int bytes = static_cast<int>(reinterpret_cast<uintptr_t>(c.Q + row * c.ldq) + col) & 7;
-        const uint64_t both = bytes ? raw[i][0] >> (8 * bytes) | raw[i][1] << (64 - 8 * bytes) : raw[i][0];
-        // Columns below `border` have the first scale.
-        const int border = static_cast<int>((max(0LL, col) / kCheckpointBlock + 1) * kCheckpointBlock - col);
-        auto of = [&](int k) { return k < border ? scale[i][0] : scale[i][1]; };
-        const uint2 a = restore4<T>(static_cast<uint32_t>(both), of(0), of(1), of(2), of(3));
-        const uint2 b = restore4<T>(static_cast<uint32_t>(both >> 32), of(4), of(5), of(6), of(7));
-        uint16_t *x = c.X + row * c.ldx + col;
-        if (col >= 0 && col + 8 <= c.N) {
-            *reinterpret_cast<uint4 *>(x) = make_uint4(a.x, a.y, b.x, b.y);
-        } else {
-            const uint32_t v[4] = {a.x, a.y, b.x, b.y};
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (col + k >= 0 && col + k < c.N) x[k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
-        }
-    }
+    for_tasks<8, kRestoreRows>(split, [&](int, int row0, long long col, int step) {
+        if constexpr (VEC)
+            restore8_aligned_rows<T>(c, row0, col, step);
+        else
+            restore8_any_rows<T>(c, row0, col, step);
+    });
 }
 
 }  // namespace
 
 cudaError_t save8_launch(const Checkpoint8 &c, cudaStream_t stream, const char **detail) {
-    const Split8 split = split8(c.M, (c.N + 7LL) / 8);
     const bool vec = tma_rows(c.X, c.ldx) && c.N % 8 == 0;
-    const int q_vec = (reinterpret_cast<uintptr_t>(c.Q) & 7u) == 0 && c.ldq % 8 == 0;
+    const Split8 split = split8(c.M, (c.N + 15LL) / 16, save_rows(vec));
+    const int q_vec = (reinterpret_cast<uintptr_t>(c.Q) & 15u) == 0 && c.ldq % 16 == 0;
     auto kernel = c.dtype == kBf16 ? (vec ? save8_kernel<__nv_bfloat16, true> : save8_kernel<__nv_bfloat16, false>)
                                    : (vec ? save8_kernel<__half, true> : save8_kernel<__half, false>);
-    const cudaError_t err = blocks8(split) > 0x7fffffffLL
-                                ? cudaErrorInvalidValue
-                                : launch_early(kernel, dim3(static_cast<unsigned>(blocks8(split))), 256, 0, stream, c, split, q_vec);
+    const cudaError_t err = launch_early(kernel, split.grid(), 256, 0, stream, c, split, q_vec);
     if (err != cudaSuccess) *detail = "checkpoint kernel launch failed";
     return err;
 }
 
 cudaError_t restore8_launch(const Restore8 &c, cudaStream_t stream, const char **detail) {
     const bool vec = tma_rows(c.X, c.ldx) && c.N % 8 == 0 && (reinterpret_cast<uintptr_t>(c.Q) & 7u) == 0 && c.ldq % 8 == 0;
-    const Split8 split = split8(c.M, (c.N + (vec ? 7LL : 14LL)) / 8);  // a row may begin inside its first 16 bytes
-    auto kernel = c.dtype == kBf16 ? (vec ? restore8_aligned_kernel<__nv_bfloat16> : restore8_kernel<__nv_bfloat16>)
-                                   : (vec ? restore8_aligned_kernel<__half> : restore8_kernel<__half>);
-    const cudaError_t err = blocks8(split) > 0x7fffffffLL
-                                ? cudaErrorInvalidValue
-                                : launch_early(kernel, dim3(static_cast<unsigned>(blocks8(split))), 256, 0, stream, c, split);
+    const Split8 split = split8(c.M, (c.N + (vec ? 7LL : 14LL)) / 8, kRestoreRows);  // a row may begin inside its first 16 bytes
+    auto kernel = c.dtype == kBf16 ? (vec ? restore8_kernel<__nv_bfloat16, true> : restore8_kernel<__nv_bfloat16, false>)
+                                   : (vec ? restore8_kernel<__half, true> : restore8_kernel<__half, false>);
+    const cudaError_t err = launch_early(kernel, split.grid(), 256, 0, stream, c, split);
     if (err != cudaSuccess) *detail = "restore kernel launch failed";
     return err;
 }
