@@ -59,15 +59,21 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float2 *parts,
     }
 }
 
-// factor[0] = 2^s with the largest finite |dloss| of the counted tokens times 2^s in [2^14, 2^15), factor[1] =
-// 2^-s: half then holds probabilities down to 2^-38 of the largest gradient.
+// The products of the gradient read dz in 16 bits. It is stored for rows' weights of `unit` at most, dloss
+// over its largest magnitude m, and the outputs are multiplied by m / unit: where every token has the same
+// dloss (a mean), dz is then p - [v = label] itself, which near -1 is rounded with almost no error, where a
+// dloss between powers of two would round all rows the same way. In half, whose smallest value is 2^-24, unit =
+// 2^14 keeps probabilities down to 2^-38.
+float unit_of(int dtype) { return dtype == kF16 ? 16384.0f : 1.0f; }
+
+// factor[0] = unit / m, factor[1] = m, with m the largest finite |dloss| of the counted tokens.
 __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long long incd, const int64_t *labels,
-                                                      int T, int V, float *factor) {
+                                                      int T, int V, float unit, float *factor) {
     __shared__ float top[32];
     grid_dependents();
     grid_dependency();
     float a = 0.0f;
-    for (int t = threadIdx.x; t < T; t += 1024) {
+    for (long long t = threadIdx.x; t < T; t += 1024) {
         const int64_t label = labels[t];
         const float d = fabsf(dloss[t * incd]);
         if (label >= 0 && label < V && d < INFINITY) a = fmaxf(a, d);
@@ -81,9 +87,9 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long l
 #pragma unroll
         for (int s = 16; s > 0; s /= 2) a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, s));
         if (threadIdx.x == 0) {
-            const int s = a > 0.0f ? max(-100, min(100, 14 - ilogbf(a))) : 0;
-            factor[0] = ldexpf(1.0f, s);
-            factor[1] = ldexpf(1.0f, -s);
+            a = a > 0.0f ? fmaxf(a, 1e-30f) : 1.0f;
+            factor[0] = unit / a;
+            factor[1] = a;
         }
     }
 }
@@ -163,11 +169,16 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
     x.lse = h.lse_in;
     x.dloss = h.dloss;
     x.incd = h.incd;
-    if (h.dtype == kF16) {
+    const float unit = unit_of(h.dtype);
+    extra.sum.scale = 1.0f / unit;
+    if (h.incd == 0) {
+        x.unit = unit;
+        extra.sum.factor = h.dloss;
+    } else {
         err = layer_scratch(kScratchHead, stream, 8, &p, detail);
         if (err != cudaSuccess) return err;
         float *factor = static_cast<float *>(p);
-        err = launch_early(factor_kernel, dim3(1), 1024, 0, stream, h.dloss, h.incd, h.labels, h.T, h.V, factor);
+        err = launch_early(factor_kernel, dim3(1), 1024, 0, stream, h.dloss, h.incd, h.labels, h.T, h.V, unit, factor);
         if (err != cudaSuccess) {
             *detail = "loss gradient kernel launch failed";
             return err;

@@ -137,6 +137,11 @@ struct ActGrad {
     long long lddy = 0;
     const uint16_t *z = nullptr;
     long long ldz = 0;
+    // z as a checkpoint instead, rows of codes 8-byte aligned
+    const int8_t *zq = nullptr;
+    long long ldzq = 0;
+    const float *zs = nullptr;
+    long long ldzs = 0;
     int act = 0;
     uint16_t *dz = nullptr;
     long long lddz = 0;

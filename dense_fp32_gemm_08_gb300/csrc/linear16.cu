@@ -1,6 +1,7 @@
 // linear16.cu: the linear layer on 16-bit values, Y = act(X op(W) + b) + R, and the products
 // and reductions of its gradient.
 #include "activation16.cuh"
+#include "checkpoint8.cuh"
 #include "half16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
@@ -110,26 +111,44 @@ __device__ __forceinline__ void align8_row(uint32_t (&out)[4], const uint32_t (&
     }
 }
 
-template <typename T, int ACT, bool VEC>
+// Z8: z comes from a checkpoint whose rows of codes are 8-byte aligned (the words read at a row's end may hold
+// bytes that follow it, in its last 8 bytes).
+template <typename T, int ACT, bool VEC, bool Z8>
 __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, long long r1, int c,
                                               int count, float (&sum)[8]) {
     using H = Half16<T>;
     constexpr int UNROLL = VEC ? 4 : 2;
     for (long long r = r0; r < r1; r += 8 * UNROLL) {
         constexpr int W = VEC ? 4 : 5;
-        uint32_t dy[UNROLL][W], z[UNROLL][W];
+        uint32_t dy[UNROLL][W], z[UNROLL][Z8 ? 1 : W];
+        uint2 codes[Z8 ? UNROLL : 1];
+        float scale[Z8 ? UNROLL : 1];
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i)
             if (r + 8 * i < r1) {
                 load8_row<VEC>(dy[i], g.dy + (r + 8 * i) * g.lddy + c, count);
-                if (ACT != kActNone) load8_row<VEC>(z[i], g.z + (r + 8 * i) * g.ldz + c, count);
+                if constexpr (Z8) {
+                    codes[i] = __ldg(reinterpret_cast<const uint2 *>(g.zq + (r + 8 * i) * g.ldzq + c));
+                    scale[i] = __ldg(g.zs + (r + 8 * i) * g.ldzs + c / kCheckpointBlock);
+                } else if (ACT != kActNone) {
+                    load8_row<VEC>(z[i], g.z + (r + 8 * i) * g.ldz + c, count);
+                }
             }
 #pragma unroll
         for (int i = 0; i < UNROLL; ++i) {
             if (r + 8 * i >= r1) break;
             uint32_t d4[4], z4[4] = {};
             align8_row<VEC>(d4, dy[i], g.dy + (r + 8 * i) * g.lddy + c);
-            if (ACT != kActNone) align8_row<VEC>(z4, z[i], g.z + (r + 8 * i) * g.ldz + c);
+            if constexpr (Z8) {
+                const float s = scale[i];
+                const uint2 lo = restore4<T>(codes[i].x, s, s, s, s), hi = restore4<T>(codes[i].y, s, s, s, s);
+                z4[0] = lo.x;
+                z4[1] = lo.y;
+                z4[2] = hi.x;
+                z4[3] = hi.y;
+            } else if (ACT != kActNone) {
+                align8_row<VEC>(z4, z[i], g.z + (r + 8 * i) * g.ldz + c);
+            }
             uint32_t out[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -152,8 +171,8 @@ __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, lo
     }
 }
 
-// VEC: dy and z allow 16-byte loads (and N is a multiple of 8).
-template <typename T, bool VEC>
+// VEC: dy and a 16-bit z allow 16-byte loads (and N is a multiple of 8).
+template <typename T, bool VEC, bool Z8>
 __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int rows, float *part,
                                                        unsigned int *counters) {
     __shared__ __align__(16) float sums[8][kGradCols];
@@ -168,7 +187,7 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int r
     float sum[8] = {};
     if (count > 0)
         with_activation(g.act, [&](auto act) {
-            act_grad_rows<T, decltype(act)::value, VEC>(g, r0 + w, r1, c, count, sum);
+            act_grad_rows<T, decltype(act)::value, VEC, Z8>(g, r0 + w, r1, c, count, sum);
         });
     if (!g.db) return;
 #pragma unroll
@@ -210,6 +229,12 @@ __global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int r
     __syncthreads();
     if (n < g.N)
         g.db[n] = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) + (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+}
+
+template <bool Z8>
+auto act_grad_choice(int dtype, bool vec) {
+    return dtype == kBf16 ? (vec ? act_grad_kernel<__nv_bfloat16, true, Z8> : act_grad_kernel<__nv_bfloat16, false, Z8>)
+                          : (vec ? act_grad_kernel<__half, true, Z8> : act_grad_kernel<__half, false, Z8>);
 }
 
 __global__ void zero_kernel(float *p, int n) {
@@ -295,13 +320,26 @@ cudaError_t gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const 
     return together > 0 ? pair_gemm16_launch(q, together, stream, detail) : cudaSuccess;
 }
 
+// The pair product's epilogue saves its tiles. The products of few rows and those without a k keep their
+// pre-activation in 16 bits in scratch, from which it is saved.
 cudaError_t gemm16_save8_launch(const Gemm16 &g, const Checkpoint8 &c, cudaStream_t stream, const char **detail) {
-    // The pre-activation goes through scratch in 16 bits.
     Gemm16 q = g;
+    cudaError_t err = cudaSuccess;
+    if (q.K > 0) {
+        const Pack16 packs[2] = {{&q.A, &q.lda, q.a_mn ? q.K : q.M, q.a_mn ? q.M : q.K},
+                                 {&q.B, &q.ldb, q.b_mn ? q.K : q.N, q.b_mn ? q.N : q.K}};
+        err = pack16_launch(packs, 2, stream, detail);
+        if (err != cudaSuccess) return err;
+        if (!stream_gemm16_supports(q)) {
+            PairExtra extra;
+            extra.save = {c.Q, c.ldq, c.S, c.lds};
+            return pair_gemm16_extra_launch(&q, 1, kPairSave8, extra, stream, detail);
+        }
+    }
     Checkpoint8 save = c;
     q.ldz = (g.N + 7LL) / 8 * 8;
     void *z = nullptr;
-    cudaError_t err = layer_scratch(kScratchRestoreZ, stream, static_cast<size_t>(g.M) * q.ldz * 2, &z, detail);
+    err = layer_scratch(kScratchRestoreZ, stream, static_cast<size_t>(g.M) * q.ldz * 2, &z, detail);
     if (err != cudaSuccess) return err;
     q.pre = static_cast<uint16_t *>(z);
     save.X = q.pre;
@@ -316,7 +354,8 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
         err = launch_early(zero_kernel, dim3(static_cast<unsigned>((g.N + 255LL) / 256)), 256, 0, stream, g.db,
                            g.N);
     } else {
-        const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) && (g.act == kActNone || tma_rows(g.z, g.ldz));
+        const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) &&
+                         (g.act == kActNone || g.zq || tma_rows(g.z, g.ldz));
         // Rows per CTA, in whole steps: about whole rounds of the CTAs that run at once, three per SM, with 256
         // rows or so at most (a short last round) and a step at least (the last CTA of a column
         // block adds the sums of all of them). db alone, 2048 x 2048: 18.0 us with 8 rows, 9.5 with 32;
@@ -349,9 +388,7 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
             counters = static_cast<unsigned int *>(q);
         }
         const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(parts));
-        auto kernel = g.dtype == kBf16
-                          ? (vec ? act_grad_kernel<__nv_bfloat16, true> : act_grad_kernel<__nv_bfloat16, false>)
-                          : (vec ? act_grad_kernel<__half, true> : act_grad_kernel<__half, false>);
+        auto kernel = g.zq ? act_grad_choice<true>(g.dtype, vec) : act_grad_choice<false>(g.dtype, vec);
         err = launch_early(kernel, grid, 256, 0, stream, g, static_cast<int>(rows), part, counters);
     }
     if (err != cudaSuccess) *detail = "gradient kernel launch failed";

@@ -39,6 +39,7 @@
 // Every wait is bounded (ptx.cuh); a wait that expires ends the role, and the CTAs still meet at
 // the final cluster barrier and free their TMEM.
 #include "activation16.cuh"
+#include "checkpoint8.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
 #include "raster.cuh"
@@ -258,6 +259,36 @@ __device__ __forceinline__ void add_residual(float (&v)[32], uint32_t (&raw)[20]
     __syncwarp();
 }
 
+// The codes of up to 32 values of a row.
+template <typename T>
+__device__ __forceinline__ void save_codes(const float (&v)[32], const Coder8<T> &coder, int8_t *q, bool vec,
+                                           int count) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint2 codes[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int at = 16 * h + 8 * k + 2 * i;
+                w[i] = Half16<T>::narrow2(v[at], v[at + 1]);
+            }
+            codes[k] = coder.eight(w);
+        }
+        if (vec && count >= 16 * h + 16) {
+            *reinterpret_cast<uint4 *>(q + 16 * h) = make_uint4(codes[0].x, codes[0].y, codes[1].x, codes[1].y);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint64_t both = static_cast<uint64_t>(codes[k].y) << 32 | codes[k].x;
+                for (int i = 0; i < min(8, count - 16 * h - 8 * k); ++i)
+                    q[16 * h + 8 * k + i] = static_cast<int8_t>(both >> (8 * i));
+            }
+        }
+    }
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMinusInf = -__builtin_huge_valf();
 
@@ -400,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t raw[20];  // the next block's residual
         float bias[2] = {0.0f, 0.0f};  // of columns col0 + lane and col0 + 32 + lane
         float factor = 1.0f;
-        if (MODE == kPairSum && p.extra.sum.factor) factor = *p.extra.sum.factor;
+        if (MODE == kPairSum) factor = p.extra.sum.scale * *p.extra.sum.factor;
         if (MODE == kPairLogitGrad && p.extra.head.factor) factor = *p.extra.head.factor;
         for (int t = pair; t < p.total_items; t += pairs, ++j) {
             const int set = j & 1;
@@ -422,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             float lse = 0.0f, dloss = 0.0f;
             if (MODE == kPairLogitGrad && label.counts) {
                 lse = p.extra.head.lse[row0 + lane];
-                dloss = factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd];
+                dloss = p.extra.head.factor ? factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd]
+                                            : p.extra.head.unit;
             }
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
             tc_after_sync();
@@ -559,16 +591,44 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 }
                 continue;
             }
+            auto add_bias = [&](int b, float(&v)[32]) {
+                if (p.bias) {
+                    const float mine = b ? bias[1] : bias[0];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
+                }
+            };
+            // The checkpoint's block of 64 columns is this warp's share of the tile: its largest magnitude
+            // first, so that the values pass twice (out of TMEM, or the pieces).
+            uint32_t top = 0;
+            if constexpr (MODE == kPairSave8) {
+#pragma unroll 1
+                for (int b = 0; b < blocks; ++b) {
+                    float v[32];
+                    values(b, v);
+                    add_bias(b, v);
+                    const int cols = g.N - col0 - 32 * b;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t w = Half16<T>::narrow2(v[2 * i], v[2 * i + 1]);
+                        top = magnitude2<T>(top, cols > 2 * i + 1 ? w : cols > 2 * i ? w & 0xFFFFu : 0u);
+                    }
+                }
+                top = magnitude(top);
+                if (row0 + lane < g.M)
+                    p.extra.save.scales[(row0 + lane) * p.extra.save.lds + col0 / kCheckpointBlock] = scale8<T>(top);
+            }
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b) {
                 const int col = col0 + 32 * b;
                 float v[32];
                 values(b, v);
                 if (b == blocks - 1 && !pieces) release();
-                if (p.bias) {
-                    const float mine = b ? bias[1] : bias[0];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
+                add_bias(b, v);
+                if constexpr (MODE == kPairSave8) {
+                    if (row0 + lane < g.M)
+                        save_codes<T>(v, Coder8<T>(top), p.extra.save.codes + (row0 + lane) * p.extra.save.ldq + col,
+                                      p.q_vec != 0, g.N - col);
                 }
                 if (p.pre) {
                     if (lane == 0) bulk_wait_read<0>();
@@ -739,6 +799,7 @@ cudaError_t launch(const Gemm16 *list, int n, const PairExtra &extra, cudaStream
         p.counters = static_cast<unsigned int *>(sync);
     }
     p.extra = extra;
+    p.q_vec = (reinterpret_cast<uintptr_t>(extra.save.codes) & 15u) == 0 && extra.save.ldq % 16 == 0;
     p.sum_product = MODE == kPairSum && extra.sum.sums ? order[0] : -1;  // list[0]
     if (n == 1) {
         const Gemm16 &g = list[0];
@@ -777,6 +838,9 @@ cudaError_t pair_gemm16_extra_launch(const Gemm16 *list, int n, int mode, const 
                                      cudaStream_t stream, const char **detail) {
     const bool bf16 = list[0].dtype == kBf16;
     switch (mode) {
+        case kPairSave8:
+            return bf16 ? launch<__nv_bfloat16, kPairSave8>(list, n, extra, stream, detail)
+                        : launch<__half, kPairSave8>(list, n, extra, stream, detail);
         case kPairLogits:
             return bf16 ? launch<__nv_bfloat16, kPairLogits>(list, n, extra, stream, detail)
                         : launch<__half, kPairLogits>(list, n, extra, stream, detail);

@@ -42,16 +42,18 @@ struct PairHead {
     float2 *parts = nullptr;
     long long ld_parts = 0;
     float *at = nullptr;
-    // kPairLogitGrad
+    // kPairLogitGrad: the rows' weights are factor * dloss, or `unit` for every row without a factor.
     const float *lse = nullptr, *dloss = nullptr;
     long long incd = 0;
-    const float *factor = nullptr;  // multiplies dloss
+    const float *factor = nullptr;
+    float unit = 1.0f;
 };
 // The first product's sums, in the kernel's own order; a piece that is not the last writes no output.
 struct PairSum {
     float *sums = nullptr;
     int first = 1, last = 1;
-    const float *factor = nullptr;  // multiplies both products' outputs
+    const float *factor = nullptr;  // times scale, multiplies both products' outputs
+    float scale = 1.0f;
 };
 struct PairExtra {
     PairSave8 save;

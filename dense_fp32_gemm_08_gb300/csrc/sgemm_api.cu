@@ -407,7 +407,7 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
                                int64_t K, const void *dY, int64_t lddy, const void *Z, int64_t ldz,
                                sgemm_activation_t act, const void *X, int64_t ldx, const void *W,
                                int64_t ldw, void *dX, int64_t lddx, void *dW, int64_t lddw,
-                               float *db, cudaStream_t stream, bool only_check = false) {
+                               float *db, cudaStream_t stream, const Codes8 *z8 = nullptr, bool only_check = false) {
     sgemm_status_t st = check_linear(dtype, transw, act, M, N, K);
     if (st != SGEMM_OK) return st;
     const bool t = transw == SGEMM_OP_T;
@@ -448,8 +448,15 @@ sgemm_status_t linear_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M
         a.N = static_cast<int>(N);
         a.dy = in16(dY);
         a.lddy = lddy;
-        a.z = in16(Z);
-        a.ldz = ldz;
+        if (z8) {
+            a.zq = z8->Q;
+            a.ldzq = z8->ldq;
+            a.zs = z8->S;
+            a.ldzs = z8->lds;
+        } else {
+            a.z = in16(Z);
+            a.ldz = ldz;
+        }
         a.act = act;
         a.db = db;
         if (make_dz) {
@@ -533,16 +540,18 @@ sgemm_status_t linear_backward8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t 
     const void *X = x.Q ? &kStandIn : nullptr, *Z = z.Q ? &kStandIn : nullptr;
     int64_t ldx = std::max<int64_t>(1, K), ldz = std::max<int64_t>(1, N);
     st = linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db,
-                         stream, true);
+                         stream, nullptr, true);
     if (st != SGEMM_OK) return st;
     const char *detail = "";
     cudaError_t err = cudaSuccess;
+    // The gradient pass reads aligned codes itself; the product needs X in 16 bits.
+    const bool z_direct = use_z && (reinterpret_cast<uintptr_t>(z.Q) & 7u) == 0 && z.ldq % 8 == 0;
     if (use_x) err = restore_to_scratch(x, dtype, M, K, sg::kScratchRestoreX, stream, &X, &ldx, &detail);
-    if (err == cudaSuccess && use_z)
+    if (err == cudaSuccess && use_z && !z_direct)
         err = restore_to_scratch(z, dtype, M, N, sg::kScratchRestoreZ, stream, &Z, &ldz, &detail);
     if (err != cudaSuccess) return fail_cuda(detail, err);
     return linear_backward(dtype, transw, M, N, K, dY, lddy, Z, ldz, act, X, ldx, W, ldw, dX, lddx, dW, lddw, db,
-                           stream, false);
+                           stream, z_direct ? &z : nullptr);
 }
 
 // Checks what the loss and its gradient share.
