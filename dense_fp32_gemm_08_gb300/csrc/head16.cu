@@ -5,7 +5,8 @@
 //   dz_tv = dloss_t (exp(z_tv - lse_t) - [v = label]),   dX = dz . op(W)^T,   dW = X^T . dz
 //
 // The forward pass is the pair product (pair_gemm16.cu) with an epilogue that reduces each row's 64
-// logits of a warp to their maximum and sum of exponentials; a second kernel joins those. The gradient
+// logits of a warp to their maximum and sum of exponentials, or the streaming product for few tokens
+// (stream_gemm16.cu) with one that does so for 32; a second kernel joins those. The gradient
 // computes the logits again, a piece of the vocabulary at a time: one product whose epilogue
 // writes the piece's dz in 16 bits to scratch, then dX and dW's rows (or columns) of the piece in one
 // launch. dX adds up over the pieces in fp32.
@@ -20,42 +21,79 @@ namespace sg {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-constexpr int kJoinThreads = 1024;
+// Maximum and sum of exponentials of two parts together. (A part without finite logits has m = -inf, s = 0.)
+__device__ __forceinline__ float2 join(float2 a, float2 b) {
+    const float m = fmaxf(a.x, b.x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    return make_float2(m, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
+}
+__device__ __forceinline__ float2 join_lanes(float2 a) {
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2)
+        a = join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, s), __shfl_xor_sync(0xFFFFFFFFu, a.y, s)));
+    return a;
+}
+struct LossOut {
+    const float *at;
+    const int64_t *labels;
+    int T, V;
+    float *loss, *lse;
+    __device__ __forceinline__ void put(int row, float2 a) const {
+        const float l = a.x + logf(a.y);
+        const int64_t label = labels[row];
+        if (lse) lse[row] = l;
+        if (loss) loss[row] = label >= 0 && label < V ? l - at[row] : 0.0f;
+    }
+};
 
-// Joins the parts of 32 rows: lane = row, a warp every 32nd part, then the warps through shared memory.
+// Joins the parts of 32 rows, parts[part][row]: lane = row, a warp every 32nd part, then the warps through
+// shared memory.
+constexpr int kJoinThreads = 1024;
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float2 *parts, long long ld, int n_parts,
-                                                            const float *at, const int64_t *labels, int T, int V,
-                                                            float *loss, float *lse) {
+                                                            const LossOut out) {
     __shared__ float2 shared[32][33];
     grid_dependents();
     grid_dependency();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
-    auto join = [](float2 a, float2 b) {
-        const float m = fmaxf(a.x, b.x);
-        const float base = m == -INFINITY ? 0.0f : m;
-        return make_float2(m, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
-    };
     float2 a = make_float2(-INFINITY, 0.0f);
-    if (row < T) {
+    if (row < out.T) {
 #pragma unroll 4
         for (int i = warp; i < n_parts; i += 32) a = join(a, __ldcg(parts + i * ld + row));
     }
     shared[warp][lane] = a;
     __syncthreads();
     // Warp w now joins row w's 32 values.
-    a = shared[lane][warp];
-#pragma unroll
-    for (int s = 16; s > 0; s /= 2) {
-        const float2 b = make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, s), __shfl_xor_sync(0xFFFFFFFFu, a.y, s));
-        a = join(a, b);
-    }
+    a = join_lanes(shared[lane][warp]);
     const int mine = blockIdx.x * 32 + warp;
-    if (lane == 0 && mine < T) {
-        const float l = a.x + logf(a.y);
-        const int64_t label = labels[mine];
-        if (lse) lse[mine] = l;
-        if (loss) loss[mine] = label >= 0 && label < V ? l - at[mine] : 0.0f;
+    if (lane == 0 && mine < out.T) out.put(mine, a);
+}
+
+// Joins parts[row][part]: a row per warp, or per CTA where it has many parts.
+constexpr int kRowWarps = 8;
+__global__ void __launch_bounds__(32 * kRowWarps) join_rows_kernel(const float2 *parts, long long ld, int n_parts,
+                                                                   int wide, const LossOut out) {
+    __shared__ float2 shared[kRowWarps];
+    grid_dependents();
+    grid_dependency();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = wide ? blockIdx.x : blockIdx.x * kRowWarps + warp;
+    float2 a = make_float2(-INFINITY, 0.0f);
+    if (row < out.T) {
+#pragma unroll 4
+        for (int i = wide ? threadIdx.x : lane; i < n_parts; i += wide ? 32 * kRowWarps : 32)
+            a = join(a, __ldcg(parts + row * ld + i));
+    }
+    a = join_lanes(a);
+    if (!wide) {
+        if (lane == 0 && row < out.T) out.put(row, a);
+        return;
+    }
+    if (lane == 0) shared[warp] = a;
+    __syncthreads();
+    if (warp == 0) {
+        a = join_lanes(lane < kRowWarps ? shared[lane] : make_float2(-INFINITY, 0.0f));
+        if (lane == 0) out.put(row, a);
     }
 }
 
@@ -122,12 +160,15 @@ cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **
     Head16 h = head;
     cudaError_t err = pack(h, stream, detail);
     if (err != cudaSuccess) return err;
-    const int n_parts = static_cast<int>((h.V + 63LL) / 64);
     for (int t0 = 0; t0 < h.T; t0 += std::min(kTokens, h.T - t0)) {
         const int T = std::min(kTokens, h.T - t0);
-        const long long ld = (T + 31) / 32 * 32;
+        const Gemm16 g = logits(h, t0, T, 0, h.V);
+        const bool few = stream_gemm16_supports(g);
+        const int n_parts = static_cast<int>((h.V + (few ? 31LL : 63LL)) / (few ? 32 : 64));
+        const long long ld = (T + 31) / 32 * 32, ld_parts = few ? n_parts : ld;
         void *p = nullptr;
-        err = layer_scratch(kScratchHead, stream, static_cast<size_t>(ld) * 4 + static_cast<size_t>(ld) * n_parts * 8, &p, detail);
+        err = layer_scratch(kScratchHead, stream,
+                            static_cast<size_t>(ld) * 4 + static_cast<size_t>(ld) * n_parts * 8, &p, detail);
         if (err != cudaSuccess) return err;
         PairExtra extra;
         PairHead &x = extra.head;
@@ -135,13 +176,21 @@ cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **
         x.V = h.V;
         x.at = static_cast<float *>(p);
         x.parts = reinterpret_cast<float2 *>(x.at + ld);
-        x.ld_parts = ld;
-        const Gemm16 g = logits(h, t0, T, 0, h.V);
-        err = pair_gemm16_extra_launch(&g, 1, kPairLogits, extra, stream, detail);
-        if (err != cudaSuccess) return err;
-        err = launch_early(join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), kJoinThreads, 0, stream,
-                           static_cast<const float2 *>(x.parts), ld, n_parts, static_cast<const float *>(x.at),
-                           x.labels, T, h.V, h.loss ? h.loss + t0 : nullptr, h.lse ? h.lse + t0 : nullptr);
+        x.ld_parts = ld_parts;
+        const LossOut out{x.at, x.labels, T, h.V, h.loss ? h.loss + t0 : nullptr, h.lse ? h.lse + t0 : nullptr};
+        const float2 *parts = x.parts;
+        if (few) {
+            err = stream_gemm16_extra_launch(g, kPairLogits, extra, stream, detail);
+            if (err != cudaSuccess) return err;
+            const int wide = n_parts > 128;
+            err = launch_early(join_rows_kernel, dim3(static_cast<unsigned>(wide ? T : (T + kRowWarps - 1) / kRowWarps)),
+                               32 * kRowWarps, 0, stream, parts, ld_parts, n_parts, wide, out);
+        } else {
+            err = pair_gemm16_extra_launch(&g, 1, kPairLogits, extra, stream, detail);
+            if (err != cudaSuccess) return err;
+            err = launch_early(join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), kJoinThreads, 0, stream,
+                               parts, ld_parts, n_parts, out);
+        }
         if (err != cudaSuccess) {
             *detail = "loss kernel launch failed";
             return err;
@@ -197,7 +246,8 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
         g.D = static_cast<uint16_t *>(dz);
         g.ldd = ldz;
         x.v0 = v0;
-        err = pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
+        err = stream_gemm16_supports(g) ? stream_gemm16_extra_launch(g, kPairLogitGrad, extra, stream, detail)
+                                        : pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
         if (err != cudaSuccess) return err;
         Gemm16 list[2];
         int count = 0;
@@ -214,6 +264,11 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
             q.b_mn = !h.w_dv;
             q.D = h.dX;
             q.ldd = h.lddx;
+            if (h.T <= 64 && n == h.V && stream_gemm16_supports(q)) {
+                err = stream_gemm16_extra_launch(q, kPairSum, extra, stream, detail);
+                if (err != cudaSuccess) return err;
+                --count;
+            }
         }
         if (h.dW) {
             Gemm16 &q = list[count++];
@@ -232,7 +287,7 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
         }
         extra.sum.first = v0 == 0;
         extra.sum.last = v0 + n == h.V;
-        err = pair_gemm16_extra_launch(list, count, kPairSum, extra, stream, detail);
+        if (count > 0) err = pair_gemm16_extra_launch(list, count, kPairSum, extra, stream, detail);
         if (err != cudaSuccess) return err;
     }
     return cudaSuccess;

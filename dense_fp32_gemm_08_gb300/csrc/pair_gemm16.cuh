@@ -20,7 +20,7 @@ bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols
 cudaError_t pair_gemm16_launch(const Gemm16 *list, int n, cudaStream_t stream, const char **detail);
 
 // What the epilogue does with a product, besides Gemm16's own parts.
-enum PairMode : int {
+enum PairMode : int {  // (the streaming product has all but kPairSave8)
     kPairLayer = 0,  // bias, activation, residual, pre-activation
     kPairSave8,      // the same, the pre-activation as an 8-bit checkpoint
     kPairLogits,     // logits of the head: their sums of exponentials and the labels' values; no output
@@ -38,7 +38,8 @@ struct PairHead {
     const int64_t *labels = nullptr;
     int V = 0, v0 = 0;
     // kPairLogits: of 64 columns' logits of a row, the largest m and the sum of exp(z - m), at
-    // parts[(column / 64) * ld_parts + row]; and the row's logit at its label.
+    // parts[(column / 64) * ld_parts + row]; and the row's logit at its label. The streaming product: of
+    // 32 columns' logits, at parts[row * ld_parts + column / 32].
     float2 *parts = nullptr;
     long long ld_parts = 0;
     float *at = nullptr;
@@ -68,5 +69,8 @@ cudaError_t pair_gemm16_extra_launch(const Gemm16 *list, int n, int mode, const 
 // where the 128 x 64 tiles number at most 128. A and B must satisfy tma_rows; K > 0.
 bool stream_gemm16_supports(const Gemm16 &g);
 cudaError_t stream_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail);
+// kPairSum here: no sums, only the factor.
+cudaError_t stream_gemm16_extra_launch(const Gemm16 &g, int mode, const PairExtra &extra, cudaStream_t stream,
+                                       const char **detail);
 
 }  // namespace sg

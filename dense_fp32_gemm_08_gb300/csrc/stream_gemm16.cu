@@ -39,6 +39,8 @@ struct StreamParams {
     long long ldz;
     unsigned int *counters;  // [tiles][epilogue warps], zero between calls
     float *pieces;           // [2 * CTAs][NT / 4][128][4]
+    PairHead head;
+    PairSum sum;
 };
 
 template <int NT>
@@ -59,12 +61,53 @@ struct StreamConfig {
     static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
 };
 
-// 16 columns (tokens m0 .. m0 + 15) of output feature n.
-template <typename T>
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 16 columns (tokens m0 .. m0 + 15) of output feature n; a warp has 32 features in order.
+template <typename T, int MODE>
 __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, float b, float (&v)[16]) {
     using H = Half16<T>;
-    if (n >= p.N) return;
     const int rows = min(16, p.M - m0);
+    if constexpr (MODE == kPairLogits) {
+        const int lane = threadIdx.x & 31;
+        if (n - lane >= p.N) return;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+            if (p.head.labels[m0 + i] == n && n < p.N) p.head.at[m0 + i] = v[i];
+            const float z = n < p.N ? v[i] : -INFINITY;
+            float m = z;
+#pragma unroll
+            for (int s = 16; s > 0; s /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+            float e = exp2_approx((z - (m == -INFINITY ? 0.0f : m)) * kLog2e);
+#pragma unroll
+            for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
+            if (lane == 0) p.head.parts[(m0 + i) * p.head.ld_parts + n / 32] = make_float2(m, e);
+        }
+        return;
+    }
+    if (n >= p.N) return;
+    if constexpr (MODE == kPairLogitGrad) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (i >= rows) break;
+            const int64_t label = p.head.labels[m0 + i];
+            float dz = 0.0f;
+            if (label >= 0 && label < p.head.V) {
+                const float dloss = p.head.factor ? *p.head.factor * p.head.dloss[(m0 + i) * p.head.incd] : p.head.unit;
+                dz = (exp2_approx((v[i] - p.head.lse[m0 + i]) * kLog2e) - (label == p.head.v0 + n ? 1.0f : 0.0f)) * dloss;
+            }
+            p.D[(m0 + i) * p.ldd + n] = H::narrow(dz);
+        }
+        return;
+    }
+    if constexpr (MODE == kPairSum) {
+        const float factor = p.sum.scale * *p.sum.factor;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < rows) p.D[(m0 + i) * p.ldd + n] = H::narrow(v[i] * factor);
+        return;
+    }
     float r[16];
     if (p.res) {
 #pragma unroll
@@ -85,7 +128,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
         if (i < rows) p.D[(m0 + i) * p.ldd + n] = H::narrow(p.res ? v[i] + r[i] : v[i]);
 }
 
-template <int NT, bool W_MN, typename T>
+template <int NT, bool W_MN, typename T, int MODE>
 __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::CTAS)
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const StreamParams p) {
@@ -231,7 +274,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T>(p, n, m0 + c, b, v);
+                    finish16<T, MODE>(p, n, m0 + c, b, v);
                 } else {
                     put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, tokens, r);
                 }
@@ -244,7 +287,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             for (int c = first_col; c < min(tokens, first_col + COLS); c += 16) {
                 float v[16];
                 sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, tokens, v);
-                finish16<T>(p, n, m0 + c, b, v);
+                finish16<T, MODE>(p, n, m0 + c, b, v);
             }
         }
     }
@@ -258,10 +301,10 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     }
 }
 
-template <int NT, bool W_MN, typename T>
-cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
+template <int NT, bool W_MN, typename T, int MODE>
+cudaError_t launch(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream, const char **detail) {
     using C = StreamConfig<NT>;
-    auto kernel = stream_gemm16_kernel<NT, W_MN, T>;
+    auto kernel = stream_gemm16_kernel<NT, W_MN, T, MODE>;
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
@@ -312,6 +355,8 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     p.ldd = g.ldd;
     p.pre = g.pre;
     p.ldz = g.ldz;
+    p.head = extra.head;
+    p.sum = extra.sum;
     void *ws = nullptr;
     err = layer_scratch(kScratchStream, stream,
                         kCounterBytes + static_cast<size_t>(2) * sms[dev] * 64 * kStreamRows * 4, &ws, detail);
@@ -330,16 +375,21 @@ cudaError_t launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
     return err;
 }
 
-template <int NT, typename T>
-cudaError_t launch_major(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    return g.b_mn ? launch<NT, true, T>(g, stream, detail) : launch<NT, false, T>(g, stream, detail);
+template <int MODE, typename T>
+cudaError_t launch_width(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream, const char **detail) {
+    if (g.M <= 16)
+        return g.b_mn ? launch<16, true, T, MODE>(g, extra, stream, detail)
+                      : launch<16, false, T, MODE>(g, extra, stream, detail);
+    if (g.M <= 32)
+        return g.b_mn ? launch<32, true, T, MODE>(g, extra, stream, detail)
+                      : launch<32, false, T, MODE>(g, extra, stream, detail);
+    return g.b_mn ? launch<64, true, T, MODE>(g, extra, stream, detail)
+                  : launch<64, false, T, MODE>(g, extra, stream, detail);
 }
-
-template <typename T>
-cudaError_t launch_width(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    if (g.M <= 16) return launch_major<16, T>(g, stream, detail);
-    if (g.M <= 32) return launch_major<32, T>(g, stream, detail);
-    return launch_major<64, T>(g, stream, detail);
+template <int MODE>
+cudaError_t launch_mode(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream, const char **detail) {
+    return g.dtype == kBf16 ? launch_width<MODE, __nv_bfloat16>(g, extra, stream, detail)
+                            : launch_width<MODE, __half>(g, extra, stream, detail);
 }
 
 }  // namespace
@@ -357,8 +407,14 @@ bool stream_gemm16_supports(const Gemm16 &g) {
 }
 
 cudaError_t stream_gemm16_launch(const Gemm16 &g, cudaStream_t stream, const char **detail) {
-    return g.dtype == kBf16 ? launch_width<__nv_bfloat16>(g, stream, detail)
-                            : launch_width<__half>(g, stream, detail);
+    return launch_mode<kPairLayer>(g, PairExtra(), stream, detail);
+}
+
+cudaError_t stream_gemm16_extra_launch(const Gemm16 &g, int mode, const PairExtra &extra, cudaStream_t stream,
+                                       const char **detail) {
+    return mode == kPairLogits      ? launch_mode<kPairLogits>(g, extra, stream, detail)
+           : mode == kPairLogitGrad ? launch_mode<kPairLogitGrad>(g, extra, stream, detail)
+                                    : launch_mode<kPairSum>(g, extra, stream, detail);
 }
 
 }  // namespace sg
