@@ -123,6 +123,11 @@ __device__ __forceinline__ void with_layout(const PairProduct &g, Body body) {
         body(std::false_type(), std::false_type());
 }
 
+// The blocks that one accumulator sums. The tensor cores add to it with fp32 sums cut, not rounded, once per 16 k
+// values, which leaves the logits of 4096 values 3e-6 too small; the epilogue adds runs of 1024 in
+// registers (16384 x 32000 x 4096: the loss's error falls from 2.9e-6 to that of a plain fp32 product).
+__device__ __forceinline__ int run_blocks(int mode, int blocks) { return mode == kPairLogits ? kLogitBlocks : blocks; }
+
 // A wait whose arrivals may come from the other CTA of the pair.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
     uint32_t done;
@@ -295,12 +300,12 @@ constexpr float kMinusInf = -__builtin_huge_valf();
 // Where the row's label is among the columns from col0 on (outside them: some other number). The
 // token counts if its label is an entry of the vocabulary.
 struct RowLabel {
-    long long at;
+    int at;
     bool counts;
     __device__ __forceinline__ RowLabel(const PairHead &h, int row, int M, int col0) {
         const long long label = row < M ? h.labels[row] : -1;
         counts = label >= 0 && label < h.V;
-        at = counts ? label - h.v0 - col0 : -1;
+        at = counts ? static_cast<int>(label) - h.v0 - col0 : -1;
     }
 };
 
@@ -388,37 +393,42 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (lane == 0 && rank == 0) {
             int it = 0, j = 0;
             bool ok = true;
-            for (int t = pair; t < p.total_items && ok; t += pairs, ++j) {
+            for (int t = pair; t < p.total_items && ok; t += pairs) {
                 const Item item(p, t);
                 const int i = item.product;
-                const int set = j & 1;
-                if (j >= 2 && !mbar_wait_cluster(&acc_free[set], ((j >> 1) - 1) & 1)) break;
-                tc_after_sync();
-                const uint32_t d = tmem + static_cast<uint32_t>(set * kBN);
-                const int KB = item.n;
                 const uint32_t idesc = p.g[i].idesc;
-                auto blocks = [&](auto a_layout, auto b_layout) {
-                    constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
-                    for (int kb = 0; kb < KB; ++kb, ++it) {
-                        const int s = it % kStages;
-                        if (!mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_after_sync();
-                        const uint32_t sa = smem_addr(smem + s * kStageBytes), sb = sa + kPartBytes;
-                        const uint64_t da = a_mn ? desc_mn_major(sa, 8192) : desc_k_major(sa);
-                        const uint64_t db = b_mn ? desc_mn_major(sb, 8192) : desc_k_major(sb);
-#pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k)  // start addresses count 16 bytes: a
-                            mma_16<2>(d, da + static_cast<uint64_t>(k * (a_mn ? 128 : 2)),  // k-step is
-                                      db + static_cast<uint64_t>(k * (b_mn ? 128 : 2)),     // 32 bytes
-                                      idesc, kb > 0 || k > 0);  // of a row or 16 rows
-                        mma_commit_16<2>(&empty[s]);
+                for (int kb0 = 0; kb0 < item.n && ok; kb0 += run_blocks(MODE, item.n), ++j) {
+                    const int set = j & 1;
+                    if (j >= 2 && !mbar_wait_cluster(&acc_free[set], ((j >> 1) - 1) & 1)) {
+                        ok = false;
+                        break;
                     }
-                };
-                with_layout(p.g[i], blocks);
-                if (ok) mma_commit_16<2>(&acc_full[set]);
+                    tc_after_sync();
+                    const uint32_t d = tmem + static_cast<uint32_t>(set * kBN);
+                    const int KB = min(run_blocks(MODE, item.n), item.n - kb0);
+                    auto blocks = [&](auto a_layout, auto b_layout) {
+                        constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
+                        for (int kb = 0; kb < KB; ++kb, ++it) {
+                            const int s = it % kStages;
+                            if (!mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_after_sync();
+                            const uint32_t sa = smem_addr(smem + s * kStageBytes), sb = sa + kPartBytes;
+                            const uint64_t da = a_mn ? desc_mn_major(sa, 8192) : desc_k_major(sa);
+                            const uint64_t db = b_mn ? desc_mn_major(sb, 8192) : desc_k_major(sb);
+#pragma unroll
+                            for (int k = 0; k < kBK / 16; ++k)  // start addresses count 16 bytes: a
+                                mma_16<2>(d, da + static_cast<uint64_t>(k * (a_mn ? 128 : 2)),  // k-step is
+                                          db + static_cast<uint64_t>(k * (b_mn ? 128 : 2)),     // 32 bytes
+                                          idesc, kb > 0 || k > 0);  // of a row or 16 rows
+                            mma_commit_16<2>(&empty[s]);
+                        }
+                    };
+                    with_layout(p.g[i], blocks);
+                    if (ok) mma_commit_16<2>(&acc_full[set]);
+                }
             }
         }
     } else if (warp >= 4) {
@@ -455,6 +465,68 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 lse = p.extra.head.lse[row0 + lane];
                 dloss = p.extra.head.factor ? factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd]
                                             : p.extra.head.unit;
+            }
+            if constexpr (MODE == kPairLogits) {
+                float v[64];
+#pragma unroll
+                for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                bool ok = true;
+                for (int kb = 0; kb < item.n; kb += kLogitBlocks, ++j) {
+                    ok = ok && mbar_wait_cluster(&acc_full[j & 1], (j >> 1) & 1);
+                    if (!ok) break;
+                    tc_after_sync();
+                    if (inside) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t r[16];
+                            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * kBN + c0 + 16 * q), r);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[16 * q + i] += __uint_as_float(r[i]);
+                        }
+                    }
+                    tc_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_at(j & 1 ? free1 : free0);
+                }
+                --j;  // the tile's last accumulator
+                if (!ok) break;
+                if (!inside) continue;
+                if (g.split > 1) {
+                    constexpr size_t kPiece = 2ull * kBN * kBM;
+                    const size_t at = static_cast<size_t>(g.piece0 + item.tile * g.split);
+                    float *base = p.pieces + (2 * at + rank) * kBN * kBM + c0 * kBM + quarter * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) __stcg(base + item.piece * kPiece + i * kBM, v[i]);
+                    unsigned int *counter =
+                        p.counters + (2 * static_cast<size_t>(g.tile0 + item.tile) + rank) * kEpiWarps + w;
+                    if (!piece_arrived(counter, 1, g.split, lane)) continue;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                    for (int k = 0; k < g.split; ++k)
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) v[i] += __ldcg(base + k * kPiece + i * kBM);
+                }
+                if (__any_sync(0xFFFFFFFFu, label.at >= 0 && label.at < 64)) {
+                    float z = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) z = label.at == i ? v[i] : z;
+                    if (label.at >= 0 && label.at < 64) p.extra.head.at[row0 + lane] = z;
+                }
+                if (g.N - col0 < 64) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i] = i < g.N - col0 ? v[i] : kMinusInf;
+                }
+                float m = kMinusInf, s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) m = fmaxf(m, v[i]);
+                const float base = m == kMinusInf ? 0.0f : m;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) s += exp2_approx((v[i] - base) * kLog2e);
+                if (row0 + lane < g.M)
+                    p.extra.head.parts[static_cast<size_t>(col0 / 64) * p.extra.head.ld_parts + row0 + lane] =
+                        make_float2(m, s);
+                continue;
             }
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
             tc_after_sync();
@@ -506,40 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     tmem_ld_wait();
                 }
             };
-            if constexpr (MODE == kPairLogits) {
-                float m = kMinusInf, s = 0.0f;
-#pragma unroll 1
-                for (int b = 0; b < blocks; ++b) {
-                    float v[32];
-                    values(b, v);
-                    if (b == blocks - 1 && !pieces) release();
-                    const int at = static_cast<int>(label.at) - 32 * b;
-                    const bool mine = label.at >= 32 * b && label.at < 32 * b + 32;
-                    if (__any_sync(0xFFFFFFFFu, mine)) {
-                        float z = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) z = i == at ? v[i] : z;
-                        if (mine) p.extra.head.at[row0 + lane] = z;
-                    }
-                    const int cols = g.N - col0 - 32 * b;
-                    if (cols < 32) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = i < cols ? v[i] : kMinusInf;
-                    }
-                    float top = m;
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) top = fmaxf(top, v[i]);
-                    const float base = top == kMinusInf ? 0.0f : top;
-                    s *= exp2_approx((m - base) * kLog2e);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) s += exp2_approx((v[i] - base) * kLog2e);
-                    m = top;
-                }
-                if (row0 + lane < g.M)
-                    p.extra.head.parts[static_cast<size_t>(col0 / 64) * p.extra.head.ld_parts + row0 + lane] =
-                        make_float2(m, s);
-                continue;
-            }
             if constexpr (MODE == kPairLogitGrad) {
 #pragma unroll 1
                 for (int b = 0; b < blocks; ++b) {
@@ -548,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     if (b == blocks - 1 && !pieces) release();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = exp2_approx((v[i] - lse) * kLog2e);
-                    const int at = static_cast<int>(label.at) - 32 * b;
+                    const int at = label.at - 32 * b;
                     const bool mine = label.at >= 32 * b && label.at < 32 * b + 32;
                     if (__any_sync(0xFFFFFFFFu, mine)) {
 #pragma unroll

@@ -33,6 +33,8 @@ struct PairSave8 {
     float *scales = nullptr;
     long long lds = 0;
 };
+// The k-blocks of 64 that one accumulator sums of the logits (see the pair product).
+constexpr int kLogitBlocks = 16;
 // The product's columns are the vocabulary's entries from v0 on.
 struct PairHead {
     const int64_t *labels = nullptr;

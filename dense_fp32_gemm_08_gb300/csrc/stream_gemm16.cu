@@ -216,13 +216,15 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     } else if (warp == 1) {
         if (lane == 0) {
             RingCursor<STAGES> ring;
-            int j = -1, kb = u0 % p.KB;
+            int j = -1, kb = u0 % p.KB, run = 0;
             bool ok = true;
             uint32_t d = tmem;
             for (int u = u0; u < u1 && ok; ++u) {
-                const bool first = u == u0 || kb == 0;
+                // A new accumulator per tile, and per run of blocks that one sums (see the pair product).
+                const bool first = u == u0 || kb == 0 || (MODE == kPairLogits && run == kLogitBlocks);
                 if (first) {
                     ++j;
+                    run = 0;
                     if (j >= 2 && !mbar_wait(&acc_free[j & 1], ((j >> 1) - 1) & 1)) break;
                     tc_after_sync();
                     d = tmem + static_cast<uint32_t>((j & 1) * NT);
@@ -239,7 +241,9 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 mma_commit_16<1>(&empty[ring.stage]);
                 ring.next();
                 if (++kb == p.KB) kb = 0;
-                if (kb == 0 || u + 1 == u1) mma_commit_16<1>(&acc_full[j & 1]);
+                ++run;
+                if (kb == 0 || u + 1 == u1 || (MODE == kPairLogits && run == kLogitBlocks))
+                    mma_commit_16<1>(&acc_full[j & 1]);
             }
         }
     } else if (warp >= 4) {
@@ -248,47 +252,50 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
         constexpr int COLS = NT / C::GROUPS;
         const int first_col = (warp - 4) / 4 * COLS;
         int j = 0;
-        for (int u = u0; u < u1; ++j) {
+        for (int u = u0; u < u1;) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
             const int n_units = min(p.KB - kb0, u1 - u);
             u += n_units;
             const int n = (C::TOKEN_TILES ? tile / p.m_tiles : tile) * kStreamRows + row;
             const int m0 = C::TOKEN_TILES ? tile % p.m_tiles * NT : 0, tokens = min(NT, p.M - m0);
             const float b = p.bias && n < p.N ? Half16<T>::widen(p.bias[n]) : 0.0f;
-            if (!mbar_wait(&acc_full[j & 1], (j >> 1) & 1)) break;
-            tc_after_sync();
-            const uint32_t acc = tmem + lane_base + static_cast<uint32_t>((j & 1) * NT);
             const bool whole = n_units == p.KB;
-#pragma unroll 1
-            for (int c = first_col; c < first_col + COLS; c += 16) {
-                uint32_t r[16];
-                tmem_ld_x16(acc + static_cast<uint32_t>(c), r);
+            static_assert(COLS == 16, "a warp's columns are one load");
+            uint32_t r[16];
+            bool ok = true;
+            for (int first = 0; first < n_units; first += MODE == kPairLogits ? kLogitBlocks : n_units, ++j) {
+                ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+                if (!ok) break;
+                tc_after_sync();
+                uint32_t more[16];
+                tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), more);
                 tmem_ld_wait();
-                if (c + 16 == first_col + COLS) {
-                    tc_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[j & 1]);
-                }
-                if (c >= tokens) continue;
-                if (whole) {
-                    float v[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T, MODE>(p, n, m0 + c, b, v);
-                } else {
-                    put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), c, row, tokens, r);
-                }
+                for (int i = 0; i < 16; ++i)
+                    r[i] = MODE == kPairLogits && first > 0
+                               ? __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(more[i]))
+                               : more[i];
+                tc_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_free[j & 1]);
             }
-            if (whole || first_col >= tokens ||
+            if (!ok) break;
+            if (first_col >= tokens) continue;
+            if (whole) {
+                float v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                finish16<T, MODE>(p, n, m0 + first_col, b, v);
+            } else {
+                put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), first_col, row, tokens, r);
+            }
+            if (whole ||
                 !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.KB, lane))
                 continue;
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
-#pragma unroll 1
-            for (int c = first_col; c < min(tokens, first_col + COLS); c += 16) {
-                float v[16];
-                sum_pieces<NT>(p.pieces, c0, c1, 1, 0, c, row, tokens, v);
-                finish16<T, MODE>(p, n, m0 + c, b, v);
-            }
+            float v[16];
+            sum_pieces<NT>(p.pieces, c0, c1, 1, 0, first_col, row, tokens, v);
+            finish16<T, MODE>(p, n, m0 + first_col, b, v);
         }
     }
 
