@@ -104,11 +104,17 @@ struct Item {
         product = t >= p.g[0].items ? 1 : 0;
         const PairProduct &g = p.g[product];
         if (product) t -= p.g[0].items;
-        tile = t / g.split;
-        piece = t - tile * g.split;
+        tile = t;
+        piece = kb0 = 0;
+        n = g.KB;
+        if (g.split > 1) {  // at most 8 pieces: the products below stay in 32 bits
+            const unsigned split = static_cast<unsigned>(g.split), blocks = static_cast<unsigned>(g.KB);
+            tile = static_cast<int>(static_cast<unsigned>(t) / split);
+            piece = t - tile * g.split;
+            kb0 = static_cast<int>(static_cast<unsigned>(piece) * blocks / split);
+            n = static_cast<int>((static_cast<unsigned>(piece) + 1u) * blocks / split) - kb0;
+        }
         tile_coords(tile, g.tiles_m, g.tiles_n, kGroupM, tm, tn);
-        kb0 = static_cast<int>(static_cast<long long>(piece) * g.KB / g.split);
-        n = static_cast<int>((piece + 1LL) * g.KB / g.split) - kb0;
     }
 };
 
