@@ -53,7 +53,7 @@ struct Coder8 {
         float a = Half16<T>::widen(static_cast<uint16_t>(top));
         finite = is_finite<T>(top);
         // 127 / a could overflow, or leave the range of the approximate division
-        lift = a < 1e-30f ? 18446744073709551616.0f : a > 1e30f ? 5.42101086e-20f : 1.0f;  // 2^64, 2^-64
+        lift = !finite || a > 1e30f ? 5.42101086e-20f : a < 1e-30f ? 18446744073709551616.0f : 1.0f;  // 2^-64, 2^64
         a *= lift;
         hi = __fdividef(127.0f, a);
         lo = __fdividef(fmaf(-hi, a, 127.0f), a);
@@ -61,22 +61,28 @@ struct Coder8 {
     }
     // Eight codes, two's complement, lowest byte first.
     __device__ __forceinline__ uint2 eight(const uint32_t (&w)[4]) const {
+        if (lift == 1.0f) return round8<false>(w);
+        return finite ? round8<true>(w) : make_uint2(0, 0);
+    }
+
+private:
+    template <bool LIFT>
+    __device__ __forceinline__ uint2 round8(const uint32_t (&w)[4]) const {
         uint32_t bits[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float2 f = Half16<T>::widen2(w[i]);
-            if (lift != 1.0f) {
-                f.x *= lift;
-                f.y *= lift;
-            }
+            if (LIFT) f = __fmul2_rn(f, make_float2(lift, lift));
+            const float2 q = __ffma2_rn(f, make_float2(hi, hi), __fmul2_rn(f, make_float2(lo, lo)));
             // 1.5 2^23: the sum's low bits are the nearest integer, ties to even
-            bits[2 * i] = __float_as_uint(fmaf(f.x, hi, f.x * lo) + 12582912.0f);
-            bits[2 * i + 1] = __float_as_uint(fmaf(f.y, hi, f.y * lo) + 12582912.0f);
+            const float2 m = __fadd2_rn(q, make_float2(12582912.0f, 12582912.0f));
+            bits[2 * i] = __float_as_uint(m.x);
+            bits[2 * i + 1] = __float_as_uint(m.y);
         }
         auto four = [](const uint32_t *b) {
             return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
         };
-        return finite ? make_uint2(four(bits), four(bits + 4)) : make_uint2(0, 0);
+        return make_uint2(four(bits), four(bits + 4));
     }
 };
 

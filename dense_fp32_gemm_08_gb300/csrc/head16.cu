@@ -20,12 +20,12 @@
 namespace sg {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.69314718055994531f;
-// Maximum and sum of exponentials of two parts together. (A part without finite logits has m = -inf, s = 0.)
+constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.904654e-9f;  // ln 2 in two parts
+// Maximum and sum of powers of 2 of two parts together. (A part without finite logits has m = -inf, s = 0.)
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
     const float base = m == -INFINITY ? 0.0f : m;
-    return make_float2(m, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
+    return make_float2(m, a.y * exp2_approx(a.x - base) + b.y * exp2_approx(b.x - base));
 }
 __device__ __forceinline__ float2 join_lanes(float2 a) {
 #pragma unroll
@@ -39,7 +39,7 @@ struct LossOut {
     int T, V;
     float *loss, *lse;
     __device__ __forceinline__ void put(int row, float2 a) const {
-        const float l = a.x + logf(a.y);
+        const float l = fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
         const int64_t label = labels[row];
         if (lse) lse[row] = l;
         if (loss) loss[row] = label >= 0 && label < V ? l - at[row] : 0.0f;

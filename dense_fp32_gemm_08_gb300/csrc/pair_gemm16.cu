@@ -90,7 +90,7 @@ struct PairParams {
     int z_tma;
     PairExtra extra;
     int sum_product;  // the product that adds to the sums (-1: none)
-    int q_vec;        // the codes' rows allow 16-byte stores
+    int q_tma;        // the codes' rows are addressable by TMA (its map is in the pre-activation's place)
 };
 struct PairMaps {
     CUtensorMap a[kMaxProducts], b[kMaxProducts], d[kMaxProducts], z;
@@ -270,33 +270,12 @@ __device__ __forceinline__ void add_residual(float (&v)[32], uint32_t (&raw)[20]
     __syncwarp();
 }
 
-// The codes of up to 32 values of a row.
-template <typename T>
-__device__ __forceinline__ void save_codes(const float (&v)[32], const Coder8<T> &coder, int8_t *q, bool vec,
-                                           int count) {
+// The codes of a row's block of 64 values, of which `count` belong to the matrix, one by one.
+__device__ __forceinline__ void put_codes(int8_t *q, const uint2 (&codes)[8], int count) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint2 codes[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = 16 * h + 8 * k + 2 * i;
-                w[i] = Half16<T>::narrow2(v[at], v[at + 1]);
-            }
-            codes[k] = coder.eight(w);
-        }
-        if (vec && count >= 16 * h + 16) {
-            *reinterpret_cast<uint4 *>(q + 16 * h) = make_uint4(codes[0].x, codes[0].y, codes[1].x, codes[1].y);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint64_t both = static_cast<uint64_t>(codes[k].y) << 32 | codes[k].x;
-                for (int i = 0; i < min(8, count - 16 * h - 8 * k); ++i)
-                    q[16 * h + 8 * k + i] = static_cast<int8_t>(both >> (8 * i));
-            }
-        }
+    for (int k = 0; k < 8; ++k) {
+        const uint64_t both = static_cast<uint64_t>(codes[k].y) << 32 | codes[k].x;
+        for (int i = 0; i < min(8, count - 8 * k); ++i) q[8 * k + i] = static_cast<int8_t>(both >> (8 * i));
     }
 }
 
@@ -466,29 +445,34 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             }
             RowLabel label(p.extra.head, MODE == kPairLogits || MODE == kPairLogitGrad ? row0 + lane : g.M,
                            g.M, col0);
-            float lse = 0.0f, dloss = 0.0f;
+            float lse2 = 0.0f, dloss = 0.0f;  // lse in units of log 2
             if (MODE == kPairLogitGrad && label.counts) {
-                lse = p.extra.head.lse[row0 + lane];
+                lse2 = p.extra.head.lse[row0 + lane] * kLog2e;
                 dloss = p.extra.head.factor ? factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd]
                                             : p.extra.head.unit;
             }
             if constexpr (MODE == kPairLogits) {
-                float v[64];
-#pragma unroll
-                for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                float2 v[32];
                 bool ok = true;
                 for (int kb = 0; kb < item.n; kb += kLogitBlocks, ++j) {
                     ok = ok && mbar_wait_cluster(&acc_full[j & 1], (j >> 1) & 1);
                     if (!ok) break;
                     tc_after_sync();
                     if (inside) {
+                        const uint32_t from = tmem + lane_base + static_cast<uint32_t>((j & 1) * kBN + c0);
+                        if (kb == 0) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t r[16];
-                            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * kBN + c0 + 16 * q), r);
+                            for (int q = 0; q < 2; ++q) tmem_ld_x32(from + 32 * q, reinterpret_cast<uint32_t(&)[32]>(v[16 * q]));
                             tmem_ld_wait();
+                        } else {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) v[16 * q + i] += __uint_as_float(r[i]);
+                            for (int q = 0; q < 4; ++q) {
+                                float2 r[8];
+                                tmem_ld_x16(from + 16 * q, reinterpret_cast<uint32_t(&)[16]>(r));
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[8 * q + i] = __fadd2_rn(v[8 * q + i], r[i]);
+                            }
                         }
                     }
                     tc_before_sync();
@@ -502,36 +486,55 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     constexpr size_t kPiece = 2ull * kBN * kBM;
                     const size_t at = static_cast<size_t>(g.piece0 + item.tile * g.split);
                     float *base = p.pieces + (2 * at + rank) * kBN * kBM + c0 * kBM + quarter * 32 + lane;
+                    float *mine = base + item.piece * kPiece;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) __stcg(base + item.piece * kPiece + i * kBM, v[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        __stcg(mine + 2 * i * kBM, v[i].x);
+                        __stcg(mine + (2 * i + 1) * kBM, v[i].y);
+                    }
                     unsigned int *counter =
                         p.counters + (2 * static_cast<size_t>(g.tile0 + item.tile) + rank) * kEpiWarps + w;
                     if (!piece_arrived(counter, 1, g.split, lane)) continue;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) v[i] = 0.0f;
+                    for (int i = 0; i < 32; ++i) v[i] = make_float2(0.0f, 0.0f);
                     for (int k = 0; k < g.split; ++k)
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) v[i] += __ldcg(base + k * kPiece + i * kBM);
+                        for (int i = 0; i < 32; ++i) {
+                            v[i].x += __ldcg(base + k * kPiece + 2 * i * kBM);
+                            v[i].y += __ldcg(base + k * kPiece + (2 * i + 1) * kBM);
+                        }
                 }
-                if (__any_sync(0xFFFFFFFFu, label.at >= 0 && label.at < 64)) {
+                const bool mine = label.at >= 0 && label.at < 64;
+                if (__any_sync(0xFFFFFFFFu, mine)) {
                     float z = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) z = label.at == i ? v[i] : z;
-                    if (label.at >= 0 && label.at < 64) p.extra.head.at[row0 + lane] = z;
+                    for (int i = 0; i < 32; ++i) {
+                        z = label.at == 2 * i ? v[i].x : z;
+                        z = label.at == 2 * i + 1 ? v[i].y : z;
+                    }
+                    if (mine) p.extra.head.at[row0 + lane] = z;
                 }
                 if (g.N - col0 < 64) {
 #pragma unroll
-                    for (int i = 0; i < 64; ++i) v[i] = i < g.N - col0 ? v[i] : kMinusInf;
+                    for (int i = 0; i < 32; ++i) {
+                        if (2 * i >= g.N - col0) v[i].x = kMinusInf;
+                        if (2 * i + 1 >= g.N - col0) v[i].y = kMinusInf;
+                    }
                 }
-                float m = kMinusInf, s = 0.0f;
+                float top = kMinusInf;
 #pragma unroll
-                for (int i = 0; i < 64; ++i) m = fmaxf(m, v[i]);
-                const float base = m == kMinusInf ? 0.0f : m;
+                for (int i = 0; i < 32; ++i) top = fmaxf(fmaxf(top, v[i].x), v[i].y);
+                // In units of log 2: 2^(z log2 e - m), the difference rounded once.
+                const float m = top * kLog2e, base = top == kMinusInf ? 0.0f : -m;
+                float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) s += exp2_approx((v[i] - base) * kLog2e);
+                for (int i = 0; i < 32; ++i) {
+                    const float2 t = __ffma2_rn(v[i], make_float2(kLog2e, kLog2e), make_float2(base, base));
+                    s = __fadd2_rn(s, make_float2(exp2_approx(t.x), exp2_approx(t.y)));
+                }
                 if (row0 + lane < g.M)
                     p.extra.head.parts[static_cast<size_t>(col0 / 64) * p.extra.head.ld_parts + row0 + lane] =
-                        make_float2(m, s);
+                        make_float2(m, s.x + s.y);
                 continue;
             }
             if (!mbar_wait_cluster(&acc_full[set], (j >> 1) & 1)) break;
@@ -590,16 +593,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     float v[32];
                     values(b, v);
                     if (b == blocks - 1 && !pieces) release();
+                    float2(&w2)[16] = reinterpret_cast<float2(&)[16]>(v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = exp2_approx((v[i] - lse) * kLog2e);
+                    for (int i = 0; i < 16; ++i) {
+                        const float2 t = __ffma2_rn(w2[i], make_float2(kLog2e, kLog2e), make_float2(-lse2, -lse2));
+                        w2[i] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+                    }
                     const int at = label.at - 32 * b;
-                    const bool mine = label.at >= 32 * b && label.at < 32 * b + 32;
-                    if (__any_sync(0xFFFFFFFFu, mine)) {
+                    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] -= mine && i == at ? 1.0f : 0.0f;
+                        for (int i = 0; i < 32; ++i) v[i] -= i == at ? 1.0f : 0.0f;
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = label.counts ? v[i] * dloss : 0.0f;
+                    for (int i = 0; i < 16; ++i) w2[i] = __fmul2_rn(w2[i], make_float2(dloss, dloss));
+                    if (__any_sync(0xFFFFFFFFu, !label.counts)) {  // (a selection: their values may not be finite)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = label.counts ? v[i] : 0.0f;
+                    }
                     if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
                     store_block<T>(v, buf, &maps.d[0], 1, g.D, g.ldd, g.M, g.N, row0, col0 + 32 * b, lane);
@@ -636,31 +646,65 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 continue;
             }
             auto add_bias = [&](int b, float(&v)[32]) {
-                if (p.bias) {
-                    const float mine = b ? bias[1] : bias[0];
+                if (!p.bias) return;
+                const float mine = b ? bias[1] : bias[0];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
-                }
+                for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(0xFFFFFFFFu, mine, i);
             };
-            // The checkpoint's block of 64 columns is this warp's share of the tile: its largest magnitude
-            // first, so that the values pass twice (out of TMEM, or the pieces).
-            uint32_t top = 0;
+            // The checkpoint's block of 64 columns is this warp's share of the tile: the pre-activation in 16
+            // bits is kept until its largest magnitude is known. (The sums pass again for the output, out of
+            // TMEM or the pieces: 32 more registers would not fit.)
             if constexpr (MODE == kPairSave8) {
-#pragma unroll 1
-                for (int b = 0; b < blocks; ++b) {
-                    float v[32];
-                    values(b, v);
-                    add_bias(b, v);
-                    const int cols = g.N - col0 - 32 * b;
+                uint32_t z[32], top = 0;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t w = Half16<T>::narrow2(v[2 * i], v[2 * i + 1]);
-                        top = magnitude2<T>(top, cols > 2 * i + 1 ? w : cols > 2 * i ? w & 0xFFFFu : 0u);
+                for (int b = 0; b < 2; ++b) {
+                    if (b < blocks) {
+                        float v[32];
+                        values(b, v);
+                        add_bias(b, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) z[16 * b + i] = Half16<T>::narrow2(v[2 * i], v[2 * i + 1]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) z[16 * b + i] = 0;
                     }
                 }
+                const int cols = g.N - col0;
+                if (cols < 64) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (2 * i >= cols) z[i] = 0;
+                        if (2 * i + 1 == cols) z[i] &= 0xFFFFu;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) top = magnitude2<T>(top, z[i]);
                 top = magnitude(top);
+                const Coder8<T> coder(top);
+                uint2 codes[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t w4[4] = {z[4 * k], z[4 * k + 1], z[4 * k + 2], z[4 * k + 3]};
+                    codes[k] = coder.eight(w4);
+                }
                 if (row0 + lane < g.M)
                     p.extra.save.scales[(row0 + lane) * p.extra.save.lds + col0 / kCheckpointBlock] = scale8<T>(top);
+                if (p.q_tma) {  // a row's 64 codes are as many bytes as 32 values
+                    if (lane == 0) bulk_wait_read<0>();
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(buf + store_chunk(lane, c)) =
+                            make_uint4(codes[2 * c].x, codes[2 * c].y, codes[2 * c + 1].x, codes[2 * c + 1].y);
+                    async_proxy_fence();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_2d(&maps.z, buf, col0, row0);
+                        bulk_commit();
+                    }
+                } else if (row0 + lane < g.M) {
+                    put_codes(p.extra.save.codes + (row0 + lane) * p.extra.save.ldq + col0, codes, min(64, cols));
+                }
             }
 #pragma unroll 1
             for (int b = 0; b < blocks; ++b) {
@@ -669,11 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 values(b, v);
                 if (b == blocks - 1 && !pieces) release();
                 add_bias(b, v);
-                if constexpr (MODE == kPairSave8) {
-                    if (row0 + lane < g.M)
-                        save_codes<T>(v, Coder8<T>(top), p.extra.save.codes + (row0 + lane) * p.extra.save.ldq + col,
-                                      p.q_vec != 0, g.N - col);
-                }
                 if (p.pre) {
                     if (lane == 0) bulk_wait_read<0>();
                     __syncwarp();
@@ -843,7 +882,14 @@ cudaError_t launch(const Gemm16 *list, int n, const PairExtra &extra, cudaStream
         p.counters = static_cast<unsigned int *>(sync);
     }
     p.extra = extra;
-    p.q_vec = (reinterpret_cast<uintptr_t>(extra.save.codes) & 15u) == 0 && extra.save.ldq % 16 == 0;
+    if (MODE == kPairSave8) {
+        // (As of the output: rows that end on 16 bytes.)
+        p.q_tma = (reinterpret_cast<uintptr_t>(extra.save.codes) & 15u) == 0 && extra.save.ldq % 16 == 0 && list[0].N % 16 == 0;
+        if (p.q_tma && !tensor_map_8(&maps.z, extra.save.codes, list[0].N, list[0].M, extra.save.ldq, 64, 32)) {
+            *detail = "cuTensorMapEncodeTiled rejected a matrix";
+            return cudaErrorInvalidValue;
+        }
+    }
     p.sum_product = MODE == kPairSum && extra.sum.sums ? order[0] : -1;  // list[0]
     if (n == 1) {
         const Gemm16 &g = list[0];
@@ -921,20 +967,32 @@ EncodeTiledFn encode_fn() {
 }
 }  // namespace
 
-bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,
-                   long long ld, int box_cols, int box_rows, bool narrow, long long depth,
-                   long long stride) {
+namespace {
+// rows x cols values of `bytes` each, or depth > 0 such matrices.
+bool tensor_map(CUtensorMap *map, CUtensorMapDataType type, int bytes, const void *base, long long cols, long long rows,
+                long long ld, int box_cols, int box_rows, bool narrow, long long depth, long long stride) {
     const EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
                                 static_cast<cuuint64_t>(depth)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * bytes, static_cast<cuuint64_t>(stride) * bytes};
     const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return enc(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-               depth > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE,
-               narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return enc(map, type, depth > 0 ? 3 : 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,
+                   long long ld, int box_cols, int box_rows, bool narrow, long long depth,
+                   long long stride) {
+    return tensor_map(map, dtype == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base,
+                      cols, rows, ld, box_cols, box_rows, narrow, depth, stride);
+}
+bool tensor_map_8(CUtensorMap *map, const void *base, long long cols, long long rows, long long ld, int box_cols,
+                  int box_rows) {
+    return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, cols, rows, ld, box_cols, box_rows, true, 0, 0);
 }
 
 }  // namespace sg

@@ -13,6 +13,9 @@ namespace sg {
 bool tensor_map_16(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,
                    long long ld, int box_cols, int box_rows, bool narrow = false, long long depth = 0,
                    long long stride = 0);
+// Of a matrix of bytes, with the 64-byte swizzle.
+bool tensor_map_8(CUtensorMap *map, const void *base, long long cols, long long rows, long long ld, int box_cols,
+                  int box_rows);
 
 // One grid over the tiles of one or two products (of two, the epilogue is the plain store: no
 // bias, activation, residual or pre-activation). A and B must satisfy tma_rows; K > 0. The other
@@ -39,7 +42,7 @@ constexpr int kLogitBlocks = 16;
 struct PairHead {
     const int64_t *labels = nullptr;
     int V = 0, v0 = 0;
-    // kPairLogits: of 64 columns' logits of a row, the largest m and the sum of exp(z - m), at
+    // kPairLogits: of 64 columns' logits z log2(e) of a row, the largest m and the sum of 2^(z log2(e) - m), at
     // parts[(column / 64) * ld_parts + row]; and the row's logit at its label. The streaming product: of
     // 32 columns' logits, at parts[row * ld_parts + column / 32].
     float2 *parts = nullptr;

@@ -79,7 +79,8 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
             float m = z;
 #pragma unroll
             for (int s = 16; s > 0; s /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-            float e = exp2_approx((z - (m == -INFINITY ? 0.0f : m)) * kLog2e);
+            m *= kLog2e;
+            float e = exp2_approx(fmaf(z, kLog2e, m == -INFINITY ? 0.0f : -m));
 #pragma unroll
             for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
             if (lane == 0) p.head.parts[(m0 + i) * p.head.ld_parts + n / 32] = make_float2(m, e);
@@ -95,7 +96,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
             float dz = 0.0f;
             if (label >= 0 && label < p.head.V) {
                 const float dloss = p.head.factor ? *p.head.factor * p.head.dloss[(m0 + i) * p.head.incd] : p.head.unit;
-                dz = (exp2_approx((v[i] - p.head.lse[m0 + i]) * kLog2e) - (label == p.head.v0 + n ? 1.0f : 0.0f)) * dloss;
+                dz = (exp2_approx(fmaf(v[i], kLog2e, -(p.head.lse[m0 + i] * kLog2e))) - (label == p.head.v0 + n ? 1.0f : 0.0f)) * dloss;
             }
             p.D[(m0 + i) * p.ldd + n] = H::narrow(dz);
         }
