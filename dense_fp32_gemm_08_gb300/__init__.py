@@ -13,7 +13,6 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
-from typing import Any, NamedTuple
 
 __all__ = [
     "SgemmError", "library_path", "lib", "sgemm", "sgemm_strided_batched", "sgemm_3xtf32",
@@ -337,16 +336,13 @@ def _side_stream(torch, device, queue):
     return torch.cuda.ExternalStream(queue, device=device)
 
 
-def _empty(torch, side, shape, dtype, device, ld=None):
+def _empty(torch, side, shape, dtype, device):
     """An output. On a side stream its memory comes from that stream's pool, so that no pending work
-    of the current stream still uses it, and is kept while the current stream may use it. With `ld` its
-    rows are that far apart."""
+    of the current stream still uses it, and is kept while the current stream may use it."""
     if side is None:
-        if ld is not None:
-            return torch.empty_strided(shape, (ld, 1), dtype=dtype, device=device)
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(side):
-        t = _empty(torch, None, shape, dtype, device, ld)
+        t = torch.empty(shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(device))
     return t
 
@@ -588,44 +584,74 @@ def _weight_shape(weight, transw):
     return (a, b, op) if op == SGEMM_OP_T else (b, a, op)
 
 
-class Checkpoint8(NamedTuple):
-    """A matrix of 16-bit values kept in 8 bits: int8 codes, a float32 scale for each 64 columns of a
-    row, and the type that it is restored to (include/sgemm.h has the format)."""
-    codes: Any
-    scale: Any
-    dtype: Any
+class Checkpoint8:
+    """A matrix of 16-bit values kept in 8 bits: int8 ``codes``, a float32 ``scale`` for each 64 columns
+    of a row, and the type that it is restored to (include/sgemm.h has the format). One that this
+    library made has both in one buffer, of which ``codes`` and ``scale`` are views."""
+    __slots__ = ("shape", "dtype", "device", "_codes", "_scale", "_buffer", "_ldq")
+
+    def __init__(self, codes, scale, dtype):
+        self.shape, self.dtype, self.device = tuple(codes.shape), dtype, codes.device
+        self._codes, self._scale, self._buffer, self._ldq = codes, scale, None, 0
+
+    @classmethod
+    def _make(cls, torch, side, rows, cols, dtype, device):
+        """A new one, codes in rows of whole 16 bytes; its scales follow them."""
+        self = cls.__new__(cls)
+        ldq = (cols + 15) // 16 * 16
+        self.shape, self.dtype, self.device, self._codes, self._ldq = (rows, cols), dtype, device, None, ldq
+        self._buffer = _empty(torch, side, (rows * (ldq + (cols + 63) // 64 * 4),), torch.int8, device)
+        return self
+
+    def _views(self):
+        rows, cols = self.shape
+        at = rows * self._ldq
+        self._codes = self._buffer[:at].view(rows, self._ldq)[:, :cols]
+        self._scale = self._buffer[at:].view(_torch.float32).view(rows, (cols + 63) // 64)
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        if self._codes is None:
+            self._views()
+        return self._codes
 
+    @property
+    def scale(self):
+        if self._codes is None:
+            self._views()
+        return self._scale
 
-def _new_checkpoint(torch, side, rows, cols, dtype, device):
-    """A checkpoint with codes in rows of whole 16 bytes, and its (codes, ldq, scale, lds)."""
-    ldq, blocks = (cols + 15) // 16 * 16 or 1, (cols + 63) // 64
-    codes = _empty(torch, side, (rows, cols), torch.int8, device, ldq)
-    scale = _empty(torch, side, (rows, blocks), torch.float32, device)
-    return Checkpoint8(codes, scale, dtype), (codes.data_ptr(), ldq, scale.data_ptr(), blocks or 1)
+    def __repr__(self):
+        return f"Checkpoint8(shape={self.shape}, dtype={self.dtype}, device={self.device})"
 
+    def _tensors(self):
+        return (self._codes, self._scale) if self._buffer is None else (self._buffer,)
 
-def _codes(c, rows, cols, dtype, device, what):
-    """(codes, ldq, scale, lds) of a rows x cols checkpoint of the call's type and device."""
-    blocks = -(-cols // 64)
-    if c.codes.shape != (rows, cols) or c.scale.shape != (rows, blocks):
-        raise ValueError(f"{what} must be a checkpoint of shape {(rows, cols)}, got codes "
-                         f"{tuple(c.codes.shape)} and scales {tuple(c.scale.shape)}")
-    if c.dtype is not dtype:
-        raise TypeError(f"{what} is a checkpoint of {c.dtype}: every matrix of a call has one 16-bit type")
-    if c.codes.dtype is not _torch.int8 or c.scale.dtype is not _torch.float32:
-        raise TypeError(f"{what}: a checkpoint has int8 codes and float32 scales")
-    if c.codes.device != device or c.scale.device != device:
-        raise ValueError("the tensors of a call must be on one device")
-    (ldq, inner_q), (lds, inner_s) = c.codes.stride(), c.scale.stride()
-    if (inner_q != 1 and cols > 1) or (inner_s != 1 and blocks > 1):
-        raise ValueError(f"{what}: rows must be contiguous")
-    if rows <= 1:
-        ldq, lds = max(ldq, cols, 1), max(lds, blocks, 1)
-    return c.codes.data_ptr(), ldq, c.scale.data_ptr(), lds
+    def _pointers(self, rows, cols, dtype, device, what):
+        """(codes, ldq, scale, lds) of a rows x cols checkpoint of the call's type and device."""
+        blocks = (cols + 63) // 64
+        if self.shape != (rows, cols):
+            raise ValueError(f"{what} must be a checkpoint of shape {(rows, cols)}, got {self.shape}")
+        if self.dtype is not dtype:
+            raise TypeError(f"{what} is a checkpoint of {self.dtype}: every matrix of a call has one 16-bit type")
+        if self._buffer is not None:
+            if self.device != device:
+                raise ValueError("the tensors of a call must be on one device")
+            at = self._buffer.data_ptr()
+            return at, self._ldq or 1, at + rows * self._ldq, blocks or 1
+        codes, scale = self._codes, self._scale
+        if scale.shape != (rows, blocks):
+            raise ValueError(f"{what}: scales must have shape {(rows, blocks)}, got {tuple(scale.shape)}")
+        if codes.dtype is not _torch.int8 or scale.dtype is not _torch.float32:
+            raise TypeError(f"{what}: a checkpoint has int8 codes and float32 scales")
+        if codes.device != device or scale.device != device:
+            raise ValueError("the tensors of a call must be on one device")
+        (ldq, inner_q), (lds, inner_s) = codes.stride(), scale.stride()
+        if (inner_q != 1 and cols > 1) or (inner_s != 1 and blocks > 1):
+            raise ValueError(f"{what}: rows must be contiguous")
+        if rows <= 1 or cols == 0:
+            ldq, lds = max(ldq, cols, 1), max(lds, blocks, 1)
+        return codes.data_ptr(), ldq, scale.data_ptr(), lds
 
 
 def checkpoint8(x, stream=None):
@@ -637,10 +663,10 @@ def checkpoint8(x, stream=None):
     M, N = x.shape
     px, ldx = _matrix(x, M, N, dtype, device, "x")
     queue, side = _queue(torch, device, stream)
-    c, saved = _new_checkpoint(torch, side, M, N, dtype, device)
+    c = Checkpoint8._make(torch, side, M, N, dtype, device)
     if side is not None:
         _in_use(side, x)
-    status = (_lib or lib()).sgemm_checkpoint8(code, M, N, px, ldx, *saved, queue)
+    status = (_lib or lib()).sgemm_checkpoint8(code, M, N, px, ldx, *c._pointers(M, N, dtype, device, "x"), queue)
     if status:
         _check(status)
     return c
@@ -649,14 +675,14 @@ def checkpoint8(x, stream=None):
 def restore8(checkpoint, stream=None):
     """torch convenience: the matrix that a ``Checkpoint8`` stands for, in its 16-bit type."""
     torch, dtype, device, code = _begin(checkpoint)
-    if checkpoint.codes.dim() != 2 or checkpoint.scale.dim() != 2:
-        raise ValueError("a checkpoint's codes and scales must be 2-D")
-    M, N = checkpoint.codes.shape
-    saved = _codes(checkpoint, M, N, dtype, device, "the argument")
+    if len(checkpoint.shape) != 2:
+        raise ValueError("a checkpoint's codes must be 2-D")
+    M, N = checkpoint.shape
+    saved = checkpoint._pointers(M, N, dtype, device, "the argument")
     queue, side = _queue(torch, device, stream)
     x = _empty(torch, side, (M, N), dtype, device)
     if side is not None:
-        _in_use(side, checkpoint.codes, checkpoint.scale)
+        _in_use(side, *checkpoint._tensors())
     status = (_lib or lib()).sgemm_restore8(code, M, N, *saved, x.data_ptr(), max(N, 1), queue)
     if status:
         _check(status)
@@ -693,7 +719,7 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
         out, ldy = _empty(torch, side, (M, N), dtype, device), max(N, 1)
         py = out.data_ptr()
     if save_pre == "8bit":
-        pre, saved = _new_checkpoint(torch, side, M, N, dtype, device)
+        pre = Checkpoint8._make(torch, side, M, N, dtype, device)
     elif save_pre:
         pre = _empty(torch, side, (M, N), dtype, device)
         pz = pre.data_ptr()
@@ -701,7 +727,8 @@ def linear(x, weight, bias=None, act="none", residual=None, transw="T", save_pre
         _in_use(side, x, weight, bias, residual, out)
     if save_pre == "8bit":
         status = (_lib or lib()).sgemm_linear_checkpoint8(code, op, M, N, K, px, ldx, pw, ldw, pb, _act_code(act),
-                                                          pr, ldr, py, ldy, *saved, queue)
+                                                          pr, ldr, py, ldy,
+                                                          *pre._pointers(M, N, dtype, device, "pre"), queue)
         if status:
             _check(status)
         return out, pre
@@ -726,9 +753,10 @@ def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=Tru
     torch, dtype, device, code = _begin(x)
     N, K, op = _weight_shape(weight, transw)
     if saved:
-        M = x.codes.shape[0]
-        px8 = _codes(x, M, K, dtype, device, "x")
-        pz8 = (None, max(N, 1), None, max(-(-N // 64), 1)) if pre is None else _codes(pre, M, N, dtype, device, "pre")
+        M = x.shape[0]
+        px8 = x._pointers(M, K, dtype, device, "x")
+        pz8 = ((None, max(N, 1), None, max(-(-N // 64), 1)) if pre is None
+               else pre._pointers(M, N, dtype, device, "pre"))
     else:
         M = x.shape[0]
         px, ldx = _matrix(x, M, K, dtype, device, "x")
@@ -747,7 +775,7 @@ def linear_backward(dy, x, weight, pre=None, act="none", transw="T", need_dx=Tru
         db = _empty(torch, side, (N,), torch.float32, device)
         pb_out = db.data_ptr()
     if side is not None:
-        _in_use(side, dy, weight, *((*x[:2], *(pre[:2] if pre else ())) if saved else (x, pre)))
+        _in_use(side, dy, weight, *((*x._tensors(), *(pre._tensors() if pre else ())) if saved else (x, pre)))
     if saved:
         status = (_lib or lib()).sgemm_linear_backward_checkpoint8(
             code, op, M, N, K, pg, ldg, *pz8, _act_code(act), *px8, pw, ldw, px_out, max(K, 1), pw_out,

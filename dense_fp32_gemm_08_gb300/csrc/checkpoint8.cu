@@ -166,8 +166,8 @@ __device__ __forceinline__ void restore8_aligned_rows(const Restore8 &c, int row
 #pragma unroll
     for (int i = 0; i < kRestoreRows; ++i)
         if (i < rows) {
-            const uint2 a = restore4<T>(codes[i].x, scale[i], scale[i], scale[i], scale[i]);
-            const uint2 b = restore4<T>(codes[i].y, scale[i], scale[i], scale[i], scale[i]);
+            const float2 s2 = make_float2(scale[i], scale[i]);
+            const uint2 a = restore4<T>(codes[i].x, s2, s2), b = restore4<T>(codes[i].y, s2, s2);
             *reinterpret_cast<uint4 *>(x + i * x_step) = make_uint4(a.x, a.y, b.x, b.y);
         }
 }
@@ -209,13 +209,15 @@ __device__ __forceinline__ void restore8_any_rows(const Restore8 &c, int row0, l
             const uint32_t lo = __funnelshift_r(w0, w1, 8 * (at & 3)), hi = __funnelshift_r(w1, w2, 8 * (at & 3));
             const int border = kCheckpointBlock - (col & (kCheckpointBlock - 1));  // columns of the first scale
             auto of = [&](int k) { return k < border ? scale[i][0] : scale[i][1]; };
-            const uint2 a = restore4<T>(lo, of(0), of(1), of(2), of(3)), b = restore4<T>(hi, of(4), of(5), of(6), of(7));
+            auto two = [&](int k) { return make_float2(of(k), of(k + 1)); };
+            const uint2 a = restore4<T>(lo, two(0), two(2)), b = restore4<T>(hi, two(4), two(6));
             *reinterpret_cast<uint4 *>(x + i * x_step + col) = make_uint4(a.x, a.y, b.x, b.y);
         } else {
             for (int k = max(0, -col); k < min(8, c.N - col); ++k) {
                 const uint32_t code = static_cast<uint8_t>(q[i * q_step + col + k]);
                 const float v = s[i * s_step + (col + k) / kCheckpointBlock];
-                x[i * x_step + col + k] = static_cast<uint16_t>(restore4<T>(code, v, v, v, v).x);
+                x[i * x_step + col + k] =
+                    static_cast<uint16_t>(restore4<T>(code, make_float2(v, v), make_float2(v, v)).x);
             }
         }
     }

@@ -86,18 +86,16 @@ private:
     }
 };
 
-// The value of code k (0..3) of a word, times the scale. (The bytes, made unsigned, become the low bits of
-// 2^23 + byte; the difference is exact.)
-template <int K>
-__device__ __forceinline__ float decode8(uint32_t word_biased, float scale) {
-    return (__uint_as_float(__byte_perm(word_biased, 0x4B000000u, 0x7540 + K)) - 8388736.0f) * scale;
-}
-// The restored values of four codes, in 16 bits.
+// The restored values of four codes, in 16 bits: the bytes, made unsigned, become the low bits of 2^23 +
+// byte, from which the difference is exact.
 template <typename T>
-__device__ __forceinline__ uint2 restore4(uint32_t word, float s0, float s1, float s2, float s3) {
+__device__ __forceinline__ uint2 restore4(uint32_t word, float2 s01, float2 s23) {
     const uint32_t b = word ^ 0x80808080u;
-    return make_uint2(Half16<T>::narrow2(decode8<0>(b, s0), decode8<1>(b, s1)),
-                      Half16<T>::narrow2(decode8<2>(b, s2), decode8<3>(b, s3)));
+    auto at = [&](int k) { return __uint_as_float(__byte_perm(b, 0x4B000000u, 0x7540 + k)); };
+    const float2 bias = make_float2(-8388736.0f, -8388736.0f);  // 2^23 + 128
+    const float2 lo = __fmul2_rn(__fadd2_rn(make_float2(at(0), at(1)), bias), s01);
+    const float2 hi = __fmul2_rn(__fadd2_rn(make_float2(at(2), at(3)), bias), s23);
+    return make_uint2(Half16<T>::narrow2(lo.x, lo.y), Half16<T>::narrow2(hi.x, hi.y));
 }
 
 }  // namespace sg

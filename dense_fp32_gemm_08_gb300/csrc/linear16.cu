@@ -117,7 +117,7 @@ template <typename T, int ACT, bool VEC, bool Z8>
 __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, long long r1, int c,
                                               int count, float (&sum)[8]) {
     using H = Half16<T>;
-    constexpr int UNROLL = VEC ? 4 : 2;
+    constexpr int UNROLL = VEC && !Z8 ? 4 : 2;
     for (long long r = r0; r < r1; r += 8 * UNROLL) {
         constexpr int W = VEC ? 4 : 5;
         uint32_t dy[UNROLL][W], z[UNROLL][Z8 ? 1 : W];
@@ -140,8 +140,8 @@ __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, lo
             uint32_t d4[4], z4[4] = {};
             align8_row<VEC>(d4, dy[i], g.dy + (r + 8 * i) * g.lddy + c);
             if constexpr (Z8) {
-                const float s = scale[i];
-                const uint2 lo = restore4<T>(codes[i].x, s, s, s, s), hi = restore4<T>(codes[i].y, s, s, s, s);
+                const float2 s = make_float2(scale[i], scale[i]);
+                const uint2 lo = restore4<T>(codes[i].x, s, s), hi = restore4<T>(codes[i].y, s, s);
                 z4[0] = lo.x;
                 z4[1] = lo.y;
                 z4[2] = hi.x;
@@ -171,9 +171,13 @@ __device__ __forceinline__ void act_grad_rows(const ActGrad &g, long long r0, lo
     }
 }
 
+// CTAs per SM. (16384 x 14336 bf16 with GELU from codes, two rows in flight and four CTAs: 229 us; four rows and three
+// CTAs, which spill: 313.)
+__host__ __device__ constexpr int grad_ctas(bool vec, bool z8) { return vec && z8 ? 4 : 3; }
+
 // VEC: dy and a 16-bit z allow 16-byte loads (and N is a multiple of 8).
 template <typename T, bool VEC, bool Z8>
-__global__ void __launch_bounds__(256, 3) act_grad_kernel(const ActGrad g, int rows, float *part,
+__global__ void __launch_bounds__(256, grad_ctas(VEC, Z8)) act_grad_kernel(const ActGrad g, int rows, float *part,
                                                        unsigned int *counters) {
     __shared__ __align__(16) float sums[8][kGradCols];
     __shared__ unsigned int arrived;
@@ -356,7 +360,7 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
     } else {
         const bool vec = g.N % 8 == 0 && tma_rows(g.dy, g.lddy) &&
                          (g.act == kActNone || g.zq || tma_rows(g.z, g.ldz));
-        // Rows per CTA, in whole steps: about whole rounds of the CTAs that run at once, three per SM, with 256
+        // Rows per CTA, in whole steps: about whole rounds of the CTAs that run at once, with 256
         // rows or so at most (a short last round) and a step at least (the last CTA of a column
         // block adds the sums of all of them). db alone, 2048 x 2048: 18.0 us with 8 rows, 9.5 with 32;
         // 4095 x 3001 unaligned: 49 us with 8 rows, 24.8 with 88 (1.2 rounds), 19.2 with 112 (one).
@@ -369,7 +373,7 @@ cudaError_t act_grad_launch(const ActGrad &g, cudaStream_t stream, const char **
             *detail = "device query failed";
             return err;
         }
-        const long long resident = 3LL * sms;
+        const long long resident = 3LL * sms;  // (from codes too: db is then the same sum in the same order)
         const long long rounds = g.M / std::max<long long>(1, resident / blocks) / 256 + 1;
         const long long want = std::max<long long>(1, rounds * resident / blocks);
         long long rows = std::max(step, (g.M / want + step / 2) / step * step);

@@ -119,15 +119,21 @@ def test_python_shapes_and_types(sgemm_lib):
     with pytest.raises(ValueError):
         sg.linear(x, w, save_pre="16bit")
     codes, scale = torch.zeros(3, 8, dtype=torch.int8), torch.zeros(3, 1)
-    good = sg.Checkpoint8(codes, scale, torch.bfloat16)
-    for bad in (good._replace(scale=torch.zeros(3, 2)), good._replace(scale=f)):
+
+    def checkpoint(codes=codes, scale=scale, dtype=torch.bfloat16):
+        return sg.Checkpoint8(codes, scale, dtype)
+
+    assert checkpoint().shape == (3, 8) and checkpoint().codes is codes and checkpoint().scale is scale
+    for bad in (checkpoint(scale=torch.zeros(3, 2)), checkpoint(scale=f), checkpoint(codes=codes[0]),
+                checkpoint(codes=torch.zeros(8, 3, dtype=torch.int8).t())):
         with pytest.raises(ValueError):
             sg.restore8(bad)
-    for bad in (good._replace(codes=codes.to(torch.uint8)), good._replace(scale=scale.double()), good._replace(dtype=torch.float32)):
+    for bad in (checkpoint(codes=codes.to(torch.uint8)), checkpoint(scale=scale.double()), checkpoint(dtype=torch.float32),
+                checkpoint()):  # (the last: on the host)
         with pytest.raises(TypeError):
             sg.restore8(bad)
     dy = torch.zeros(3, 5, dtype=torch.bfloat16)
     with pytest.raises(TypeError):  # a checkpoint of another type
-        sg.linear_backward(dy, good._replace(dtype=torch.float16), w)
+        sg.linear_backward(dy, checkpoint(dtype=torch.float16), w)
     with pytest.raises(ValueError):  # of another shape
-        sg.linear_backward(dy, good._replace(codes=codes[:2], scale=scale[:2]), w)
+        sg.linear_backward(dy, checkpoint(codes[:2], scale[:2]), w)
