@@ -42,7 +42,6 @@
 #include "checkpoint8.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
-#include "raster.cuh"
 #include "stream16.cuh"
 
 #include <algorithm>
@@ -67,6 +66,7 @@ static_assert(kSmem <= 227 * 1024, "ring and store buffers fit in shared memory"
 struct PairProduct {
     int M, N, KB;  // KB: k-blocks
     int tiles_m, tiles_n, split, items;  // items: tiles x split pieces along k
+    unsigned long long by_width, by_rest;  // 2^64 / (tiles of a raster group), / (tile rows of the last one), plus 1
     int piece0, tile0;                   // first piece and first counted tile in scratch (split > 1)
     int a_mn, b_mn;
     uint32_t idesc;
@@ -114,7 +114,11 @@ struct Item {
             kb0 = static_cast<int>(static_cast<unsigned>(piece) * blocks / split);
             n = static_cast<int>((static_cast<unsigned>(piece) + 1u) * blocks / split) - kb0;
         }
-        tile_coords(tile, g.tiles_m, g.tiles_n, kGroupM, tm, tn);
+        // The grouped raster (raster.cuh) without its divisions: every role decodes each tile between two others.
+        const int group = static_cast<int>(__umul64hi(static_cast<unsigned>(tile), g.by_width));
+        const int in = tile - group * kGroupM * g.tiles_n, rows = min(g.tiles_m - group * kGroupM, kGroupM);
+        tn = rows == kGroupM ? in / kGroupM : rows == 1 ? in : static_cast<int>(__umul64hi(static_cast<unsigned>(in), g.by_rest));
+        tm = group * kGroupM + in - tn * rows;
     }
 };
 
@@ -841,6 +845,9 @@ cudaError_t launch(const Gemm16 *list, int n, const PairExtra &extra, cudaStream
         }
         q.split = 1;
         q.items = static_cast<int>(tiles);
+        const unsigned rest = static_cast<unsigned>(q.tiles_m) % kGroupM;
+        q.by_width = ~0ULL / (static_cast<unsigned long long>(kGroupM) * static_cast<unsigned>(q.tiles_n)) + 1;
+        q.by_rest = rest > 1 ? ~0ULL / rest + 1 : 0;
         q.a_mn = g.a_mn;
         q.b_mn = g.b_mn;
         q.idesc = idesc_16(256, kBN, Half16<T>::kind, g.a_mn, g.b_mn);
