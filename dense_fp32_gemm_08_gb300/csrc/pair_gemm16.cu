@@ -336,9 +336,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     grid_dependents();  // after the TMEM allocation: a later kernel's CTA cannot take it first
     grid_dependency();
 
+    // The copies and the MMAs are each issued by one lane among 16 busy epilogue warps: what a k-block costs
+    // them is kept to few instructions (a division by the number of stages, barrier addresses and descriptors
+    // made anew took 2% of 16384 x 14336 x 4096).
     if (warp == 0) {
         if (lane == 0) {
             int it = 0;
+            RingCursor<kStages> ring;
+            const uint32_t full0 = map_to_rank(&full[0], 0);
             bool ok = true;
             for (int t = pair; t < p.total_items && ok; t += pairs) {
                 const Item item(p, t);
@@ -347,15 +352,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const int n0 = item.tn * kBN + static_cast<int>(rank) * (kBN / 2);
                 auto blocks = [&](auto a_layout, auto b_layout) {
                     constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
-                    for (int kb = item.kb0; kb < item.kb0 + item.n; ++kb, ++it) {
-                        const int s = it % kStages, k0 = kb * kBK;
-                        if (it >= kStages && !mbar_wait_cluster(&empty[s], ((it / kStages) - 1) & 1)) {
+                    int k0 = item.kb0 * kBK;
+                    for (int kb = 0; kb < item.n; ++kb, ++it, k0 += kBK) {
+                        const int s = ring.stage;
+                        // (A new barrier counts as past its odd phase: the first round does not wait.)
+                        if (!mbar_wait_cluster(&empty[s], ring.parity ^ 1u)) {
                             ok = false;
                             break;
                         }
                         uint8_t *sa = smem + s * kStageBytes, *sb = sa + kPartBytes;
                         if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-                        const uint32_t bar = map_to_rank(&full[s], 0);
+                        const uint32_t bar = full0 + 8u * static_cast<uint32_t>(s);
+                        ring.next();
                         if (a_mn) {
                             tma_load_2d_pair(sa, ma, bar, m0, k0);
                             tma_load_2d_pair(sa + 8192, ma, bar, m0 + 64, k0);
@@ -380,7 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            int it = 0, j = 0;
+            int j = 0;
+            RingCursor<kStages> ring;
+            const uint32_t smem0 = smem_addr(smem);
             bool ok = true;
             for (int t = pair; t < p.total_items && ok; t += pairs) {
                 const Item item(p, t);
@@ -397,22 +407,26 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     const int KB = min(run_blocks(MODE, item.n), item.n - kb0);
                     auto blocks = [&](auto a_layout, auto b_layout) {
                         constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
-                        for (int kb = 0; kb < KB; ++kb, ++it) {
-                            const int s = it % kStages;
-                            if (!mbar_wait_cluster(&full[s], (it / kStages) & 1)) {
+                        // Descriptors of stage 0; their start addresses count 16 bytes.
+                        const uint64_t a0 = a_mn ? desc_mn_major(smem0, 8192) : desc_k_major(smem0);
+                        const uint64_t b0 = b_mn ? desc_mn_major(smem0 + kPartBytes, 8192) : desc_k_major(smem0 + kPartBytes);
+                        uint32_t more = 0;  // adds to the accumulator from the second step on
+                        for (int kb = 0; kb < KB; ++kb) {
+                            if (!mbar_wait_cluster(&full[ring.stage], ring.parity)) {
                                 ok = false;
                                 break;
                             }
                             tc_after_sync();
-                            const uint32_t sa = smem_addr(smem + s * kStageBytes), sb = sa + kPartBytes;
-                            const uint64_t da = a_mn ? desc_mn_major(sa, 8192) : desc_k_major(sa);
-                            const uint64_t db = b_mn ? desc_mn_major(sb, 8192) : desc_k_major(sb);
+                            const uint64_t at = static_cast<uint64_t>(ring.stage) * (kStageBytes >> 4);
+                            const uint64_t da = a0 + at, db = b0 + at;
 #pragma unroll
-                            for (int k = 0; k < kBK / 16; ++k)  // start addresses count 16 bytes: a
-                                mma_16<2>(d, da + static_cast<uint64_t>(k * (a_mn ? 128 : 2)),  // k-step is
-                                          db + static_cast<uint64_t>(k * (b_mn ? 128 : 2)),     // 32 bytes
-                                          idesc, kb > 0 || k > 0);  // of a row or 16 rows
-                            mma_commit_16<2>(&empty[s]);
+                            for (int k = 0; k < kBK / 16; ++k) {  // a k-step: 32 bytes of a row or 16 rows
+                                mma_16<2>(d, da + static_cast<uint64_t>(k * (a_mn ? 128 : 2)),
+                                          db + static_cast<uint64_t>(k * (b_mn ? 128 : 2)), idesc, more);
+                                more = 1;
+                            }
+                            mma_commit_16<2>(&empty[ring.stage]);
+                            ring.next();
                         }
                     };
                     with_layout(p.g[i], blocks);
