@@ -39,8 +39,17 @@ struct StreamParams {
     long long ldz;
     unsigned int *counters;  // [tiles][epilogue warps], zero between calls
     float *pieces;           // [2 * CTAs][NT / 4][128][4]
+};
+// What the head's products have besides (the layers' kernels carry no more parameters than they use).
+template <int MODE>
+struct StreamMore {
     PairHead head;
     PairSum sum;
+    explicit StreamMore(const PairExtra &x) : head(x.head), sum(x.sum) {}
+};
+template <>
+struct StreamMore<kPairLayer> {
+    explicit StreamMore(const PairExtra &) {}
 };
 
 template <int NT>
@@ -65,7 +74,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // 16 columns (tokens m0 .. m0 + 15) of output feature n; a warp has 32 features in order.
 template <typename T, int MODE>
-__device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, float b, float (&v)[16]) {
+__device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore<MODE> &more, int n, int m0,
+                                         float b, float (&v)[16]) {
     using H = Half16<T>;
     const int rows = min(16, p.M - m0);
     if constexpr (MODE == kPairLogits) {
@@ -74,7 +84,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (i >= rows) break;
-            if (p.head.labels[m0 + i] == n && n < p.N) p.head.at[m0 + i] = v[i];
+            if (more.head.labels[m0 + i] == n && n < p.N) more.head.at[m0 + i] = v[i];
             const float z = n < p.N ? v[i] : -INFINITY;
             float m = z;
 #pragma unroll
@@ -83,7 +93,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
             float e = exp2_approx(fmaf(z, kLog2e, m == -INFINITY ? 0.0f : -m));
 #pragma unroll
             for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
-            if (lane == 0) p.head.parts[(m0 + i) * p.head.ld_parts + n / 32] = make_float2(m, e);
+            if (lane == 0) more.head.parts[(m0 + i) * more.head.ld_parts + n / 32] = make_float2(m, e);
         }
         return;
     }
@@ -92,18 +102,18 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (i >= rows) break;
-            const int64_t label = p.head.labels[m0 + i];
+            const int64_t label = more.head.labels[m0 + i];
             float dz = 0.0f;
-            if (label >= 0 && label < p.head.V) {
-                const float dloss = p.head.factor ? *p.head.factor * p.head.dloss[(m0 + i) * p.head.incd] : p.head.unit;
-                dz = (exp2_approx(fmaf(v[i], kLog2e, -(p.head.lse[m0 + i] * kLog2e))) - (label == p.head.v0 + n ? 1.0f : 0.0f)) * dloss;
+            if (label >= 0 && label < more.head.V) {
+                const float dloss = more.head.factor ? *more.head.factor * more.head.dloss[(m0 + i) * more.head.incd] : more.head.unit;
+                dz = (exp2_approx(fmaf(v[i], kLog2e, -(more.head.lse[m0 + i] * kLog2e))) - (label == more.head.v0 + n ? 1.0f : 0.0f)) * dloss;
             }
             p.D[(m0 + i) * p.ldd + n] = H::narrow(dz);
         }
         return;
     }
     if constexpr (MODE == kPairSum) {
-        const float factor = p.sum.scale * *p.sum.factor;
+        const float factor = more.sum.scale * *more.sum.factor;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (i < rows) p.D[(m0 + i) * p.ldd + n] = H::narrow(v[i] * factor);
@@ -132,7 +142,7 @@ __device__ __forceinline__ void finish16(const StreamParams &p, int n, int m0, f
 template <int NT, bool W_MN, typename T, int MODE>
 __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::CTAS)
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
-                         const __grid_constant__ CUtensorMap map_x, const StreamParams p) {
+                         const __grid_constant__ CUtensorMap map_x, const StreamParams p, const StreamMore<MODE> more) {
     using C = StreamConfig<NT>;
     constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
@@ -253,7 +263,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
         constexpr int COLS = NT / C::GROUPS;
         const int first_col = (warp - 4) / 4 * COLS;
         int j = 0;
-        for (int u = u0; u < u1;) {
+        for (int u = u0; u < u1; ++j) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
             const int n_units = min(p.KB - kb0, u1 - u);
             u += n_units;
@@ -263,40 +273,48 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             const bool whole = n_units == p.KB;
             static_assert(COLS == 16, "a warp's columns are one load");
             uint32_t r[16];
-            bool ok = true;
-            for (int first = 0; first < n_units; first += MODE == kPairLogits ? kLogitBlocks : n_units, ++j) {
-                ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
-                if (!ok) break;
-                tc_after_sync();
-                uint32_t more[16];
-                tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), more);
-                tmem_ld_wait();
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    r[i] = MODE == kPairLogits && first > 0
-                               ? __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(more[i]))
-                               : more[i];
-                tc_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&acc_free[j & 1]);
-            }
+            bool ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
             if (!ok) break;
-            if (first_col >= tokens) continue;
-            if (whole) {
-                float v[16];
+            tc_after_sync();
+            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), r);
+            tmem_ld_wait();
+            tc_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&acc_free[j & 1]);
+            if constexpr (MODE == kPairLogits) {  // the other runs' sums
+                for (int first = kLogitBlocks; first < n_units; first += kLogitBlocks) {
+                    ++j;
+                    ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+                    if (!ok) break;
+                    tc_after_sync();
+                    uint32_t next[16];
+                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), next);
+                    tmem_ld_wait();
+                    tc_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&acc_free[j & 1]);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                finish16<T, MODE>(p, n, m0 + first_col, b, v);
-            } else {
-                put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), first_col, row, tokens, r);
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(next[i]));
+                }
+                if (!ok) break;
             }
-            if (whole ||
+            if (first_col < tokens) {
+                if (whole) {
+                    float v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+                    finish16<T, MODE>(p, more, n, m0 + first_col, b, v);
+                } else {
+                    put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), first_col, row, tokens, r);
+                }
+            }
+            if (whole || first_col >= tokens ||
                 !piece_arrived(p.counters + tile * 4 * C::GROUPS + warp - 4, n_units, p.KB, lane))
                 continue;
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
             float v[16];
             sum_pieces<NT>(p.pieces, c0, c1, 1, 0, first_col, row, tokens, v);
-            finish16<T, MODE>(p, n, m0 + first_col, b, v);
+            finish16<T, MODE>(p, more, n, m0 + first_col, b, v);
         }
     }
 
@@ -363,8 +381,6 @@ cudaError_t launch(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream,
     p.ldd = g.ldd;
     p.pre = g.pre;
     p.ldz = g.ldz;
-    p.head = extra.head;
-    p.sum = extra.sum;
     void *ws = nullptr;
     err = layer_scratch(kScratchStream, stream,
                         kCounterBytes + static_cast<size_t>(2) * sms[dev] * 64 * kStreamRows * 4, &ws, detail);
@@ -378,7 +394,7 @@ cudaError_t launch(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream,
         *detail = "cuTensorMapEncodeTiled rejected a matrix";
         return cudaErrorInvalidValue;
     }
-    err = launch_early(kernel, dim3(p.split.ctas), C::THREADS, C::SMEM, stream, mw, mx, p);
+    err = launch_early(kernel, dim3(p.split.ctas), C::THREADS, C::SMEM, stream, mw, mx, p, StreamMore<MODE>(extra));
     if (err != cudaSuccess) *detail = "linear layer kernel launch failed";
     return err;
 }
