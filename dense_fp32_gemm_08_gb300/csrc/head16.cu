@@ -264,7 +264,10 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
             q.b_mn = !h.w_dv;
             q.D = h.dX;
             q.ldd = h.lddx;
-            if (h.T <= 64 && n == h.V && stream_gemm16_supports(q)) {
+            // Up to 64 tokens and from 2048 entries on, dX streams the weights by itself; else it is in one grid
+            // with dW. (1 token, apart and together: 1000 x 512 16.6 and 12.4 us, 2000 x 512 17.0 and 17.6, 4000 x 512
+            // 17.7 and 22.9. 64 tokens: 1000 x 1024 24.0 and 19.0, 2000 x 1024 24.0 and 24.3, 8000 x 256 22.4 and 31.3.)
+            if (h.T <= 64 && n == h.V && n >= 2048 && stream_gemm16_supports(q)) {
                 err = stream_gemm16_extra_launch(q, kPairSum, extra, stream, detail);
                 if (err != cudaSuccess) return err;
                 --count;
