@@ -33,6 +33,25 @@ __device__ __forceinline__ float2 join_lanes(float2 a) {
         a = join(a, make_float2(__shfl_xor_sync(0xFFFFFFFFu, a.x, s), __shfl_xor_sync(0xFFFFFFFFu, a.y, s)));
     return a;
 }
+// `n` parts, `apart` from one to the next, N loads of them under way at once.
+template <int N>
+__device__ __forceinline__ float2 join_run(const float2 *part, long long apart, int n) {
+    float2 a = make_float2(-INFINITY, 0.0f);
+    for (; n > 0; n -= N, part += N * apart) {
+        float2 q[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) q[k] = k < n ? __ldcg(part + k * apart) : make_float2(-INFINITY, 0.0f);
+        float m = a.x;
+#pragma unroll
+        for (int k = 0; k < N; ++k) m = fmaxf(m, q[k].x);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float s = a.y * exp2_approx(a.x - base);
+#pragma unroll
+        for (int k = 0; k < N; ++k) s = fmaf(q[k].y, exp2_approx(q[k].x - base), s);
+        a = make_float2(m, s);
+    }
+    return a;
+}
 struct LossOut {
     const float *at;
     const int64_t *labels;
@@ -49,7 +68,7 @@ struct LossOut {
 // Joins the parts of 32 rows, parts[part][row]: lane = row, a warp every 32nd part, then the warps through
 // shared memory.
 constexpr int kJoinThreads = 1024;
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const float2 *parts, long long ld, int n_parts,
+__global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const float2 *parts, long long ld, int n_parts,
                                                             const LossOut out) {
     __shared__ float2 shared[32][33];
     grid_dependents();
@@ -57,10 +76,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const float2 *parts,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
     float2 a = make_float2(-INFINITY, 0.0f);
-    if (row < out.T) {
-#pragma unroll 4
-        for (int i = warp; i < n_parts; i += 32) a = join(a, __ldcg(parts + i * ld + row));
-    }
+    if (row < out.T) a = join_run<5>(parts + warp * ld + row, 32 * ld, (n_parts - warp + 31) / 32);
     shared[warp][lane] = a;
     __syncthreads();
     // Warp w now joins row w's 32 values.
@@ -80,9 +96,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) join_rows_kernel(const float2 
     const int row = wide ? blockIdx.x : blockIdx.x * kRowWarps + warp;
     float2 a = make_float2(-INFINITY, 0.0f);
     if (row < out.T) {
-#pragma unroll 4
-        for (int i = wide ? threadIdx.x : lane; i < n_parts; i += wide ? 32 * kRowWarps : 32)
-            a = join(a, __ldcg(parts + row * ld + i));
+        const int first = wide ? threadIdx.x : lane, step = wide ? 32 * kRowWarps : 32;
+        a = join_run<4>(parts + row * ld + first, step, (n_parts - first + step - 1) / step);
     }
     a = join_lanes(a);
     if (!wide) {
