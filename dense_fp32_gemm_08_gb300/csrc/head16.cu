@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const float2 *par
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
     float2 a = make_float2(-INFINITY, 0.0f);
-    if (row < out.T) a = join_run<5>(parts + warp * ld + row, 32 * ld, (n_parts - warp + 31) / 32);
+    if (row < out.T) a = join_run<6>(parts + warp * ld + row, 32 * ld, (n_parts - warp + 31) / 32);
     shared[warp][lane] = a;
     __syncthreads();
     // Warp w now joins row w's 32 values.

@@ -72,48 +72,105 @@ struct StreamConfig {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Reduces each of a lane's 16 values over the warp, halving the values at each exchange; the result of value t is
+// in lanes 2 t and 2 t + 1. (16 exchanges; a butterfly per value takes 80.)
+template <typename Op>
+__device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
+#pragma unroll
+    for (int half = 8; half > 0; half /= 2) {
+        const bool upper = (lane & (2 * half)) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = upper ? v[i] : v[i + half], keep = upper ? v[i + half] : v[i];
+            v[i] = op(keep, __shfl_xor_sync(0xFFFFFFFFu, send, 2 * half));
+        }
+    }
+    return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
+}
+
+// Lane i's share of what the head's products read of token m0 + i % 16: one round trip for all tokens.
+struct TokenShare {
+    int label = -1;  // outside the vocabulary: the token does not count
+    float lse2 = 0.0f, dloss = 0.0f;
+    template <int MODE>
+    __device__ __forceinline__ void load(const PairHead &h, int t, int M, float factor) {
+        if (t >= M) return;
+        const int64_t l = h.labels[t];
+        if (l < 0 || l >= h.V) return;
+        label = static_cast<int>(l);
+        if constexpr (MODE == kPairLogitGrad) {
+            lse2 = h.lse[t] * kLog2e;  // in units of log 2
+            dloss = h.factor ? factor * h.dloss[t * h.incd] : h.unit;
+        }
+    }
+};
+
 // 16 columns (tokens m0 .. m0 + 15) of output feature n; a warp has 32 features in order.
 template <typename T, int MODE>
-__device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore<MODE> &more, int n, int m0,
-                                         float b, float (&v)[16]) {
+__device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore<MODE> &more, float factor, int n,
+                                         int m0, float b, float (&v)[16]) {
     using H = Half16<T>;
     const int rows = min(16, p.M - m0);
     if constexpr (MODE == kPairLogits) {
         const int lane = threadIdx.x & 31;
         if (n - lane >= p.N) return;
+        TokenShare share;
+        share.load<MODE>(more.head, m0 + (lane & 15), p.M, factor);
+        // Lane i has the label of token i: does one of the warp's 32 logits belong to it?
+        const int at = share.label - (n - lane);
+        if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < rows && __shfl_sync(0xFFFFFFFFu, share.label, i) == n) more.head.at[m0 + i] = v[i];
+        }
+        float z[16];
+        const auto larger = [](float x, float y) { return fmaxf(x, y); };
+        const auto add = [](float x, float y) { return x + y; };
+        float2 *parts = more.head.parts + n / 32;
+        if (rows <= 4) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i >= rows) break;
+                const float mine = n < p.N ? v[i] : -INFINITY;
+                float m = mine;
+#pragma unroll
+                for (int s = 16; s > 0; s /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
+                m *= kLog2e;
+                float e = exp2_approx(fmaf(mine, kLog2e, m == -INFINITY ? 0.0f : -m));
+#pragma unroll
+                for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
+                if (lane == 0) parts[(m0 + i) * more.head.ld_parts] = make_float2(m, e);
+            }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (n >= p.N) v[i] = -INFINITY;
+            z[i] = v[i];
+        }
+        const float m = reduce16(z, lane, larger) * kLog2e;
+        const float base = m == -INFINITY ? 0.0f : -m;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = exp2_approx(fmaf(v[i], kLog2e, __shfl_sync(0xFFFFFFFFu, base, 2 * i)));
+        const float e = reduce16(z, lane, add);
+        if ((lane & 1) == 0 && lane / 2 < rows) parts[(m0 + lane / 2) * more.head.ld_parts] = make_float2(m, e);
+        return;
+    }
+    if constexpr (MODE == kPairLogitGrad) {
+        TokenShare share;
+        share.load<MODE>(more.head, m0 + (threadIdx.x & 15), p.M, factor);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (i >= rows) break;
-            if (more.head.labels[m0 + i] == n && n < p.N) more.head.at[m0 + i] = v[i];
-            const float z = n < p.N ? v[i] : -INFINITY;
-            float m = z;
-#pragma unroll
-            for (int s = 16; s > 0; s /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-            m *= kLog2e;
-            float e = exp2_approx(fmaf(z, kLog2e, m == -INFINITY ? 0.0f : -m));
-#pragma unroll
-            for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
-            if (lane == 0) more.head.parts[(m0 + i) * more.head.ld_parts + n / 32] = make_float2(m, e);
+            const int label = __shfl_sync(0xFFFFFFFFu, share.label, i);
+            const float lse2 = __shfl_sync(0xFFFFFFFFu, share.lse2, i), dloss = __shfl_sync(0xFFFFFFFFu, share.dloss, i);
+            const float dz = (exp2_approx(fmaf(v[i], kLog2e, -lse2)) - (label == more.head.v0 + n ? 1.0f : 0.0f)) * dloss;
+            if (n < p.N) p.D[(m0 + i) * p.ldd + n] = H::narrow(label >= 0 ? dz : 0.0f);
         }
         return;
     }
     if (n >= p.N) return;
-    if constexpr (MODE == kPairLogitGrad) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            if (i >= rows) break;
-            const int64_t label = more.head.labels[m0 + i];
-            float dz = 0.0f;
-            if (label >= 0 && label < more.head.V) {
-                const float dloss = more.head.factor ? *more.head.factor * more.head.dloss[(m0 + i) * more.head.incd] : more.head.unit;
-                dz = (exp2_approx(fmaf(v[i], kLog2e, -(more.head.lse[m0 + i] * kLog2e))) - (label == more.head.v0 + n ? 1.0f : 0.0f)) * dloss;
-            }
-            p.D[(m0 + i) * p.ldd + n] = H::narrow(dz);
-        }
-        return;
-    }
     if constexpr (MODE == kPairSum) {
-        const float factor = more.sum.scale * *more.sum.factor;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             if (i < rows) p.D[(m0 + i) * p.ldd + n] = H::narrow(v[i] * factor);
@@ -262,6 +319,10 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         constexpr int COLS = NT / C::GROUPS;
         const int first_col = (warp - 4) / 4 * COLS;
+        float factor = 1.0f;
+        if constexpr (MODE == kPairSum) factor = more.sum.scale * *more.sum.factor;
+        if constexpr (MODE == kPairLogitGrad)
+            if (more.head.factor) factor = *more.head.factor;
         int j = 0;
         for (int u = u0; u < u1; ++j) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
@@ -303,7 +364,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T, MODE>(p, more, n, m0 + first_col, b, v);
+                    finish16<T, MODE>(p, more, factor, n, m0 + first_col, b, v);
                 } else {
                     put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), first_col, row, tokens, r);
                 }
@@ -314,7 +375,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
             float v[16];
             sum_pieces<NT>(p.pieces, c0, c1, 1, 0, first_col, row, tokens, v);
-            finish16<T, MODE>(p, more, n, m0 + first_col, b, v);
+            finish16<T, MODE>(p, more, factor, n, m0 + first_col, b, v);
         }
     }
 
