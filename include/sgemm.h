@@ -376,7 +376,7 @@ sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T,
  *     S = a / 127,   Q = 127 x / a rounded to the nearest integer, ties to even,   restored value: Q * S rounded
  *     to the matrix's type
  *
- * so a restored value is within a / 254 (and its rounding) of x, and a itself comes back as it was. A block of zeros
+ * so a restored value is within a / 254 (and two roundings) of x, and a itself comes back as it was. A block of zeros
  * has S = 0; one that holds an infinity or a NaN restores to NaN throughout. Q in rows of a multiple of 16 bytes at a
  * 16-byte aligned base is read and written fastest; any other is taken too.
  */
@@ -389,8 +389,10 @@ sgemm_status_t sgemm_restore8(sgemm_dtype_t dtype, int64_t M, int64_t N, const i
                               int64_t lds, void *X, int64_t ldx, void *stream);
 
 /*
- * sgemm_linear with the pre-activation kept as a checkpoint (Zq, Zs) of the M x N values that Z would hold there. Y
- * is computed from the unrounded pre-activation, as there. Neither array may be NULL or overlap another matrix.
+ * sgemm_linear with the pre-activation kept as a checkpoint (Zq, Zs) of the M x N values that Z would hold there, to the
+ * bit. Y is computed from the unrounded pre-activation, as there. Neither array may be NULL or overlap another matrix.
+ * (Few rows or small outputs, and K == 0, pass through Z in a workspace of 2 * M * N' bytes, N' = N rounded up to a multiple of 8; larger
+ * products save their tiles directly.)
  */
 sgemm_status_t sgemm_linear_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N, int64_t K,
                                         const void *X, int64_t ldx, const void *W, int64_t ldw, const void *bias,
@@ -399,8 +401,10 @@ sgemm_status_t sgemm_linear_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, 
 
 /*
  * sgemm_linear_backward from checkpoints of X (M x K) and of the pre-activation Z (M x N): its results are those of
- * sgemm_linear_backward on the restored values. (Zq, Zs) are read unless act is none, (Xq, Xs) only for dW (NULL
- * otherwise).
+ * sgemm_linear_backward on the restored values, to the bit. (Zq, Zs) are read unless act is none, (Xq, Xs) only for dW
+ * (NULL otherwise). X is restored in a workspace of 2 * M * K' bytes; Z is read from its codes, through a workspace
+ * only where their rows are not 8-byte aligned (in the last 8 bytes of such rows what follows the row is read, and not
+ * used).
  */
 sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
                                                  int64_t K, const void *dY, int64_t lddy, const int8_t *Zq,
@@ -418,8 +422,9 @@ sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t
  *   W       SGEMM_OP_T: V x D, ldw >= D. SGEMM_OP_N: D x V, ldw >= V.
  *   labels  T int64 values. A token whose label is outside [0, V) (such as -100) does not count: its loss is 0.
  *   loss, lse  T fp32 values each; either may be NULL (not computed). lse is what the gradient reads.
- * T == 0 is a no-op. Sums are fp32, in an order that does not depend on timing. A logit of minus infinity has
- * probability 0; a logit of plus infinity or NaN makes its token's lse and loss NaN.
+ * T == 0 is a no-op. Sums are fp32, in an order that does not depend on timing; a logit's products are added up in
+ * runs of 1024. The workspace holds 8 bytes for every 32 or 64 logits of up to 32768 tokens at a time. A logit of minus
+ * infinity has probability 0; plus infinity, NaN, or a magnitude above 2^127 makes its token's lse and loss NaN.
  */
 sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
                                    const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *labels,
@@ -433,11 +438,13 @@ sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64
  *     dX = dz . op(W)^T (T x D, lddx >= D),   dW = X^T . dz in W's layout (lddw as ldw)
  *
  * dX and dW may each be NULL (not computed). With T == 0, dW is set to zero. The logits are computed again, a piece
- * of the vocabulary at a time; a piece's dz lives in a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
- * sums over the pieces in another of 4 * T' * D' (T and D rounded up to multiples of 256). The products read dz in the
- * call's dtype, in half times a power of two that brings the largest counted |dloss| to 2^14 and that the outputs are
- * divided by again. X of a token that does not count is multiplied by 0 for dW, so it must be finite. Outputs must
- * not overlap inputs or each other.
+ * of the vocabulary at a time. A piece's dz lives in a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
+ * sums over several pieces in another of 4 * T' * D' bytes (T and D rounded up to multiples of 256). The products read dz
+ * in the call's dtype, for weights dloss / m, m the largest finite |dloss[t]| of the tokens that count (incd == 0: m =
+ * dloss[0], whatever it is), in half times 2^14; the outputs are multiplied by m (in half, divided by 2^14). So equal
+ * dloss are not rounded at all, and half holds probabilities down to 2^-38. With incd == 0 a dloss that is not finite
+ * makes every value of dX and dW NaN or infinite. X of a token that does not count is multiplied by 0 for dW, as in
+ * the formula, so it must be finite. Outputs must not overlap inputs or each other.
  */
 sgemm_status_t sgemm_cross_entropy_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
                                             const float *dloss, int64_t incd, const void *X, int64_t ldx,
