@@ -1,9 +1,10 @@
 // checkpoint8.cu: 16-bit matrices to 8-bit checkpoints and back (checkpoint8.cuh has the form).
 //
-// Bound by memory: 2 + 1.06 bytes a value each way (16384 x 14336 bf16: saved in 108 us, 6.5 TB/s; restored in
-// 103 us, 6.9 TB/s). Saving is near the issue rate too: a lane has 16 consecutive columns of a row, so that a
-// block's maximum is two exchanges among 4 lanes and what a block costs besides its values is paid by 16 of them
-// (with 8 columns: 137 us). Several rows are under way per lane, so that its loads are out before the first is used.
+// Bound by memory: 2 + 1.06 bytes a value each way (16384 x 14336 bf16: saved in 102 us, 7.1 TB/s, restored in 103 us, 6.9
+// TB/s; 4095 x 3001 in unaligned rows 10.6 and 12.2 us). Saving is near the issue rate too (65% of the cycles issue): a
+// lane has 16 consecutive columns of a row, so that a block's maximum is two exchanges among 4 lanes and what a block costs
+// besides its values is paid by 16 of them (with 8 columns: 137 us). Several rows are under way per lane, so that its
+// loads are out before the first is used.
 #include "checkpoint8.cuh"
 #include "layer16.cuh"
 

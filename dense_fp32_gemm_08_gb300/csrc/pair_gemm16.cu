@@ -13,7 +13,8 @@
 // Roles of a CTA's 20 warps:
 //   warp 0, lane 0: TMA producer: this CTA's 128 rows of A and 128 columns of B per 64-wide
 //                   k-block into a ring of 6 stages (512 x 12288 x 4096 with 4, 5, 6: 55, 49.3 and
-//                   47.5 us, so the sixth has the room of a second store buffer per epilogue warp);
+//                   47.5 us, so the sixth has the room of a second store buffer per epilogue warp; a seventh,
+//                   in place of all store buffers, takes 3% longer at K = 4096);
 //                   both CTAs' copies complete on the leader's "full" barrier.
 //   warp 1, lane 0: (leader CTA) issues the MMAs, four k-steps of 16 per block, into one of two
 //                   TMEM accumulators of 256 columns; commits free the stage in both CTAs and,
@@ -30,11 +31,20 @@
 // MMA descriptors differ, the arithmetic does not, so the three products of a linear layer and
 // its gradient need no transposed copies.
 //
-// Measured: 16384 x 14336 x 4096 bf16 with bias, GELU and kept pre-activation 1.10 ms (1,745 TFLOP/s;
-// 1.27 ms when run without a pause, at the clocks that the power limit then leaves): bound by the
-// tensor cores. 512 x 12288 x 4096: 48.5 us, two rounds of tiles for 1.26 (tensor pipe busy 63%).
+// The epilogue comes in modes (PairMode), each a kernel of its own: the layer's; the layer's with its pre-activation
+// saved as an 8-bit checkpoint; the head's logits, reduced and not written; their gradient; and sums over pieces of the
+// vocabulary.
+//
+// Measured: 16384 x 14336 x 4096 bf16 with bias, GELU and kept pre-activation 1.05 to 1.08 ms (1,780 to 1,830 TFLOP/s;
+// 1.24 ms when run without a pause, at the clocks that the power limit then leaves): bound by the
+// tensor cores. With the pre-activation saved in 8 bits 1.12 ms; logits of the same size 1.05 ms. 512 x 12288 x 4096:
+// 46 us, two rounds of tiles for 1.26 (tensor pipe busy 63%).
 // 4095 x 3001 x 1537 f16 with every epilogue part in unaligned rows: 56 us without the repacking, bound
 // by the epilogue's 2-byte stores. (Asking L2 for operands 6 to 12 k-blocks ahead: 4 to 25% longer.)
+// A tile's epilogue is hidden behind the next tile's MMAs only in part: what its warps issue takes from the tensor cores'
+// time even where it is the shorter (K = 4096: a k-block 0.314 us without any, 0.328 with the plain one, 0.371 with GELU and
+// the checkpoint). At K = 64 it alone decides: 16384 x 14336 plain 131 us, 0.6 us a tile for the reads of TMEM, 0.65 for
+// the conversion, 0.6 for the stores.
 //
 // Every wait is bounded (ptx.cuh); a wait that expires ends the role, and the CTAs still meet at
 // the final cluster barrier and free their TMEM.
@@ -135,7 +145,7 @@ __device__ __forceinline__ void with_layout(const PairProduct &g, Body body) {
 
 // The blocks that one accumulator sums. The tensor cores add to it with fp32 sums cut, not rounded, once per 16 k
 // values, which leaves the logits of 4096 values 3e-6 too small; the epilogue adds runs of 1024 in
-// registers (16384 x 32000 x 4096: the loss's error falls from 2.9e-6 to that of a plain fp32 product).
+// registers (16384 x 32000 x 4096: the loss's error falls from 2.9e-6 to 6.6e-7, a plain fp32 product's is 6.1e-7).
 __device__ __forceinline__ int run_blocks(int mode, int blocks) { return mode == kPairLogits ? kLogitBlocks : blocks; }
 
 // A wait whose arrivals may come from the other CTA of the pair.
