@@ -12,7 +12,7 @@
 // Measured, one row 4096 -> 14336 bf16 with bias and SiLU (117 MB): 24.0 us, 4.9 TB/s: 112 whole tiles, of
 // 64 blocks at 0.325 us, and 2.9 us until the first block arrives, for the epilogue and the launch. One row
 // 14336 -> 16384 (470 MB): 77.9 us, 6.0 TB/s. 8 rows 512 -> 512: 5.1 us, launch and round trips to memory. With the
-// join of its parts: the loss of one token, 32000 x 4096 (262 MB), 48 us, 5.5 TB/s; of 64 tokens of 1000 x 512 7.7 us.
+// join of its parts: the loss of one token, 32000 x 4096 (262 MB), 48 us, 5.5 TB/s; of 64 tokens of 1000 x 512 7.4 us.
 #include "activation16.cuh"
 #include "layer16.cuh"
 #include "pair_gemm16.cuh"
@@ -76,7 +76,8 @@ struct StreamConfig {
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Reduces each of a lane's 16 values over the warp, halving the values at each exchange; the result of value t is
-// in lanes 2 t and 2 t + 1. (16 exchanges; a butterfly per value takes 80.)
+// in lanes 2 t and 2 t + 1. (16 exchanges; a butterfly per value takes 80, and is
+// faster by 0.1 us for one value, slower from the third on.)
 template <typename Op>
 __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
 #pragma unroll
@@ -91,7 +92,8 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
     return op(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], 1));
 }
 
-// Lane i's share of what the head's products read of token m0 + i % 16: one round trip for all tokens.
+// Lane i's share of what the head's products read of token m0 + i % 16: one round trip for all tokens, made while
+// the tile multiplies.
 struct TokenShare {
     int label = -1;  // outside the vocabulary: the token does not count
     float lse2 = 0.0f, dloss = 0.0f;
@@ -110,15 +112,13 @@ struct TokenShare {
 
 // 16 columns (tokens m0 .. m0 + 15) of output feature n; a warp has 32 features in order.
 template <typename T, int MODE>
-__device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore<MODE> &more, float factor, int n,
-                                         int m0, float b, float (&v)[16]) {
+__device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore<MODE> &more, const TokenShare &share,
+                                         float factor, int n, int m0, float b, float (&v)[16]) {
     using H = Half16<T>;
     const int rows = min(16, p.M - m0);
     if constexpr (MODE == kPairLogits) {
         const int lane = threadIdx.x & 31;
         if (n - lane >= p.N) return;
-        TokenShare share;
-        share.load<MODE>(more.head, m0 + (lane & 15), p.M, factor);
         // Lane i has the label of token i: does one of the warp's 32 logits belong to it?
         const int at = share.label - (n - lane);
         if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
@@ -130,22 +130,6 @@ __device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore
         const auto larger = [](float x, float y) { return fmaxf(x, y); };
         const auto add = [](float x, float y) { return x + y; };
         float2 *parts = more.head.parts + n / 32;
-        if (rows <= 4) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (i >= rows) break;
-                const float mine = n < p.N ? v[i] : -INFINITY;
-                float m = mine;
-#pragma unroll
-                for (int s = 16; s > 0; s /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, s));
-                m *= kLog2e;
-                float e = exp2_approx(fmaf(mine, kLog2e, m == -INFINITY ? 0.0f : -m));
-#pragma unroll
-                for (int s = 16; s > 0; s /= 2) e += __shfl_xor_sync(0xFFFFFFFFu, e, s);
-                if (lane == 0) parts[(m0 + i) * more.head.ld_parts] = make_float2(m, e);
-            }
-            return;
-        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (n >= p.N) v[i] = -INFINITY;
@@ -160,8 +144,6 @@ __device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore
         return;
     }
     if constexpr (MODE == kPairLogitGrad) {
-        TokenShare share;
-        share.load<MODE>(more.head, m0 + (threadIdx.x & 15), p.M, factor);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             if (i >= rows) break;
@@ -335,6 +317,9 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             const int m0 = C::TOKEN_TILES ? tile % p.m_tiles * NT : 0, tokens = min(NT, p.M - m0);
             const float b = p.bias && n < p.N ? Half16<T>::widen(p.bias[n]) : 0.0f;
             const bool whole = n_units == p.KB;
+            TokenShare share;
+            if constexpr (MODE == kPairLogits || MODE == kPairLogitGrad)
+                share.load<MODE>(more.head, m0 + first_col + (lane & 15), p.M, factor);
             static_assert(COLS == 16, "a warp's columns are one load");
             uint32_t r[16];
             bool ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
@@ -367,7 +352,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                     float v[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-                    finish16<T, MODE>(p, more, factor, n, m0 + first_col, b, v);
+                    finish16<T, MODE>(p, more, share, factor, n, m0 + first_col, b, v);
                 } else {
                     put_piece<NT>(p.pieces, 2 * blockIdx.x + (kb0 == 0 ? 1 : 0), first_col, row, tokens, r);
                 }
@@ -378,7 +363,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             const int c0 = p.split.owner(tile * p.KB), c1 = p.split.owner(tile * p.KB + p.KB - 1);
             float v[16];
             sum_pieces<NT>(p.pieces, c0, c1, 1, 0, first_col, row, tokens, v);
-            finish16<T, MODE>(p, more, factor, n, m0 + first_col, b, v);
+            finish16<T, MODE>(p, more, share, factor, n, m0 + first_col, b, v);
         }
     }
 
