@@ -63,7 +63,7 @@ struct LossOut {
     int T, V;
     float *loss, *lse;
     __device__ __forceinline__ void put(int row, float2 a) const {
-        const float l = fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
+        const float l = a.x == -INFINITY ? a.x : fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
         const int64_t label = labels[row];
         if (lse) lse[row] = l;
         if (loss) loss[row] = label >= 0 && label < V ? l - at[row] : 0.0f;
@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long l
     grid_dependents();
     grid_dependency();
     float a = 0.0f;
+#pragma unroll 4
     for (long long t = threadIdx.x; t < T; t += 1024) {
         const int64_t label = labels[t];
         const float d = fabsf(dloss[t * incd]);
@@ -185,10 +186,10 @@ cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **
         const Gemm16 g = logits(h, t0, T, 0, h.V);
         const bool few = stream_gemm16_supports(g);
         const int n_parts = static_cast<int>((h.V + (few ? 31LL : 63LL)) / (few ? 32 : 64));
-        const long long ld = (T + 31) / 32 * 32, ld_parts = few ? n_parts : ld;
+        const long long ld = (T + 31LL) / 32 * 32, ld_parts = few ? n_parts : ld;
         void *p = nullptr;
         err = layer_scratch(kScratchHead, stream,
-                            static_cast<size_t>(ld) * 4 + static_cast<size_t>(ld) * n_parts * 8, &p, detail);
+                            static_cast<size_t>(ld) * 4 + static_cast<size_t>(few ? T : ld) * n_parts * 8, &p, detail);
         if (err != cudaSuccess) return err;
         PairExtra extra;
         PairHead &x = extra.head;
@@ -228,8 +229,8 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
     // 65536 x 1024: 2.08, 1.96, 1.92, 1.92.)
     const long long most = std::max<long long>(4096, (512LL << 20) / 2 / h.T / 256 * 256);
     const long long pieces = (h.V + most - 1) / most;
-    const int width = static_cast<int>(((h.V + pieces - 1) / pieces + 255) / 256 * 256);
-    const long long ldz = std::min<long long>(width, (h.V + 7LL) / 8 * 8);
+    const long long width = ((h.V + pieces - 1) / pieces + 255) / 256 * 256;
+    const long long ldz = std::min(width, (h.V + 7LL) / 8 * 8);
     void *dz = nullptr, *p = nullptr;
     err = layer_scratch(kScratchHeadDz, stream, static_cast<size_t>(h.T) * ldz * 2, &dz, detail);
     if (err != cudaSuccess) return err;
@@ -262,8 +263,8 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
         if (err != cudaSuccess) return err;
         extra.sum.sums = static_cast<float *>(p);
     }
-    for (int v0 = 0; v0 < h.V; v0 += std::min(width, h.V - v0)) {
-        const int n = std::min(width, h.V - v0);
+    for (long long next = 0; next < h.V; next += width) {
+        const int v0 = static_cast<int>(next), n = static_cast<int>(std::min<long long>(width, h.V - next));
         Gemm16 g = logits(h, 0, h.T, v0, n);
         g.D = static_cast<uint16_t *>(dz);
         g.ldd = ldz;

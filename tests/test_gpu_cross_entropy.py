@@ -227,6 +227,20 @@ def test_infinite_and_nan_logits(sgemm_lib):
     assert not dx[9].any()
 
 
+@pytest.mark.parametrize("T", [3, 200])
+def test_a_row_without_a_finite_logit(sgemm_lib, T):
+    """All logits -inf: lse is -inf, the loss NaN, and the other rows are as without it."""
+    sg = sgemm_lib
+    x, w, labels, _ = inputs(T, 300, 64, ignored=0.0, seed=16)
+    x[:, 0], w[:, 0] = 0.0, 1.0
+    want, want_lse = sg.cross_entropy(x, w, labels)
+    x[1, 0] = -math.inf
+    loss, lse = sg.cross_entropy(x, w, labels)
+    keep = torch.arange(T, device="cuda") != 1
+    assert float(lse[1]) == -math.inf and bool(torch.isnan(loss[1]))
+    assert torch.equal(loss[keep], want[keep]) and torch.equal(lse[keep], want_lse[keep])
+
+
 def test_gradient_against_differences(sgemm_lib):
     """The slope of the weighted loss along random directions, the loss in 64 bits: |error| <= 2^-7 |gradient|
     (dz's rounding and the outputs'), a central difference's own being h^2."""
@@ -302,3 +316,49 @@ def test_offsets_past_32_bits(sgemm_lib):
     ox, ow = far(torch.zeros_like(x)), far(torch.zeros_like(w))
     sg.sgemm_cross_entropy_backward("bf16", "T", T, V, D, dloss, 1, fx, pitch, fw, pitch, labels, lse, ox, pitch, ow, pitch)
     assert torch.equal(ox, dx) and torch.equal(ow, dw)
+
+
+@pytest.mark.parametrize("transw", ["T", "N"])
+def test_a_vocabulary_of_2_to_the_28(sgemm_lib, transw):
+    """Weights of more than 2^31 values, in both storages, their gradient in three pieces of the vocabulary."""
+    sg = sgemm_lib
+    T, V, D = 3, (1 << 28) + 5, 8
+    x = normal(1, T, D)
+    w = torch.empty((V, D) if transw == "T" else (D, (V + 7) // 8 * 8), dtype=x.dtype, device="cuda").normal_(0.0, 0.5)
+    w = w if transw == "T" else w[:, :V]
+    labels = torch.tensor([0, V - 1, V // 2], device="cuda")
+    loss, lse = sg.cross_entropy(x, w, labels, transw=transw)
+    wt = w if transw == "T" else w.t()
+    z = torch.empty(T, V, device="cuda")  # in pieces: 64 bits of all of it at once are not needed
+    total = torch.zeros(T, dtype=torch.float64, device="cuda")
+    step = 1 << 26
+    for v in range(0, V, step):
+        part = x.double() @ wt[v:v + step].double().t()
+        total += part.exp().sum(1)
+        z[:, v:v + step] = part.float()
+    want = total.log()
+    # |z| <= 8 * 12: the terms' errors 8 * ACC * 12, the sums' as in training_case.py
+    assert float((lse.double() - want).abs().max()) < 2e-3
+    at = torch.stack([z[t, labels[t]] for t in range(T)]).double()
+    assert float((loss.double() - (want - at)).abs().max()) < 2e-3
+    d = torch.full((), 1.0, device="cuda").expand(T)
+    dx, dw = sg.cross_entropy_backward(d, x, w, labels, lse, transw=transw)
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+    dwt = dw if transw == "T" else dw.t()
+    rdx = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    for v in range(0, V, step):
+        dz = (z[:, v:v + step].double() - want[:, None]).exp()
+        for t in range(T):
+            if v <= int(labels[t]) < v + step:
+                dz[t, int(labels[t]) - v] -= 1.0
+        rdx += dz @ wt[v:v + step].double()
+        ref = dz.t() @ x.double()
+        bound = 0.02 * (dz.abs().t() @ x.double().abs()) + 1e-30
+        assert bool(((dwt[v:v + step].double() - ref).abs() <= bound).all()), v
+    # dz is rounded by 2^-9 of itself, and each of dx's terms with it; sum of |dz| is 2 per token, |w| < 4
+    assert float((dx.double() - rdx).abs().max()) < 2.0 ** -8 * 2 * 4
+
+
+def test_gradient_of_many_tokens_with_their_own_dloss(sgemm_lib):
+    x, w, labels, dloss = inputs(20000, 100, 64, seed=17)
+    check(sgemm_lib, x, w, labels, dloss * 20000)
