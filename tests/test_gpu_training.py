@@ -158,6 +158,23 @@ def test_two_threads_on_one_stream(sgemm_lib):
     assert sg.sgemm_device_status() == sg.SGEMM_OK
 
 
+def test_two_streams_at_once(sgemm_lib):
+    """Steps queued on two streams without waiting in between: each stream has its own workspaces."""
+    sg = sgemm_lib
+    calls = [step(sg, 1, M=700, D=520, F=1032, V=3001), step(sg, 5, M=90, D=136, F=300, V=2000)]
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls[i]())
+    torch.cuda.synchronize()
+    assert all(equal(g, want[i]) for i in range(2) for g in got[i])
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+
+
 @pytest.mark.parametrize("what", ["checkpoint", "restore", "linear", "loss", "gradient"])
 def test_dropped_tensors_wait_for_the_side_stream(sgemm_lib, what):
     """The memory of a side stream's call is handed out again only when that stream is done: its inputs,
