@@ -1,7 +1,7 @@
 // checkpoint8.cu: 16-bit matrices to 8-bit checkpoints and back (checkpoint8.cuh has the form).
 //
 // Bound by memory: 2 + 1.06 bytes a value each way (16384 x 14336 bf16: saved in 102 us, 7.1 TB/s, restored in 103 us, 6.9
-// TB/s; 4095 x 3001 in unaligned rows 10.6 and 12.2 us). Saving is near the issue rate too (65% of the cycles issue): a
+// TB/s; 4095 x 3001 in unaligned rows 10.6 and 10.4 us). Saving is near the issue rate too (65% of the cycles issue): a
 // lane has 16 consecutive columns of a row, so that a block's maximum is two exchanges among 4 lanes and what a block costs
 // besides its values is paid by 16 of them (with 8 columns: 137 us). Several rows are under way per lane, so that its
 // loads are out before the first is used.
@@ -196,38 +196,40 @@ __device__ __forceinline__ void restore8_any_rows(const Restore8 &c, int row0, l
     auto first_col = [&](int i) {
         return static_cast<int>(min(chunk, 0x7ffffff0LL)) - (static_cast<int>(reinterpret_cast<uintptr_t>(x + i * x_step) >> 1) & 7);
     };
+    // Columns [first, last] of a chunk exist; a word is read where it holds the code of one of them.
 #pragma unroll
     for (int i = 0; i < kRestoreRows; ++i) {
-        const int col = first_col(i);
-        if (i >= rows || col < 0 || col > c.N - 8) continue;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(q + i * q_step + col);
-        const uint2 *word = reinterpret_cast<const uint2 *>(at & ~static_cast<uintptr_t>(7));
-        raw[i][0] = __ldg(word);
-        if (at & 7) raw[i][1] = __ldg(word + 1);
-        scale[i][0] = __ldg(s + i * s_step + col / kCheckpointBlock);
-        scale[i][1] = __ldg(s + i * s_step + (col + 7) / kCheckpointBlock);
+        const int col = first_col(i), first = max(col, 0), last = min(col + 7, c.N - 1);
+        raw[i][0] = raw[i][1] = make_uint2(0, 0);
+        scale[i][0] = scale[i][1] = 0.0f;
+        if (i >= rows || first > last) continue;
+        const int8_t *row = q + i * q_step;
+        const uint2 *word = reinterpret_cast<const uint2 *>(reinterpret_cast<uintptr_t>(row + col) & ~static_cast<uintptr_t>(7));
+        if (row + first < reinterpret_cast<const int8_t *>(word + 1)) raw[i][0] = __ldg(word);
+        if (row + last >= reinterpret_cast<const int8_t *>(word + 1)) raw[i][1] = __ldg(word + 1);
+        scale[i][0] = __ldg(s + i * s_step + first / kCheckpointBlock);
+        scale[i][1] = __ldg(s + i * s_step + last / kCheckpointBlock);
     }
 #pragma unroll
     for (int i = 0; i < kRestoreRows; ++i) {
-        if (i >= rows) break;
         const int col = first_col(i);
+        if (i >= rows || col >= c.N || col <= -8) continue;
+        const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q + i * q_step + col));
+        const uint32_t w0 = at & 4 ? raw[i][0].y : raw[i][0].x, w1 = at & 4 ? raw[i][1].x : raw[i][0].y;
+        const uint32_t w2 = at & 4 ? raw[i][1].y : raw[i][1].x;
+        const uint32_t lo = __funnelshift_r(w0, w1, 8 * (at & 3)), hi = __funnelshift_r(w1, w2, 8 * (at & 3));
+        const int border = (max(col, 0) / kCheckpointBlock + 1) * kCheckpointBlock - col;  // columns of the first scale
+        auto of = [&](int k) { return k < border ? scale[i][0] : scale[i][1]; };
+        auto two = [&](int k) { return make_float2(of(k), of(k + 1)); };
+        const uint2 a = restore4<T>(lo, two(0), two(2)), b = restore4<T>(hi, two(4), two(6));
+        uint16_t *to = x + i * x_step + col;
         if (col >= 0 && col <= c.N - 8) {
-            const int at = static_cast<int>(reinterpret_cast<uintptr_t>(q + i * q_step + col));
-            const uint32_t w0 = at & 4 ? raw[i][0].y : raw[i][0].x, w1 = at & 4 ? raw[i][1].x : raw[i][0].y;
-            const uint32_t w2 = at & 4 ? raw[i][1].y : raw[i][1].x;
-            const uint32_t lo = __funnelshift_r(w0, w1, 8 * (at & 3)), hi = __funnelshift_r(w1, w2, 8 * (at & 3));
-            const int border = kCheckpointBlock - (col & (kCheckpointBlock - 1));  // columns of the first scale
-            auto of = [&](int k) { return k < border ? scale[i][0] : scale[i][1]; };
-            auto two = [&](int k) { return make_float2(of(k), of(k + 1)); };
-            const uint2 a = restore4<T>(lo, two(0), two(2)), b = restore4<T>(hi, two(4), two(6));
-            *reinterpret_cast<uint4 *>(x + i * x_step + col) = make_uint4(a.x, a.y, b.x, b.y);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(a.x, a.y, b.x, b.y);
         } else {
-            for (int k = max(0, -col); k < min(8, c.N - col); ++k) {
-                const uint32_t code = static_cast<uint8_t>(q[i * q_step + col + k]);
-                const float v = s[i * s_step + (col + k) / kCheckpointBlock];
-                x[i * x_step + col + k] =
-                    static_cast<uint16_t>(restore4<T>(code, make_float2(v, v), make_float2(v, v)).x);
-            }
+            const uint32_t v[4] = {a.x, a.y, b.x, b.y};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (col + k >= 0 && col + k < c.N) to[k] = static_cast<uint16_t>(v[k >> 1] >> (16 * (k & 1)));
         }
     }
 }
