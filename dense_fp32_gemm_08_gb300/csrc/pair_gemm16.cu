@@ -146,7 +146,12 @@ __device__ __forceinline__ void with_layout(const PairProduct &g, Body body) {
 // The blocks that one accumulator sums. The tensor cores add to it with fp32 sums cut, not rounded, once per 16 k
 // values, which leaves the logits of 4096 values 3e-6 too small; the epilogue adds runs of 1024 in
 // registers (16384 x 32000 x 4096: the loss's error falls from 2.9e-6 to 6.6e-7, a plain fp32 product's is 6.1e-7).
-__device__ __forceinline__ int run_blocks(int mode, int blocks) { return mode == kPairLogits ? kLogitBlocks : blocks; }
+// The gradient's logits are the same to the bit, so that p - 1 at a label that is all but certain keeps its digits.
+__host__ __device__ constexpr bool in_runs(int mode) { return mode == kPairLogits || mode == kPairLogitGrad; }
+template <int MODE>
+__device__ __forceinline__ int run_blocks(int blocks) {
+    return in_runs(MODE) ? kLogitBlocks : blocks;
+}
 
 // A wait whose arrivals may come from the other CTA of the pair.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t *bar, uint32_t parity) {
@@ -406,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                 const Item item(p, t);
                 const int i = item.product;
                 const uint32_t idesc = p.g[i].idesc;
-                for (int kb0 = 0; kb0 < item.n && ok; kb0 += run_blocks(MODE, item.n), ++j) {
+                for (int kb0 = 0; kb0 < item.n && ok; kb0 += run_blocks<MODE>(item.n), ++j) {
                     const int set = j & 1;
                     if (j >= 2 && !mbar_wait_cluster(&acc_free[set], ((j >> 1) - 1) & 1)) {
                         ok = false;
@@ -414,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     }
                     tc_after_sync();
                     const uint32_t d = tmem + static_cast<uint32_t>(set * kBN);
-                    const int KB = min(run_blocks(MODE, item.n), item.n - kb0);
+                    const int KB = min(run_blocks<MODE>(item.n), item.n - kb0);
                     auto blocks = [&](auto a_layout, auto b_layout) {
                         constexpr bool a_mn = decltype(a_layout)::value, b_mn = decltype(b_layout)::value;
                         // Descriptors of stage 0; their start addresses count 16 bytes.
@@ -471,15 +476,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     bias[1] = g.N - col0 - 32 > lane ? Half16<T>::widen(p.bias[col0 + 32 + lane]) : 0.0f;
                 }
             }
-            RowLabel label(p.extra.head, MODE == kPairLogits || MODE == kPairLogitGrad ? row0 + lane : g.M,
-                           g.M, col0);
-            float lse2 = 0.0f, dloss = 0.0f;  // lse in units of log 2
+            RowLabel label(p.extra.head, in_runs(MODE) ? row0 + lane : g.M, g.M, col0);
+            float lse = 0.0f, dloss = 0.0f;
             if (MODE == kPairLogitGrad && label.counts) {
-                lse2 = p.extra.head.lse[row0 + lane] * kLog2e;
+                lse = p.extra.head.lse[row0 + lane];
                 dloss = p.extra.head.factor ? factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd]
                                             : p.extra.head.unit;
             }
-            if constexpr (MODE == kPairLogits) {
+            if constexpr (in_runs(MODE)) {
                 float2 v[32];
                 bool ok = true;
                 for (int kb = 0; kb < item.n; kb += kLogitBlocks, ++j) {
@@ -532,16 +536,47 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                             v[i].y += __ldcg(base + k * kPiece + (2 * i + 1) * kBM);
                         }
                 }
-                const bool mine = label.at >= 0 && label.at < 64;
-                if (__any_sync(0xFFFFFFFFu, mine)) {
-                    float z = 0.0f;
+                const bool mine = label.at >= 0 && label.at < 64, any = __any_sync(0xFFFFFFFFu, mine);
+                float z = 0.0f;  // the logit at the label
+                if (any) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         z = label.at == 2 * i ? v[i].x : z;
                         z = label.at == 2 * i + 1 ? v[i].y : z;
                     }
-                    if (mine) p.extra.head.at[row0 + lane] = z;
                 }
+                if constexpr (MODE == kPairLogitGrad) {
+                    const float lse2 = -lse * kLog2e;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float2 t = __ffma2_rn(v[i], make_float2(kLog2e, kLog2e), make_float2(lse2, lse2));
+                        v[i] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+                    }
+                    if (any) {  // p - 1, without the difference of two numbers near 1
+                        const float less = expm1f(z - lse);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            v[i].x = label.at == 2 * i ? less : v[i].x;
+                            v[i].y = label.at == 2 * i + 1 ? less : v[i].y;
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __fmul2_rn(v[i], make_float2(dloss, dloss));
+                    if (__any_sync(0xFFFFFFFFu, !label.counts)) {  // (a selection: their values may not be finite)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = label.counts ? v[i] : make_float2(0.0f, 0.0f);
+                    }
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        if (b == blocks) break;
+                        if (lane == 0) bulk_wait_read<0>();
+                        __syncwarp();
+                        store_block<T>(reinterpret_cast<const float(&)[32]>(v[16 * b]), buf, &maps.d[0], 1, g.D, g.ldd, g.M,
+                                       g.N, row0, col0 + 32 * b, lane);
+                    }
+                    continue;
+                }
+                if (mine) p.extra.head.at[row0 + lane] = z;
                 if (g.N - col0 < 64) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
@@ -615,35 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
                     tmem_ld_wait();
                 }
             };
-            if constexpr (MODE == kPairLogitGrad) {
-#pragma unroll 1
-                for (int b = 0; b < blocks; ++b) {
-                    float v[32];
-                    values(b, v);
-                    if (b == blocks - 1 && !pieces) release();
-                    float2(&w2)[16] = reinterpret_cast<float2(&)[16]>(v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 t = __ffma2_rn(w2[i], make_float2(kLog2e, kLog2e), make_float2(-lse2, -lse2));
-                        w2[i] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
-                    }
-                    const int at = label.at - 32 * b;
-                    if (__any_sync(0xFFFFFFFFu, at >= 0 && at < 32)) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] -= i == at ? 1.0f : 0.0f;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w2[i] = __fmul2_rn(w2[i], make_float2(dloss, dloss));
-                    if (__any_sync(0xFFFFFFFFu, !label.counts)) {  // (a selection: their values may not be finite)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = label.counts ? v[i] : 0.0f;
-                    }
-                    if (lane == 0) bulk_wait_read<0>();
-                    __syncwarp();
-                    store_block<T>(v, buf, &maps.d[0], 1, g.D, g.ldd, g.M, g.N, row0, col0 + 32 * b, lane);
-                }
-                continue;
-            }
             if constexpr (MODE == kPairSum) {
                 const bool summed = item.product == p.sum_product;
                 float *sums = p.extra.sum.sums + (2 * static_cast<size_t>(item.tile) + rank) * kBN * kBM +

@@ -42,6 +42,7 @@ constexpr int kLogitBlocks = 16;
 struct PairHead {
     const int64_t *labels = nullptr;
     int V = 0, v0 = 0;
+    int run = kLogitBlocks;  // of the streaming product, instead
     // kPairLogits: of 64 columns' logits z log2(e) of a row, the largest m and the sum of 2^(z log2(e) - m), at
     // parts[(column / 64) * ld_parts + row]; and the row's logit at its label. The streaming product: of
     // 32 columns' logits, at parts[row * ld_parts + column / 32].

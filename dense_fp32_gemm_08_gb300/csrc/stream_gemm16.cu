@@ -55,6 +55,13 @@ struct StreamMore<kPairLayer> {
     explicit StreamMore(const PairExtra &) {}
 };
 
+// The logits are summed in runs of k-blocks, each with an accumulator of its own (see the pair product).
+__host__ __device__ constexpr bool in_runs(int mode) { return mode == kPairLogits || mode == kPairLogitGrad; }
+// Accumulators that a tile's or a run's epilogue and the next ones' MMAs take in turn. (Runs of 512, one token's loss at 8000 x
+// 8192: 28.2 us with four, 29.9 with two; 16 tokens of 32000 x 1024 16.4 and 17.3.)
+constexpr int kMaxAccs = 4;
+__host__ __device__ constexpr int accumulators(int mode) { return in_runs(mode) ? kMaxAccs : 2; }
+
 template <int NT>
 struct StreamConfig {
     static constexpr uint32_t A_BYTES = kStreamRows * kStreamK * 2;
@@ -69,8 +76,8 @@ struct StreamConfig {
     static constexpr bool TOKEN_TILES = NT == 64;  // fewer tokens are one tile
     static constexpr int CTAS = NT <= 32 ? 2 : 1;
     static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 8;
-    static constexpr uint32_t TMEM_COLS = 2 * NT < 32 ? 32 : 2 * NT;
-    static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 4) * 8 + 32 + 1024;
+    __host__ __device__ static constexpr uint32_t tmem_cols(int accs) { return accs * NT < 32 ? 32 : accs * NT; }
+    static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 2 * kMaxAccs) * 8 + 32 + 1024;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -96,7 +103,7 @@ __device__ __forceinline__ float reduce16(float (&v)[16], int lane, Op op) {
 // the tile multiplies.
 struct TokenShare {
     int label = -1;  // outside the vocabulary: the token does not count
-    float lse2 = 0.0f, dloss = 0.0f;
+    float lse = 0.0f, dloss = 0.0f;
     template <int MODE>
     __device__ __forceinline__ void load(const PairHead &h, int t, int M, float factor) {
         if (t >= M) return;
@@ -104,7 +111,7 @@ struct TokenShare {
         if (l < 0 || l >= h.V) return;
         label = static_cast<int>(l);
         if constexpr (MODE == kPairLogitGrad) {
-            lse2 = h.lse[t] * kLog2e;  // in units of log 2
+            lse = h.lse[t];
             dloss = h.factor ? factor * h.dloss[t * h.incd] : h.unit;
         }
     }
@@ -148,8 +155,10 @@ __device__ __forceinline__ void finish16(const StreamParams &p, const StreamMore
         for (int i = 0; i < 16; ++i) {
             if (i >= rows) break;
             const int label = __shfl_sync(0xFFFFFFFFu, share.label, i);
-            const float lse2 = __shfl_sync(0xFFFFFFFFu, share.lse2, i), dloss = __shfl_sync(0xFFFFFFFFu, share.dloss, i);
-            const float dz = (exp2_approx(fmaf(v[i], kLog2e, -lse2)) - (label == more.head.v0 + n ? 1.0f : 0.0f)) * dloss;
+            const float lse = __shfl_sync(0xFFFFFFFFu, share.lse, i), dloss = __shfl_sync(0xFFFFFFFFu, share.dloss, i);
+            float dz = exp2_approx(fmaf(v[i], kLog2e, -lse * kLog2e));
+            if (label == more.head.v0 + n) dz = expm1f(v[i] - lse);  // p - 1, not the difference of two numbers near 1
+            dz *= dloss;
             if (n < p.N) p.D[(m0 + i) * p.ldd + n] = H::narrow(label >= 0 ? dz : 0.0f);
         }
         return;
@@ -186,15 +195,15 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const StreamParams p, const StreamMore<MODE> more) {
     using C = StreamConfig<NT>;
-    constexpr int STAGES = C::STAGES;
+    constexpr int STAGES = C::STAGES, ACCS = accumulators(MODE);
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES);
     uint64_t *empty = full + STAGES;
-    uint64_t *acc_full = empty + STAGES;  // [2]
-    uint64_t *acc_free = acc_full + 2;    // [2]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + 2);
+    uint64_t *acc_full = empty + STAGES;    // [ACCS]
+    uint64_t *acc_free = acc_full + ACCS;  // [ACCS]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + ACCS);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u0 = p.split.first(blockIdx.x), u1 = p.split.first(blockIdx.x + 1);
@@ -206,13 +215,13 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < ACCS; ++j) {
             mbar_init(&acc_full[j], 1);
             mbar_init(&acc_free[j], 4 * C::GROUPS);
         }
         mbar_init_fence();
     }
-    if (warp == 2) tmem_alloc<1>(tmem_slot, C::TMEM_COLS);
+    if (warp == 2) tmem_alloc<1>(tmem_slot, C::tmem_cols(ACCS));
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -272,15 +281,17 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             int j = -1, kb = u0 % p.KB, run = 0;
             bool ok = true;
             uint32_t d = tmem;
+            int longest = 0;
+            if constexpr (in_runs(MODE)) longest = more.head.run;
             for (int u = u0; u < u1 && ok; ++u) {
                 // A new accumulator per tile, and per run of blocks that one sums (see the pair product).
-                const bool first = u == u0 || kb == 0 || (MODE == kPairLogits && run == kLogitBlocks);
+                const bool first = u == u0 || kb == 0 || (in_runs(MODE) && run == longest);
                 if (first) {
                     ++j;
                     run = 0;
-                    if (j >= 2 && !mbar_wait(&acc_free[j & 1], ((j >> 1) - 1) & 1)) break;
+                    if (j >= ACCS && !mbar_wait(&acc_free[j % ACCS], (j / ACCS - 1) & 1)) break;
                     tc_after_sync();
-                    d = tmem + static_cast<uint32_t>((j & 1) * NT);
+                    d = tmem + static_cast<uint32_t>((j % ACCS) * NT);
                 }
                 if (!mbar_wait(&full[ring.stage], ring.parity)) break;
                 tc_after_sync();
@@ -295,8 +306,8 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 ring.next();
                 if (++kb == p.KB) kb = 0;
                 ++run;
-                if (kb == 0 || u + 1 == u1 || (MODE == kPairLogits && run == kLogitBlocks))
-                    mma_commit_16<1>(&acc_full[j & 1]);
+                if (kb == 0 || u + 1 == u1 || (in_runs(MODE) && run == longest))
+                    mma_commit_16<1>(&acc_full[j % ACCS]);
             }
         }
     } else if (warp >= 4) {
@@ -322,26 +333,26 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 share.load<MODE>(more.head, m0 + first_col + (lane & 15), p.M, factor);
             static_assert(COLS == 16, "a warp's columns are one load");
             uint32_t r[16];
-            bool ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+            bool ok = mbar_wait(&acc_full[j % ACCS], (j / ACCS) & 1);
             if (!ok) break;
             tc_after_sync();
-            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), r);
+            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j % ACCS) * NT + first_col), r);
             tmem_ld_wait();
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[j & 1]);
-            if constexpr (MODE == kPairLogits) {  // the other runs' sums
-                for (int first = kLogitBlocks; first < n_units; first += kLogitBlocks) {
+            if (lane == 0) mbar_arrive(&acc_free[j % ACCS]);
+            if constexpr (in_runs(MODE)) {  // the other runs' sums
+                for (int first = more.head.run; first < n_units; first += more.head.run) {
                     ++j;
-                    ok = mbar_wait(&acc_full[j & 1], (j >> 1) & 1);
+                    ok = mbar_wait(&acc_full[j % ACCS], (j / ACCS) & 1);
                     if (!ok) break;
                     tc_after_sync();
                     uint32_t next[16];
-                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & 1) * NT + first_col), next);
+                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j % ACCS) * NT + first_col), next);
                     tmem_ld_wait();
                     tc_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[j & 1]);
+                    if (lane == 0) mbar_arrive(&acc_free[j % ACCS]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(next[i]));
                 }
@@ -372,7 +383,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     __syncthreads();
     if (warp == 2) {
         tc_after_sync();
-        tmem_dealloc<1>(tmem, C::TMEM_COLS);
+        tmem_dealloc<1>(tmem, C::tmem_cols(ACCS));
     }
 }
 

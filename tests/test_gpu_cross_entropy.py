@@ -170,6 +170,61 @@ def test_half_keeps_small_probabilities(sgemm_lib):
     assert float((dw[100:].double() - rest).norm() / rest.norm()) < 0.02
 
 
+def summing_error(x, w, labels, run):
+    """What the label's logit may lose: the tensor cores cut their sum (to fp32, by less than a step) once per 16
+    products, from zero in each run of `run` products; the runs are added with rounding, half a step each."""
+    def step(v):
+        return torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=1e-30))) - 23)
+
+    products = x.double() * w.double()[labels]
+    T, D = products.shape
+    lost = torch.zeros(T, dtype=torch.float64, device=x.device)
+    total = torch.zeros_like(lost)
+    for r in range(0, D, run):
+        part = torch.zeros_like(lost)
+        for k in range(r, min(r + run, D), 16):
+            grown = part + products[:, k:min(k + 16, r + run, D)].sum(1)
+            lost += step(torch.maximum(part.abs(), grown.abs()))
+            part = grown
+        if r > 0:
+            lost += step(total + part) / 2
+        total = total + part
+    return lost
+
+
+@pytest.mark.parametrize("T", [1, 7, 64])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_labels_that_are_all_but_certain(sgemm_lib, dtype, T):
+    """1 - p at the labels is about 10^-4 and the gradient no larger, so that the logit's own error shows in it.
+    A row of dX is off by (dloss 1): the label's logit's error (times p < 1) and expm1f's two steps of 1 - p, through
+    the label's row of W; 2^-18 of each other p (a logit's error below 2^-19 and the exponential's); a rounding of each
+    dz to 16 bits; and dX's own sum and rounding. z - lse is exact: the two are within a factor 2 of each other."""
+    sg, (V, D) = sgemm_lib, (56, 704)
+    u, tiny = case.U[dtype] * 1.001, case.TINY[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = normal(1, V, D, dtype=dtype, scale=1.28 / math.sqrt(D))
+    labels = torch.randint(V, (T,), generator=g, device="cuda")
+    x = (normal(2, T, D, dtype=dtype).float() + 8.5 * w[labels].float()).to(dtype)
+    ones = torch.full((), 1.0, device="cuda").expand(T)
+    z = x.double() @ w.double().t()
+    exact = torch.logsumexp(z, 1).float()
+    own = sg.cross_entropy(x, w, labels)[1]
+    length = w.double().norm(dim=1)
+    lost = summing_error(x, w, labels, 64)
+    for lse in (exact, own):
+        dx, _ = sg.cross_entropy_backward(ones, x, w, labels, lse)
+        assert sg.sgemm_device_status() == sg.SGEMM_OK
+        gap = z - lse.double()[:, None]
+        dz = torch.exp(gap)
+        dz.scatter_(1, labels[:, None], torch.expm1(gap.gather(1, labels[:, None])))
+        ref = dz @ w.double()
+        at = dz.gather(1, labels[:, None])[:, 0].abs()
+        off = (2.0 ** -18 + u) * (dz.abs() @ length) + (lost + 2.0 ** -22 * at) * length[labels]
+        off += case.ACC * (dz.abs() @ w.double().abs()).norm(dim=1) + u * ref.norm(dim=1) + tiny * math.sqrt(D) * (1 + V)
+        ratio = (dx.double() - ref).norm(dim=1) / off
+        assert bool((ratio <= 1.0).all()), ratio
+
+
 def test_parts(sgemm_lib):
     sg = sgemm_lib
     for dtype, T in ((torch.bfloat16, 5), (torch.float16, 300)):
