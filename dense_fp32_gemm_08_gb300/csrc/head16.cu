@@ -12,7 +12,7 @@
 // launch. dX adds up over the pieces in fp32.
 //
 // Bound by the tensor cores for many tokens: 16384 of 32000 x 4096 bf16 2.24 to 2.45 ms for the loss (1,750 to 1,916
-// TFLOP/s; the join 16 us of it), 6.47 to 6.97 ms for the gradient (three products, 1,850 to 1,990). For few by reading the
+// TFLOP/s; the join 16 us of it), 6.47 to 7.12 ms for the gradient (three products, 1,810 to 1,990). For few by reading the
 // weights: one token 48 us (5.5 TB/s). In between by the rounds of 256 x 256 tiles; unaligned weights are copied first (777
 // tokens of 30001 x 1537 f16: 113 us, of which the copy is 29 and seven rounds of tiles for 6.2 are 75).
 #include "activation16.cuh"

@@ -2,7 +2,7 @@
 // by streaming B (the weights) from memory once. The split of the work is in stream16.cuh. Roles
 // of a CTA's warps:
 //   warp 0, lane 0: TMA producer (a 128 x 64 block of weights and the tokens' 64 k values per unit)
-//   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns
+//   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns, four for the head's logits
 //   warp 2:         TMEM allocation
 //   warps 4..:      epilogue: lane = output feature, columns = 16 tokens per warp. Whole tiles go from
 //                   TMEM to the epilogue; pieces go to scratch in fp32, and the warp that completes

@@ -423,7 +423,7 @@ sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t
  *   labels  T int64 values. A token whose label is outside [0, V) (such as -100) does not count: its loss is 0.
  *   loss, lse  T fp32 values each; either may be NULL (not computed). lse is what the gradient reads.
  * T == 0 is a no-op. Sums are fp32, in an order that does not depend on timing; a logit's products are added up in
- * runs of 1024. The workspace holds 8 bytes for every 32 or 64 logits of up to 32768 tokens at a time. A logit of minus
+ * runs of 64 to 1024. The workspace holds 8 bytes for every 32 or 64 logits of up to 32768 tokens at a time. A logit of minus
  * infinity has probability 0; plus infinity, NaN, or a magnitude above 2^127 makes its token's lse and loss NaN.
  */
 sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,

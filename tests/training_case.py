@@ -15,7 +15,7 @@ weight exp(-a), so a exp(-a) < 0.4 bounds its share. So
 and the loss adds its label's e and a rounding of |lse| + |z|.
 
 The gradient. p = exp(z - lse) is off by p (e + 2^-22 + |z - lse| 2^-22 + 2^-23 (|z| + |lse|)) (the last: the
-subtraction's operands are fp32), 1 is subtracted exactly to 2^-24, and dz is rounded to 16 bits: u |dz|,
+subtraction's operands are fp32), 1 is subtracted exactly to 2^-24 (or expm1 taken, which is nearer), and dz is rounded to 16 bits: u |dz|,
 and in half half a subnormal step over the factor that brings the largest |dloss| to 2^14. The products
 pass that on through the absolute values of their other factor, with ACC and one rounding of their own."""
 from __future__ import annotations
