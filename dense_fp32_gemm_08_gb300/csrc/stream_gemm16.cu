@@ -289,9 +289,9 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 if (first) {
                     ++j;
                     run = 0;
-                    if (j >= ACCS && !mbar_wait(&acc_free[j % ACCS], (j / ACCS - 1) & 1)) break;
+                    if (j >= ACCS && !mbar_wait(&acc_free[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS - 1) & 1)) break;
                     tc_after_sync();
-                    d = tmem + static_cast<uint32_t>((j % ACCS) * NT);
+                    d = tmem + static_cast<uint32_t>((j & (ACCS - 1)) * NT);
                 }
                 if (!mbar_wait(&full[ring.stage], ring.parity)) break;
                 tc_after_sync();
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 if (++kb == p.KB) kb = 0;
                 ++run;
                 if (kb == 0 || u + 1 == u1 || (in_runs(MODE) && run == longest))
-                    mma_commit_16<1>(&acc_full[j % ACCS]);
+                    mma_commit_16<1>(&acc_full[j & (ACCS - 1)]);
             }
         }
     } else if (warp >= 4) {
@@ -333,26 +333,26 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 share.load<MODE>(more.head, m0 + first_col + (lane & 15), p.M, factor);
             static_assert(COLS == 16, "a warp's columns are one load");
             uint32_t r[16];
-            bool ok = mbar_wait(&acc_full[j % ACCS], (j / ACCS) & 1);
+            bool ok = mbar_wait(&acc_full[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS) & 1);
             if (!ok) break;
             tc_after_sync();
-            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j % ACCS) * NT + first_col), r);
+            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & (ACCS - 1)) * NT + first_col), r);
             tmem_ld_wait();
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[j % ACCS]);
+            if (lane == 0) mbar_arrive(&acc_free[j & (ACCS - 1)]);
             if constexpr (in_runs(MODE)) {  // the other runs' sums
                 for (int first = more.head.run; first < n_units; first += more.head.run) {
                     ++j;
-                    ok = mbar_wait(&acc_full[j % ACCS], (j / ACCS) & 1);
+                    ok = mbar_wait(&acc_full[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS) & 1);
                     if (!ok) break;
                     tc_after_sync();
                     uint32_t next[16];
-                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j % ACCS) * NT + first_col), next);
+                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & (ACCS - 1)) * NT + first_col), next);
                     tmem_ld_wait();
                     tc_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[j % ACCS]);
+                    if (lane == 0) mbar_arrive(&acc_free[j & (ACCS - 1)]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(next[i]));
                 }
