@@ -168,11 +168,11 @@ Gemm16 logits(const Head16 &h, int t0, int T, int v0, int n) {
     return g;
 }
 
-// k-blocks that one accumulator of the streaming product sums: runs of 512 values, and of 64 for at most 1024 entries. A
+// k-blocks that one accumulator of the streaming product sums: runs of 512 values, and of 64 for at most 512 entries. A
 // small vocabulary can have labels so certain that p - 1 shows the logit's last digits. (One token of V x 704, the worst dX of
 // 12 inputs, runs of 512 and 64, a plain fp32 product: V = 56 3.7e-2, 3.9e-3, 3.7e-3; 200 2.6e-2, 3.3e-3, 3.0e-3; 500 and more
-// the same with both. The loss in us: one token of 32000 x 4096 48.9 and 53.8, 7899 of 48 x 1816 19.0 and 21.2.)
-int stream_run(const Head16 &h) { return h.V <= 1024 ? 1 : 8; }
+// the same with both. The loss in us: one token of 32000 x 4096 47.8 and 52.4, 7899 of 48 x 1816 18.6 and 22.4.)
+int stream_run(const Head16 &h) { return h.V <= 512 ? 1 : 8; }
 
 cudaError_t pack(Head16 &h, cudaStream_t stream, const char **detail) {
     const Pack16 packs[2] = {{&h.X, &h.ldx, h.T, h.D}, {&h.W, &h.ldw, h.w_dv ? h.D : h.V, h.w_dv ? h.V : h.D}};

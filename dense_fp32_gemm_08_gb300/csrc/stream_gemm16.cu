@@ -2,16 +2,16 @@
 // by streaming B (the weights) from memory once. The split of the work is in stream16.cuh. Roles
 // of a CTA's warps:
 //   warp 0, lane 0: TMA producer (a 128 x 64 block of weights and the tokens' 64 k values per unit)
-//   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns, four for the head's logits
+//   warp 1, lane 0: MMA issuer into one of two TMEM accumulators of NT columns
 //   warp 2:         TMEM allocation
 //   warps 4..:      epilogue: lane = output feature, columns = 16 tokens per warp. Whole tiles go from
 //                   TMEM to the epilogue; pieces go to scratch in fp32, and the warp that completes
 //                   its part of a tile sums them in the order of k.
 // The head's products for few tokens run here too (PairMode): logits, reduced and not written; their gradient; dX.
 //
-// Measured, one row 4096 -> 14336 bf16 with bias and SiLU (117 MB): 24.0 us, 4.9 TB/s: 112 whole tiles, of
-// 64 blocks at 0.325 us, and 2.9 us until the first block arrives, for the epilogue and the launch. One row
-// 14336 -> 16384 (470 MB): 77.9 us, 6.0 TB/s. 8 rows 512 -> 512: 5.1 us, launch and round trips to memory. With the
+// Measured, one row 4096 -> 14336 bf16 with bias and SiLU (117 MB): 22.0 us, 5.3 TB/s: 112 whole tiles, of
+// 64 blocks at 0.30 us, and 2.9 us until the first block arrives, for the epilogue and the launch. One row
+// 14336 -> 16384 (470 MB): 76.5 us, 6.1 TB/s. 8 rows 512 -> 512: 4.9 us, launch and round trips to memory. With the
 // join of its parts: the loss of one token, 32000 x 4096 (262 MB), 48 us, 5.5 TB/s; of 64 tokens of 1000 x 512 7.4 us.
 #include "activation16.cuh"
 #include "layer16.cuh"
@@ -57,10 +57,7 @@ struct StreamMore<kPairLayer> {
 
 // The logits are summed in runs of k-blocks, each with an accumulator of its own (see the pair product).
 __host__ __device__ constexpr bool in_runs(int mode) { return mode == kPairLogits || mode == kPairLogitGrad; }
-// Accumulators that a tile's or a run's epilogue and the next ones' MMAs take in turn. (Runs of 512, one token's loss at 8000 x
-// 8192: 28.2 us with four, 29.9 with two; 16 tokens of 32000 x 1024 16.4 and 17.3.)
-constexpr int kMaxAccs = 4;
-__host__ __device__ constexpr int accumulators(int mode) { return in_runs(mode) ? kMaxAccs : 2; }
+constexpr int kAccs = 2;  // accumulators (four for the logits' runs: the same times)
 
 template <int NT>
 struct StreamConfig {
@@ -76,8 +73,8 @@ struct StreamConfig {
     static constexpr bool TOKEN_TILES = NT == 64;  // fewer tokens are one tile
     static constexpr int CTAS = NT <= 32 ? 2 : 1;
     static constexpr int STAGES = NT <= 16 ? 6 : NT <= 32 ? 5 : 8;
-    __host__ __device__ static constexpr uint32_t tmem_cols(int accs) { return accs * NT < 32 ? 32 : accs * NT; }
-    static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 2 * kMaxAccs) * 8 + 32 + 1024;
+    static constexpr uint32_t TMEM_COLS = kAccs * NT < 32 ? 32 : kAccs * NT;
+    static constexpr size_t SMEM = STAGES * STAGE_BYTES + (2 * STAGES + 2 * kAccs) * 8 + 32 + 1024;
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -195,15 +192,15 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     stream_gemm16_kernel(const __grid_constant__ CUtensorMap map_w,
                          const __grid_constant__ CUtensorMap map_x, const StreamParams p, const StreamMore<MODE> more) {
     using C = StreamConfig<NT>;
-    constexpr int STAGES = C::STAGES, ACCS = accumulators(MODE);
+    constexpr int STAGES = C::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
     uint8_t *smem = smem_raw + pad;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * C::STAGE_BYTES);
     uint64_t *empty = full + STAGES;
-    uint64_t *acc_full = empty + STAGES;    // [ACCS]
-    uint64_t *acc_free = acc_full + ACCS;  // [ACCS]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + ACCS);
+    uint64_t *acc_full = empty + STAGES;    // [kAccs]
+    uint64_t *acc_free = acc_full + kAccs;  // [kAccs]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_free + kAccs);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u0 = p.split.first(blockIdx.x), u1 = p.split.first(blockIdx.x + 1);
@@ -215,13 +212,13 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int j = 0; j < ACCS; ++j) {
+        for (int j = 0; j < kAccs; ++j) {
             mbar_init(&acc_full[j], 1);
             mbar_init(&acc_free[j], 4 * C::GROUPS);
         }
         mbar_init_fence();
     }
-    if (warp == 2) tmem_alloc<1>(tmem_slot, C::tmem_cols(ACCS));
+    if (warp == 2) tmem_alloc<1>(tmem_slot, C::TMEM_COLS);
     tc_before_sync();
     __syncthreads();
     tc_after_sync();
@@ -278,36 +275,40 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     } else if (warp == 1) {
         if (lane == 0) {
             RingCursor<STAGES> ring;
-            int j = -1, kb = u0 % p.KB, run = 0;
+            RingCursor<kAccs> acc;
+            int kb = u0 % p.KB;
             bool ok = true;
-            uint32_t d = tmem;
-            int longest = 0;
-            if constexpr (in_runs(MODE)) longest = more.head.run;
-            for (int u = u0; u < u1 && ok; ++u) {
+            // What a block costs this thread bounds the kernel (one row 4096 -> 14336: 24.3 us with the tests for
+            // a tile's or a run's end made per block, 21.9 with a loop over its blocks; another 0.1 less with descriptors
+            // that are added up). Descriptors of stage 0; their start addresses count 16 bytes.
+            const uint64_t dw0 = W_MN ? desc_mn_major(smem_addr(smem), 8192) : desc_k_major(smem_addr(smem));
+            const uint64_t dx0 = desc_k_major(smem_addr(smem) + C::A_BYTES);
+            for (int u = u0; u < u1 && ok;) {
                 // A new accumulator per tile, and per run of blocks that one sums (see the pair product).
-                const bool first = u == u0 || kb == 0 || (in_runs(MODE) && run == longest);
-                if (first) {
-                    ++j;
-                    run = 0;
-                    if (j >= ACCS && !mbar_wait(&acc_free[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS - 1) & 1)) break;
-                    tc_after_sync();
-                    d = tmem + static_cast<uint32_t>((j & (ACCS - 1)) * NT);
-                }
-                if (!mbar_wait(&full[ring.stage], ring.parity)) break;
+                int blocks = min(p.KB - kb, u1 - u);
+                if constexpr (in_runs(MODE)) blocks = min(blocks, more.head.run);
+                if (!mbar_wait(&acc_free[acc.stage], acc.parity ^ 1u)) break;  // (a new barrier's last phase is over)
                 tc_after_sync();
-                const uint32_t sw = smem_addr(smem + ring.stage * C::STAGE_BYTES), sx = sw + C::A_BYTES;
-                const uint64_t dw = W_MN ? desc_mn_major(sw, 8192) : desc_k_major(sw);
-                const uint64_t dx = desc_k_major(sx);
+                const uint32_t d = tmem + static_cast<uint32_t>(acc.stage * NT);
+                for (int i = 0; i < blocks; ++i) {
+                    ok = mbar_wait(&full[ring.stage], ring.parity);
+                    if (!ok) break;
+                    tc_after_sync();
+                    const uint64_t stage = static_cast<uint64_t>(ring.stage * (C::STAGE_BYTES >> 4));
+                    const uint64_t dw = dw0 + stage, dx = dx0 + stage;
 #pragma unroll
-                for (int k = 0; k < kStreamK / 16; ++k)
-                    mma_16<1>(d, dw + static_cast<uint64_t>(k * (W_MN ? 128 : 2)),
-                              dx + static_cast<uint64_t>(k * 2), p.idesc, !first || k > 0);
-                mma_commit_16<1>(&empty[ring.stage]);
-                ring.next();
-                if (++kb == p.KB) kb = 0;
-                ++run;
-                if (kb == 0 || u + 1 == u1 || (in_runs(MODE) && run == longest))
-                    mma_commit_16<1>(&acc_full[j & (ACCS - 1)]);
+                    for (int k = 0; k < kStreamK / 16; ++k)
+                        mma_16<1>(d, dw + static_cast<uint64_t>(k * (W_MN ? 128 : 2)),
+                                  dx + static_cast<uint64_t>(k * 2), p.idesc, i > 0 || k > 0);
+                    mma_commit_16<1>(&empty[ring.stage]);
+                    ring.next();
+                }
+                if (!ok) break;
+                mma_commit_16<1>(&acc_full[acc.stage]);
+                acc.next();
+                u += blocks;
+                kb += blocks;
+                if (kb == p.KB) kb = 0;
             }
         }
     } else if (warp >= 4) {
@@ -319,8 +320,8 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
         if constexpr (MODE == kPairSum) factor = more.sum.scale * *more.sum.factor;
         if constexpr (MODE == kPairLogitGrad)
             if (more.head.factor) factor = *more.head.factor;
-        int j = 0;
-        for (int u = u0; u < u1; ++j) {
+        RingCursor<kAccs> acc;
+        for (int u = u0; u < u1; acc.next()) {
             const int tile = u / p.KB, kb0 = u - tile * p.KB;
             const int n_units = min(p.KB - kb0, u1 - u);
             u += n_units;
@@ -333,26 +334,26 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
                 share.load<MODE>(more.head, m0 + first_col + (lane & 15), p.M, factor);
             static_assert(COLS == 16, "a warp's columns are one load");
             uint32_t r[16];
-            bool ok = mbar_wait(&acc_full[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS) & 1);
+            bool ok = mbar_wait(&acc_full[acc.stage], acc.parity);
             if (!ok) break;
             tc_after_sync();
-            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & (ACCS - 1)) * NT + first_col), r);
+            tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>(acc.stage * NT + first_col), r);
             tmem_ld_wait();
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_free[j & (ACCS - 1)]);
+            if (lane == 0) mbar_arrive(&acc_free[acc.stage]);
             if constexpr (in_runs(MODE)) {  // the other runs' sums
                 for (int first = more.head.run; first < n_units; first += more.head.run) {
-                    ++j;
-                    ok = mbar_wait(&acc_full[j & (ACCS - 1)], (static_cast<unsigned>(j) / ACCS) & 1);
+                    acc.next();
+                    ok = mbar_wait(&acc_full[acc.stage], acc.parity);
                     if (!ok) break;
                     tc_after_sync();
                     uint32_t next[16];
-                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>((j & (ACCS - 1)) * NT + first_col), next);
+                    tmem_ld_x16(tmem + lane_base + static_cast<uint32_t>(acc.stage * NT + first_col), next);
                     tmem_ld_wait();
                     tc_before_sync();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&acc_free[j & (ACCS - 1)]);
+                    if (lane == 0) mbar_arrive(&acc_free[acc.stage]);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) + __uint_as_float(next[i]));
                 }
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
     __syncthreads();
     if (warp == 2) {
         tc_after_sync();
-        tmem_dealloc<1>(tmem, C::tmem_cols(ACCS));
+        tmem_dealloc<1>(tmem, C::TMEM_COLS);
     }
 }
 
@@ -420,7 +421,8 @@ cudaError_t launch(const Gemm16 &g, const PairExtra &extra, cudaStream_t stream,
     // Equal pieces of every tile, of 5 blocks or more (8 for more columns, whose pieces take longer to
     // sum): a CTA then has one piece, and the tiles complete together. Else the blocks of all tiles in
     // equal runs over all SMs. Pieces where more would be shorter than that anyway, or where they take
-    // less time: a block streams in 0.325 us on some of the SMs and 0.369 on all, whose rate memory
+    // less time (as measured when the blocks took 8% longer on some SMs; the split decides the order of the sums, so it
+    // stays): a block streams in 0.325 us on some of the SMs and 0.369 on all, whose rate memory
     // bounds; a whole tile takes 2.9 us besides, a cut one 4.4, runs that cross tiles 7.5. (One row,
     // pieces and runs: 96 tiles of 64 blocks 23.7 and 22.2 us, 112 23.9 and 24.9, 120 24.2 and 27.3; 112 of 224
     // blocks 76.0 and 69.1; 39 of 32 in three pieces 9.5 and 11.3; 52 of 224 in two 42.3 and 35.8.)
