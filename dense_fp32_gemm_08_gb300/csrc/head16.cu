@@ -26,7 +26,8 @@ namespace sg {
 namespace {
 
 constexpr float kLn2 = 0.693147182f, kLn2Rest = -1.904654e-9f;  // ln 2 in two parts
-// Maximum and sum of powers of 2 of two parts together. (A part without finite logits has m = -inf, s = 0.)
+// Maximum and sum of powers of 2 of two parts together. (A part of logits of -inf has m = -inf, s = 0. The maximum
+// leaves NaN out, the sum does not: a part of NaN has m = -inf, s = NaN.)
 __device__ __forceinline__ float2 join(float2 a, float2 b) {
     const float m = fmaxf(a.x, b.x);
     const float base = m == -INFINITY ? 0.0f : m;
@@ -63,7 +64,7 @@ struct LossOut {
     int T, V;
     float *loss, *lse;
     __device__ __forceinline__ void put(int row, float2 a) const {
-        const float l = a.x == -INFINITY ? a.x : fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
+        const float l = a.x == -INFINITY && a.y == 0.0f ? a.x : fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
         const int64_t label = labels[row];
         if (lse) lse[row] = l;
         if (loss) loss[row] = label >= 0 && label < V ? l - at[row] : 0.0f;
