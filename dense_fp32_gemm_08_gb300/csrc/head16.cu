@@ -252,8 +252,8 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
     x.incd = h.incd;
     const float unit = unit_of(h.dtype);
     extra.sum.scale = 1.0f / unit;
+    x.unit = unit;
     if (h.incd == 0) {
-        x.unit = unit;
         extra.sum.factor = h.dloss;
     } else {
         err = layer_scratch(kScratchHead, stream, 8, &p, detail);

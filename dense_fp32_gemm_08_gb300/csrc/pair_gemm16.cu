@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         uint32_t raw[20];  // the next block's residual
         float bias[2] = {0.0f, 0.0f};  // of columns col0 + lane and col0 + 32 + lane
         float factor = 1.0f;
-        if (MODE == kPairSum) factor = p.extra.sum.scale * *p.extra.sum.factor;
+        if (MODE == kPairSum) factor = p.extra.sum.multiplier();
         if (MODE == kPairLogitGrad && p.extra.head.factor) factor = *p.extra.head.factor;
         for (int t = pair; t < p.total_items; t += pairs, ++j) {
             const int set = j & 1;
@@ -481,8 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             float lse = 0.0f, dloss = 0.0f;
             if (MODE == kPairLogitGrad && label.counts) {
                 lse = p.extra.head.lse[row0 + lane];
-                dloss = p.extra.head.factor ? factor * p.extra.head.dloss[(row0 + lane) * p.extra.head.incd]
-                                            : p.extra.head.unit;
+                dloss = p.extra.head.weight(row0 + lane, factor);
             }
             if constexpr (in_runs(MODE)) {
                 float2 v[32];

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <math.h>
 
 #include "layer16.cuh"
 
@@ -49,18 +50,32 @@ struct PairHead {
     float2 *parts = nullptr;
     long long ld_parts = 0;
     float *at = nullptr;
-    // kPairLogitGrad: the rows' weights are factor * dloss, or `unit` for every row without a factor.
+    // kPairLogitGrad: the rows' weights are *factor * dloss, and the outputs are multiplied by 1 / *factor. Without a factor
+    // all rows have one dloss: their weight is `unit`, and the outputs are multiplied by dloss; one that is not finite makes the
+    // weight infinite or NaN, in the rows that count alone, and the outputs are left as they are.
     const float *lse = nullptr, *dloss = nullptr;
     long long incd = 0;
     const float *factor = nullptr;
     float unit = 1.0f;
+
+    // Of row t, with f = *factor. (dloss is read per row in either case: with the row's lse, so that it costs no round trip
+    // of its own.)
+    __device__ __forceinline__ float weight(long long t, float f) const {
+        const float d = dloss[t * incd];
+        return factor ? f * d : fabsf(d) < INFINITY ? unit : unit * d;
+    }
 };
 // The first product's sums, in the kernel's own order; a piece that is not the last writes no output.
 struct PairSum {
     float *sums = nullptr;
     int first = 1, last = 1;
-    const float *factor = nullptr;  // times scale, multiplies both products' outputs
+    const float *factor = nullptr;  // if finite, times scale, multiplies both products' outputs
     float scale = 1.0f;
+
+    __device__ __forceinline__ float multiplier() const {
+        const float f = *factor;
+        return fabsf(f) < INFINITY ? scale * f : scale;
+    }
 };
 struct PairExtra {
     PairSave8 save;

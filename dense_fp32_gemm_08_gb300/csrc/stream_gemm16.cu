@@ -109,7 +109,7 @@ struct TokenShare {
         label = static_cast<int>(l);
         if constexpr (MODE == kPairLogitGrad) {
             lse = h.lse[t];
-            dloss = h.factor ? factor * h.dloss[t * h.incd] : h.unit;
+            dloss = h.weight(t, factor);
         }
     }
 };
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(StreamConfig<NT>::THREADS, StreamConfig<NT>::C
         constexpr int COLS = NT / C::GROUPS;
         const int first_col = (warp - 4) / 4 * COLS;
         float factor = 1.0f;
-        if constexpr (MODE == kPairSum) factor = more.sum.scale * *more.sum.factor;
+        if constexpr (MODE == kPairSum) factor = more.sum.multiplier();
         if constexpr (MODE == kPairLogitGrad)
             if (more.head.factor) factor = *more.head.factor;
         RingCursor<kAccs> acc;

@@ -441,10 +441,11 @@ sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64
  * of the vocabulary at a time. A piece's dz lives in a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
  * sums over several pieces in another of 4 * T' * D' bytes (T and D rounded up to multiples of 256). The products read dz
  * in the call's dtype, for weights dloss / m, m the largest finite |dloss[t]| of the tokens that count (incd == 0: m =
- * dloss[0], whatever it is), in half times 2^14; the outputs are multiplied by m (in half, divided by 2^14). So equal
- * dloss are not rounded at all, and half holds probabilities down to 2^-38. With incd == 0 a dloss that is not finite
- * makes every value of dX and dW NaN or infinite. X of a token that does not count is multiplied by 0 for dW, as in
- * the formula, so it must be finite. Outputs must not overlap inputs or each other.
+ * dloss[0] if that is finite, else 1), in half times 2^14; the outputs are multiplied by m (in half, divided by 2^14). So
+ * equal dloss are not rounded at all, and half holds probabilities down to 2^-38 (a token whose dloss is below 2^-38 of
+ * the largest has no gradient there). A dloss that is not finite makes dX of its own token (with incd == 0, of each that
+ * counts) and then dW infinite or NaN. X of a token that does not count is multiplied by 0 for dW, as in the formula, so
+ * it must be finite. Outputs must not overlap inputs or each other.
  */
 sgemm_status_t sgemm_cross_entropy_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
                                             const float *dloss, int64_t incd, const void *X, int64_t ldx,
