@@ -8,8 +8,8 @@
 // logits of a warp to their maximum and sum of exponentials, or the streaming product for few tokens
 // (stream_gemm16.cu) with one that does so for 32; a second kernel joins those. The gradient
 // computes the logits again, a piece of the vocabulary at a time: one product whose epilogue
-// writes the piece's dz in 16 bits to scratch, then dX and dW's rows (or columns) of the piece in one
-// launch. dX adds up over the pieces in fp32.
+// writes the piece's dz in 16 bits to scratch, a pass over its entries at labels that are all but certain, then dX and
+// dW's rows (or columns) of the piece in one launch. dX adds up over the pieces in fp32.
 //
 // Bound by the tensor cores for many tokens: 16384 of 32000 x 4096 bf16 2.24 to 2.45 ms for the loss (1,750 to 1,916
 // TFLOP/s; the join 16 us of it), 6.47 to 7.12 ms for the gradient (three products, 1,810 to 1,990). For few by reading the
@@ -58,24 +58,132 @@ __device__ __forceinline__ float2 join_run(const float2 *part, long long apart, 
     }
     return a;
 }
+
+// ---- labels that are all but certain --------------------------------------------------------------
+//
+// Where p is near 1 at the label, p - 1 has only the last digits of that one logit, and the accumulators of the
+// tensor cores, which cut their sums, lose them: by up to a step of fp32 per 16 products (dX of such a token of 704 values
+// 4e-2 off; 4e-3 in plain fp32). So those logits, and no others, are multiplied once more: x_t . w_label with
+// every addition's rounding kept (Knuth's two-sum; products of 16-bit values are exact in fp32), within a step
+// of fp32 of the true sum. The loss corrects lse and the label's logit with it, the gradient its dz there.
+// It is done for 1 - p < 2^-6, in half 2^-3: above, what is lost is less than half a rounding of dz (logits of 10 in runs of
+// 1024 lose 1.5e-5). (In the epilogues of the products, for every label, as it comes: 16384 tokens of 32000 x 4096 took
+// 6% longer, of W stored D x V 3 times as long, of 56 entries 8 times.)
+// Bound by reading rows of W, and columns 32 bytes per value where W is stored D x V. The loss and the gradient of 16384 tokens
+// in ms, no label certain, and every one: V x D 32000 x 4096 2.28, 6.8, and 2.34, 6.9; stored D x V 2.28, 6.7, and 3.5, 7.8;
+// 256 x 4096 stored D x V 0.034, 0.113, and 0.54, 0.31.
+template <typename T>
+constexpr float kCertain = Half16<T>::kind == kBf16 ? 0.015625f : 0.125f;  // 1 - p, and nearly -log p
+
+struct LabelProduct {
+    const uint16_t *x, *w;  // both in rows that TMA can address
+    long long ldx, ldw;
+    int D;
+    bool w_dv;  // false: W stored V x D; true: D x V
+};
+
+struct KeptSum {
+    float s = 0.0f, rest = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float t = s + v, b = t - s;  // b: what was added of v
+        rest += (s - (t - b)) + (v - b);
+        s = t;
+    }
+};
+
+// Row `t` of X times row (D x V: column) `v` of W, by a whole warp; every lane has the result. UNROLL: loads of 8 values under
+// way (D x V: 4 UNROLL of one).
+template <typename T, int UNROLL>
+__device__ __forceinline__ float label_logit(const LabelProduct &p, long long t, long long v, int lane) {
+    using H = Half16<T>;
+    KeptSum sum;
+    const uint16_t *x = p.x + t * p.ldx;
+    if (p.w_dv) {
+        const uint16_t *w = p.w + v;
+        for (int d0 = lane; d0 < p.D; d0 += 32 * 4 * UNROLL) {
+            uint16_t xv[4 * UNROLL], wv[4 * UNROLL];
+#pragma unroll
+            for (int i = 0; i < 4 * UNROLL; ++i) {
+                const int d = d0 + 32 * i;
+                xv[i] = d < p.D ? __ldg(x + d) : 0;
+                wv[i] = d < p.D ? __ldg(w + d * p.ldw) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < 4 * UNROLL; ++i) sum.add(__fmul_rn(H::widen(xv[i]), H::widen(wv[i])));
+        }
+    } else {
+        const uint16_t *w = p.w + v * p.ldw;
+        const int whole = p.D & ~7;
+        for (int d0 = 8 * lane; d0 < whole; d0 += 256 * UNROLL) {
+            uint4 xv[UNROLL], wv[UNROLL];
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                xv[i] = wv[i] = make_uint4(0, 0, 0, 0);
+                if (d0 + 256 * i < whole) {
+                    xv[i] = __ldg(reinterpret_cast<const uint4 *>(x + d0 + 256 * i));
+                    wv[i] = __ldg(reinterpret_cast<const uint4 *>(w + d0 + 256 * i));
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < UNROLL; ++i) {
+                const uint32_t a[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w}, b[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 q = __fmul2_rn(H::widen2(a[k]), H::widen2(b[k]));
+                    sum.add(q.x);
+                    sum.add(q.y);
+                }
+            }
+        }
+        if (whole + lane < p.D) sum.add(__fmul_rn(H::widen(__ldg(x + whole + lane)), H::widen(__ldg(w + whole + lane))));
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) {
+        const float s = __shfl_xor_sync(0xFFFFFFFFu, sum.s, m);
+        sum.rest += __shfl_xor_sync(0xFFFFFFFFu, sum.rest, m);
+        sum.add(s);
+    }
+    return fabsf(sum.s) < INFINITY ? sum.s + sum.rest : sum.s;  // (the roundings of an infinite sum are NaN)
+}
+
 struct LossOut {
     const float *at;
     const int64_t *labels;
     int T, V;
     float *loss, *lse;
-    __device__ __forceinline__ void put(int row, float2 a) const {
+    LabelProduct product;
+    // By a whole warp, each lane with the row's `a`.
+    template <typename T16, int UNROLL>
+    __device__ __forceinline__ void put(int row, float2 a, int lane) const {
         const float l = a.x == -INFINITY && a.y == 0.0f ? a.x : fmaf(a.x, kLn2, fmaf(a.x, kLn2Rest, logf(a.y)));
         const int64_t label = labels[row];
+        const bool counts = label >= 0 && label < V;
+        const float minus_logp = counts ? l - at[row] : 0.0f;
+        if (counts && minus_logp < kCertain<T16>) {
+            put_certain<T16, UNROLL>(row, l, lane);
+        } else if (lane == 0) {
+            if (lse) lse[row] = l;
+            if (loss) loss[row] = minus_logp;
+        }
+    }
+    // (Not part of the joins' code: its registers made theirs spill.)
+    template <typename T16, int UNROLL>
+    __device__ __noinline__ void put_certain(int row, float l, int lane) const {
+        const float z = at[row], exact = label_logit<T16, UNROLL>(product, row, labels[row], lane);
+        if (lane != 0) return;
+        // The sum's share of it changes by that difference, which is small; and no sum is below one of its parts.
+        l = fmaxf(fmaf(expf(z - l), exact - z, l), exact);
         if (lse) lse[row] = l;
-        if (loss) loss[row] = label >= 0 && label < V ? l - at[row] : 0.0f;
+        if (loss) loss[row] = l - exact;
     }
 };
 
 // Joins the parts of 32 rows, parts[part][row]: lane = row, a warp every 32nd part, then the warps through
 // shared memory. (500 parts of 16384 rows 16 us, of 777 rows 6 us.)
 constexpr int kJoinThreads = 1024;
+template <typename T16>
 __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const float2 *parts, long long ld, int n_parts,
-                                                            const LossOut out) {
+                                                            const __grid_constant__ LossOut out) {
     __shared__ float2 shared[32][33];
     grid_dependents();
     grid_dependency();
@@ -88,13 +196,14 @@ __global__ void __launch_bounds__(kJoinThreads, 2) join_kernel(const float2 *par
     // Warp w now joins row w's 32 values.
     a = join_lanes(shared[lane][warp]);
     const int mine = blockIdx.x * 32 + warp;
-    if (lane == 0 && mine < out.T) out.put(mine, a);
+    if (mine < out.T) out.put<T16, 1>(mine, a, lane);
 }
 
 // Joins parts[row][part]: a row per warp, or per CTA where it has many parts.
 constexpr int kRowWarps = 8;
+template <typename T16>
 __global__ void __launch_bounds__(32 * kRowWarps) join_rows_kernel(const float2 *parts, long long ld, int n_parts,
-                                                                   int wide, const LossOut out) {
+                                                                   int wide, const __grid_constant__ LossOut out) {
     __shared__ float2 shared[kRowWarps];
     grid_dependents();
     grid_dependency();
@@ -107,14 +216,14 @@ __global__ void __launch_bounds__(32 * kRowWarps) join_rows_kernel(const float2 
     }
     a = join_lanes(a);
     if (!wide) {
-        if (lane == 0 && row < out.T) out.put(row, a);
+        if (row < out.T) out.put<T16, 4>(row, a, lane);
         return;
     }
     if (lane == 0) shared[warp] = a;
     __syncthreads();
     if (warp == 0) {
         a = join_lanes(lane < kRowWarps ? shared[lane] : make_float2(-INFINITY, 0.0f));
-        if (lane == 0) out.put(row, a);
+        out.put<T16, 4>(row, a, lane);
     }
 }
 
@@ -154,6 +263,36 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long l
     }
 }
 
+// The entries of dz at labels that are all but certain once more, of a piece of n entries: a warp finds them among
+// `each` tokens, as few as fill the GPU once (32 at most), and multiplies them one by one.
+int tokens_each(int T) { return std::min(32, 1 + T / 8192); }
+template <typename T16>
+__global__ void __launch_bounds__(256) certain_kernel(const PairHead h, const LabelProduct product, uint16_t *dz, long long ldz,
+                                                      int T, int n, int each) {
+    grid_dependents();
+    grid_dependency();
+    const int lane = threadIdx.x & 31;
+    const long long t0 = (blockIdx.x * 8LL + (threadIdx.x >> 5)) * each, t = t0 + lane;
+    long long label = -1;  // of the entries from v0 on
+    float lse = 0.0f, weight = 0.0f;
+    bool certain = false;
+    if (lane < each && t < T) {
+        const int64_t l = h.labels[t];
+        lse = h.lse[t];
+        weight = h.weight(t, h.factor ? *h.factor : 1.0f);
+        if (l >= h.v0 && l - h.v0 < n) {
+            label = l - h.v0;
+            // weight (p - 1); a weight or value that is not finite is not among them
+            certain = fabsf(Half16<T16>::widen(dz[t * ldz + label])) < kCertain<T16> * fabsf(weight);
+        }
+    }
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, certain); todo != 0; todo &= todo - 1) {
+        const int i = __ffs(todo) - 1;
+        const float z = label_logit<T16, 4>(product, t0 + i, __shfl_sync(0xFFFFFFFFu, label, i), lane);
+        if (lane == i) dz[t * ldz + label] = Half16<T16>::narrow(weight * expm1f(z - lse));
+    }
+}
+
 // The logits of tokens [t0, t0 + T) and vocabulary entries [v0, v0 + n).
 Gemm16 logits(const Head16 &h, int t0, int T, int v0, int n) {
     Gemm16 g;
@@ -169,11 +308,15 @@ Gemm16 logits(const Head16 &h, int t0, int T, int v0, int n) {
     return g;
 }
 
-// k-blocks that one accumulator of the streaming product sums: runs of 512 values, and of 64 for at most 512 entries. A
-// small vocabulary can have labels so certain that p - 1 shows the logit's last digits. (One token of V x 704, the worst dX of
-// 12 inputs, runs of 512 and 64, a plain fp32 product: V = 56 3.7e-2, 3.9e-3, 3.7e-3; 200 2.6e-2, 3.3e-3, 3.0e-3; 500 and more
-// the same with both. The loss in us: one token of 32000 x 4096 47.8 and 52.4, 7899 of 48 x 1816 18.6 and 22.4.)
-int stream_run(const Head16 &h) { return h.V <= 512 ? 1 : 8; }
+LabelProduct label_product(const Gemm16 &g) { return {g.A, g.B, g.lda, g.ldb, g.K, g.b_mn}; }
+
+// k-blocks that one accumulator of the streaming product sums: in the gradient runs of 64 values, with which its logits are
+// as exact as a plain fp32 product's (one token of 704 values at labels all but certain: dX 4e-3 off, as there; certain_kernel
+// after it instead costs about as much, and 1.5 us more where labels are certain); in the loss of 512, and of 64 for at most 512
+// entries. (In us: the gradient of 64 tokens of 1000 x 512 16.3, in runs of 512 15.0; of 16 of 32000 x 4096 170 and 164. The
+// loss of one token of 32000 x 4096 52.4 and 47.8, of 7899 of 48 x 1816 22.4 and 18.6.)
+constexpr int kGradRun = 1;
+int loss_run(const Head16 &h) { return h.V <= 512 ? 1 : 8; }
 
 cudaError_t pack(Head16 &h, cudaStream_t stream, const char **detail) {
     const Pack16 packs[2] = {{&h.X, &h.ldx, h.T, h.D}, {&h.W, &h.ldw, h.w_dv ? h.D : h.V, h.w_dv ? h.V : h.D}};
@@ -202,23 +345,24 @@ cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **
         PairHead &x = extra.head;
         x.labels = h.labels + t0;
         x.V = h.V;
-        x.run = stream_run(h);
+        x.run = loss_run(h);
         x.at = static_cast<float *>(p);
         x.parts = reinterpret_cast<float2 *>(x.at + ld);
         x.ld_parts = ld_parts;
-        const LossOut out{x.at, x.labels, T, h.V, h.loss ? h.loss + t0 : nullptr, h.lse ? h.lse + t0 : nullptr};
+        const LossOut out{x.at, x.labels, T, h.V, h.loss ? h.loss + t0 : nullptr, h.lse ? h.lse + t0 : nullptr,
+                          label_product(g)};
         const float2 *parts = x.parts;
         if (few) {
             err = stream_gemm16_extra_launch(g, kPairLogits, extra, stream, detail);
             if (err != cudaSuccess) return err;
             const int wide = n_parts > 128;
-            err = launch_early(join_rows_kernel, dim3(static_cast<unsigned>(wide ? T : (T + kRowWarps - 1) / kRowWarps)),
+            err = launch_early(h.dtype == kBf16 ? join_rows_kernel<__nv_bfloat16> : join_rows_kernel<__half>, dim3(static_cast<unsigned>(wide ? T : (T + kRowWarps - 1) / kRowWarps)),
                                32 * kRowWarps, 0, stream, parts, ld_parts, n_parts, wide, out);
         } else {
             err = pair_gemm16_extra_launch(&g, 1, kPairLogits, extra, stream, detail);
             if (err != cudaSuccess) return err;
-            err = launch_early(join_kernel, dim3(static_cast<unsigned>((T + 31) / 32)), kJoinThreads, 0, stream,
-                               parts, ld_parts, n_parts, out);
+            err = launch_early(h.dtype == kBf16 ? join_kernel<__nv_bfloat16> : join_kernel<__half>,
+                               dim3(static_cast<unsigned>((T + 31) / 32)), kJoinThreads, 0, stream, parts, ld_parts, n_parts, out);
         }
         if (err != cudaSuccess) {
             *detail = "loss kernel launch failed";
@@ -246,7 +390,7 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
     PairHead &x = extra.head;
     x.labels = h.labels;
     x.V = h.V;
-    x.run = stream_run(h);
+    x.run = kGradRun;
     x.lse = h.lse_in;
     x.dloss = h.dloss;
     x.incd = h.incd;
@@ -278,9 +422,21 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
         g.D = static_cast<uint16_t *>(dz);
         g.ldd = ldz;
         x.v0 = v0;
-        err = stream_gemm16_supports(g) ? stream_gemm16_extra_launch(g, kPairLogitGrad, extra, stream, detail)
-                                        : pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
-        if (err != cudaSuccess) return err;
+        if (stream_gemm16_supports(g)) {
+            err = stream_gemm16_extra_launch(g, kPairLogitGrad, extra, stream, detail);
+            if (err != cudaSuccess) return err;
+        } else {
+            err = pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
+            if (err != cudaSuccess) return err;
+            const int each = tokens_each(h.T);
+            err = launch_early(h.dtype == kBf16 ? certain_kernel<__nv_bfloat16> : certain_kernel<__half>,
+                               dim3(static_cast<unsigned>((h.T + 8LL * each - 1) / (8 * each))), 256, 0, stream, x,
+                               label_product(g), g.D, ldz, h.T, n, each);
+            if (err != cudaSuccess) {
+                *detail = "loss gradient kernel launch failed";
+                return err;
+            }
+        }
         Gemm16 list[2];
         int count = 0;
         if (h.dX) {

@@ -146,8 +146,7 @@ __device__ __forceinline__ void with_layout(const PairProduct &g, Body body) {
 // The blocks that one accumulator sums. The tensor cores add to it with fp32 sums cut, not rounded, once per 16 k
 // values, which leaves the logits of 4096 values 3e-6 too small; the epilogue adds runs of 1024 in
 // registers (16384 x 32000 x 4096: the loss's error falls from 2.9e-6 to 6.6e-7, a plain fp32 product's is 6.1e-7).
-// So do the gradient's, since p - 1 at a label that is all but certain has the logit's last digits. (They are the forward pass's
-// to the bit where both passes take the call whole.)
+// So are the gradient's. (The logit at a label that is all but certain needs more: head16.cu.)
 __host__ __device__ constexpr bool in_runs(int mode) { return mode == kPairLogits || mode == kPairLogitGrad; }
 template <int MODE>
 __device__ __forceinline__ int run_blocks(int blocks) {

@@ -423,7 +423,8 @@ sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t
  *   labels  T int64 values. A token whose label is outside [0, V) (such as -100) does not count: its loss is 0.
  *   loss, lse  T fp32 values each; either may be NULL (not computed). lse is what the gradient reads.
  * T == 0 is a no-op. Sums are fp32, in an order that does not depend on timing; a logit's products are added up in
- * runs of 64 to 1024. The workspace holds 8 bytes for every 32 or 64 logits of up to 32768 tokens at a time. A logit of minus
+ * runs of 64 to 1024, and where its label is all but certain (1 - p below 2^-6, in half 2^-3) once more to within a step
+ * of fp32. The workspace holds 8 bytes for every 32 or 64 logits of up to 32768 tokens at a time. A logit of minus
  * infinity has probability 0; plus infinity, NaN, or a magnitude above 2^127 makes its token's lse and loss NaN.
  */
 sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
@@ -445,7 +446,8 @@ sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64
  * equal dloss are not rounded at all, and half holds probabilities down to 2^-38 (a token whose dloss is below 2^-38 of
  * the largest has no gradient there). A dloss that is not finite makes dX of its own token (with incd == 0, of each that
  * counts) and then dW infinite or NaN. X of a token that does not count is multiplied by 0 for dW, as in the formula, so
- * it must be finite. Outputs must not overlap inputs or each other.
+ * it must be finite. p - 1 at a label that is all but certain is as exact as from plain fp32 logits, whichever lse is
+ * given. Outputs must not overlap inputs or each other.
  */
 sgemm_status_t sgemm_cross_entropy_backward(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t T, int64_t V, int64_t D,
                                             const float *dloss, int64_t incd, const void *X, int64_t ldx,

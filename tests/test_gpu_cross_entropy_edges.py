@@ -7,6 +7,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from test_gpu_cross_entropy import summing_error  # noqa: E402
+
 pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.bfloat16, torch.float16]
@@ -86,3 +88,59 @@ def test_a_mean_over_no_token(sgemm_lib):
     assert bool(torch.isinf(dloss).all()) and dloss.stride(0) == 0
     dx, dw = sg.cross_entropy_backward(dloss, x, w, labels, lse)
     assert not dx.any() and not dw.any()
+
+
+def fp32_step(v):
+    return torch.exp2(torch.floor(torch.log2(v.abs().clamp(min=1e-30))) - 23)
+
+
+@pytest.mark.parametrize("transw", ["T", "N"])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,V,D", [(7, 56, 704), (7, 520, 704), (64, 4000, 1000), (300, 512, 1537), (300, 4000, 704),
+                                   (2304, 520, 704), (8256, 56, 704), (40000, 56, 712),
+                                   (300, 4000, 4104), (40000, 9001, 72)])
+def test_certain_labels_of_any_vocabulary(sgemm_lib, dtype, transw, T, V, D):
+    """1 - p at the labels is about 10^-4 in each vocabulary, on either product and with tokens or entries in pieces, and
+    the gradient no larger, so that the label's logit's own error shows in it. The loss and the pair product's gradient have that
+    logit within a step of fp32 (added up with its roundings kept), the streaming product's in runs of 64 products. Times
+    p < 1 it passes to dX through the label's row of W, with two steps of 1 - p from expm1f. Besides, 2^-14 of each
+    other p (logits below 8 lose up to a step, 2^-21, per 16 products, in two runs of 1024 at most, or 2^-23 at less than
+    2 in five of them); a rounding of each dz to 16 bits (and half of a subnormal step over 2^14 in half); and dX's own sum
+    and rounding. z - lse is exact: they are within a factor 2 of each other."""
+    sg = sgemm_lib
+    u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[dtype] * 1.001
+    tiny = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(T)
+    w = normal(1, V, D, dtype=dtype, scale=1.28 / math.sqrt(D))
+    labels = torch.randint(V, (T,), generator=g, device="cuda")
+    sure = 8.5 + math.log(V / 56) / 1.28 ** 2  # the label's logit leaves the others' sum as far behind
+    x = (normal(2, T, D, dtype=dtype).float() + sure * w[labels].float()).to(dtype)
+    given = w if transw == "T" else w.t().contiguous()
+    ones = torch.full((), 1.0, device="cuda").expand(T)
+    z = x.double() @ w.double().t()
+    exact = torch.logsumexp(z, 1).float()
+    loss, own = sg.cross_entropy(x, given, labels, transw=transw)
+    zl = z.gather(1, labels[:, None])
+    step = fp32_step(zl[:, 0])
+    # The loss: a step of the label's logit, 2^-14 of the others' share, lse in fp32 from m ln 2 (two roundings, m's and
+    # the product's, of 2^-24 each) and its sum's roundings (64 + parts' joins), all of them times lse < 32 or p < 1
+    rest = -torch.expm1(zl[:, 0] - torch.logsumexp(z, 1))
+    assert bool(((loss.double() - (torch.logsumexp(z, 1) - zl[:, 0])).abs() <= 2 * step + 2.0 ** -14 * rest
+                 + (4 * exact.abs() + 64 + V / 256 + 16) * 2.0 ** -24 + 2.0 ** -22).all())
+    length = w.double().norm(dim=1)
+    few = T <= 64 or -(-V // 128) * -(-T // 64) <= 128
+    lost = summing_error(x, w, labels, 64) if few else step
+    for lse in (exact, own):
+        dx, _ = sg.cross_entropy_backward(ones, x, given, labels, lse, transw=transw)
+        assert sg.sgemm_device_status() == sg.SGEMM_OK
+        gap = z - lse.double()[:, None]
+        dz = torch.exp(gap)
+        dz.scatter_(1, labels[:, None], torch.expm1(gap.gather(1, labels[:, None])))
+        ref = dz @ w.double()
+        at = dz.gather(1, labels[:, None])[:, 0].abs()
+        off = (2.0 ** -14 + u) * (dz.abs() @ length) + (lost + 2.0 ** -22 * at) * length[labels]
+        small = 0.0 if dtype is torch.bfloat16 else 2.0 ** -25 * 2.0 ** -14
+        off += small * length.sum() + 1e-5 * (dz.abs() @ w.double().abs()).norm(dim=1)
+        off += u * ref.norm(dim=1) + tiny * math.sqrt(D)
+        ratio = (dx.double() - ref).norm(dim=1) / off
+        assert bool((ratio <= 1.0).all()), float(ratio.max())
