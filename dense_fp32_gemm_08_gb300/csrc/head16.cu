@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(1024) factor_kernel(const float *dloss, long l
 }
 
 // The entries of dz at labels that are all but certain once more, of a piece of n entries: a warp finds them among
-// `each` tokens, as few as fill the GPU once (32 at most), and multiplies them one by one.
+// `each` tokens, as few as fill the GPU once (32 at most), and multiplies them one by one. (1.3 to 4 us of the gradient, and
+// 1 to 2.5 more for few tokens where there are such labels. With runs of 64 on the streaming product in place of it: 16 tokens
+// of 32000 x 4096 168.5 us and 163.5, 256 of 1000 x 512 f16 18.3 and 18.5, with such labels 18.2 and 19.8; dX of one
+// token of 56 x 704 up to 2.7e-2 off and 7.1e-3, in plain fp32 7.8e-3.)
 int tokens_each(int T) { return std::min(32, 1 + T / 8192); }
 template <typename T16>
 __global__ void __launch_bounds__(256) certain_kernel(const PairHead h, const LabelProduct product, uint16_t *dz, long long ldz,
@@ -310,13 +313,10 @@ Gemm16 logits(const Head16 &h, int t0, int T, int v0, int n) {
 
 LabelProduct label_product(const Gemm16 &g) { return {g.A, g.B, g.lda, g.ldb, g.K, g.b_mn}; }
 
-// k-blocks that one accumulator of the streaming product sums: in the gradient runs of 64 values, with which its logits are
-// as exact as a plain fp32 product's (one token of 704 values at labels all but certain: dX 4e-3 off, as there; certain_kernel
-// after it instead costs about as much, and 1.5 us more where labels are certain); in the loss of 512, and of 64 for at most 512
-// entries. (In us: the gradient of 64 tokens of 1000 x 512 16.3, in runs of 512 15.0; of 16 of 32000 x 4096 170 and 164. The
-// loss of one token of 32000 x 4096 52.4 and 47.8, of 7899 of 48 x 1816 22.4 and 18.6.)
-constexpr int kGradRun = 1;
-int loss_run(const Head16 &h) { return h.V <= 512 ? 1 : 8; }
+// k-blocks that one accumulator of the streaming product sums: runs of 512 values, and of 64 in the loss of at most 512
+// entries. (The loss in us: one token of 32000 x 4096 47.8 and 52.4, 7899 of 48 x 1816 18.6 and 22.4.)
+constexpr int kGradRun = 8;
+int loss_run(const Head16 &h) { return h.V <= 512 ? 1 : kGradRun; }
 
 cudaError_t pack(Head16 &h, cudaStream_t stream, const char **detail) {
     const Pack16 packs[2] = {{&h.X, &h.ldx, h.T, h.D}, {&h.W, &h.ldw, h.w_dv ? h.D : h.V, h.w_dv ? h.V : h.D}};
@@ -422,20 +422,16 @@ cudaError_t head16_grad_launch(const Head16 &head, cudaStream_t stream, const ch
         g.D = static_cast<uint16_t *>(dz);
         g.ldd = ldz;
         x.v0 = v0;
-        if (stream_gemm16_supports(g)) {
-            err = stream_gemm16_extra_launch(g, kPairLogitGrad, extra, stream, detail);
-            if (err != cudaSuccess) return err;
-        } else {
-            err = pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
-            if (err != cudaSuccess) return err;
-            const int each = tokens_each(h.T);
-            err = launch_early(h.dtype == kBf16 ? certain_kernel<__nv_bfloat16> : certain_kernel<__half>,
-                               dim3(static_cast<unsigned>((h.T + 8LL * each - 1) / (8 * each))), 256, 0, stream, x,
-                               label_product(g), g.D, ldz, h.T, n, each);
-            if (err != cudaSuccess) {
-                *detail = "loss gradient kernel launch failed";
-                return err;
-            }
+        err = stream_gemm16_supports(g) ? stream_gemm16_extra_launch(g, kPairLogitGrad, extra, stream, detail)
+                                        : pair_gemm16_extra_launch(&g, 1, kPairLogitGrad, extra, stream, detail);
+        if (err != cudaSuccess) return err;
+        const int each = tokens_each(h.T);
+        err = launch_early(h.dtype == kBf16 ? certain_kernel<__nv_bfloat16> : certain_kernel<__half>,
+                           dim3(static_cast<unsigned>((h.T + 8LL * each - 1) / (8 * each))), 256, 0, stream, x,
+                           label_product(g), g.D, ldz, h.T, n, each);
+        if (err != cudaSuccess) {
+            *detail = "loss gradient kernel launch failed";
+            return err;
         }
         Gemm16 list[2];
         int count = 0;

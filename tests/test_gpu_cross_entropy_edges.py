@@ -7,8 +7,6 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_cross_entropy import summing_error  # noqa: E402
-
 pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.bfloat16, torch.float16]
@@ -101,12 +99,12 @@ def fp32_step(v):
                                    (300, 4000, 4104), (40000, 9001, 72)])
 def test_certain_labels_of_any_vocabulary(sgemm_lib, dtype, transw, T, V, D):
     """1 - p at the labels is about 10^-4 in each vocabulary, on either product and with tokens or entries in pieces, and
-    the gradient no larger, so that the label's logit's own error shows in it. The loss and the pair product's gradient have that
-    logit within a step of fp32 (added up with its roundings kept), the streaming product's in runs of 64 products. Times
-    p < 1 it passes to dX through the label's row of W, with two steps of 1 - p from expm1f. Besides, 2^-14 of each
-    other p (logits below 8 lose up to a step, 2^-21, per 16 products, in two runs of 1024 at most, or 2^-23 at less than
-    2 in five of them); a rounding of each dz to 16 bits (and half of a subnormal step over 2^14 in half); and dX's own sum
-    and rounding. z - lse is exact: they are within a factor 2 of each other."""
+    the gradient no larger, so that the label's logit's own error shows in it. That logit is held to one step of fp32 (its
+    products are added up with their roundings kept); times p < 1 it passes to dX through the label's row of W, with two
+    steps of 1 - p from expm1f. Besides, 2^-14 of each other p (logits below 8 lose up to a step, 2^-21, per 16
+    products, in two runs of 1024 at most, or 2^-23 at less than 2 in five of them); a rounding of each dz to 16 bits
+    (and half of a subnormal step over 2^14 in half); and dX's own sum and rounding. z - lse is exact: they are within
+    a factor 2 of each other."""
     sg = sgemm_lib
     u = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}[dtype] * 1.001
     tiny = {torch.bfloat16: 2.0 ** -133, torch.float16: 2.0 ** -25}[dtype]
@@ -128,8 +126,6 @@ def test_certain_labels_of_any_vocabulary(sgemm_lib, dtype, transw, T, V, D):
     assert bool(((loss.double() - (torch.logsumexp(z, 1) - zl[:, 0])).abs() <= 2 * step + 2.0 ** -14 * rest
                  + (4 * exact.abs() + 64 + V / 256 + 16) * 2.0 ** -24 + 2.0 ** -22).all())
     length = w.double().norm(dim=1)
-    few = T <= 64 or -(-V // 128) * -(-T // 64) <= 128
-    lost = summing_error(x, w, labels, 64) if few else step
     for lse in (exact, own):
         dx, _ = sg.cross_entropy_backward(ones, x, given, labels, lse, transw=transw)
         assert sg.sgemm_device_status() == sg.SGEMM_OK
@@ -138,7 +134,7 @@ def test_certain_labels_of_any_vocabulary(sgemm_lib, dtype, transw, T, V, D):
         dz.scatter_(1, labels[:, None], torch.expm1(gap.gather(1, labels[:, None])))
         ref = dz @ w.double()
         at = dz.gather(1, labels[:, None])[:, 0].abs()
-        off = (2.0 ** -14 + u) * (dz.abs() @ length) + (lost + 2.0 ** -22 * at) * length[labels]
+        off = (2.0 ** -14 + u) * (dz.abs() @ length) + (step + 2.0 ** -22 * at) * length[labels]
         small = 0.0 if dtype is torch.bfloat16 else 2.0 ** -25 * 2.0 ** -14
         off += small * length.sum() + 1e-5 * (dz.abs() @ w.double().abs()).norm(dim=1)
         off += u * ref.norm(dim=1) + tiny * math.sqrt(D)
