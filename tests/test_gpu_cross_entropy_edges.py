@@ -140,3 +140,39 @@ def test_certain_labels_of_any_vocabulary(sgemm_lib, dtype, transw, T, V, D):
         off += u * ref.norm(dim=1) + tiny * math.sqrt(D)
         ratio = (dx.double() - ref).norm(dim=1) / off
         assert bool((ratio <= 1.0).all()), float(ratio.max())
+
+
+def test_logits_are_summed_in_runs(sgemm_lib):
+    """The pair product's accumulators lose up to a step of fp32 per 16 products, always towards zero (the tensor
+    cores cut). From zero in each run of 1024 products, and half a step for each run added, that bounds how far lse is
+    below its value where all products are positive; one accumulator for all 4104 would lose half of its own bound on
+    average, which is more. (In lse an error of every logit counts once, since the probabilities add up to 1; the
+    exponentials, their sums and lse's rounding are as in training_case.py.)"""
+    sg, (T, V, D) = sgemm_lib, (300, 3500, 4104)
+    x = normal(1, T, D).abs()
+    w = (normal(2, V, D).abs().float() * (12.0 / (D * 2 / math.pi))).bfloat16()
+    labels = torch.full((T,), -100, device="cuda")
+    _, lse = sg.cross_entropy(x, w, labels)
+    xd, wd = x.double(), w.double()
+
+    def lost(run):
+        total, all_lost = torch.zeros(T, V, dtype=torch.float64, device="cuda"), torch.zeros(T, V, device="cuda")
+        for r in range(0, D, run):
+            part = torch.zeros_like(total)
+            for k in range(r, min(r + run, D), 16):
+                end = min(k + 16, r + run, D)
+                part += xd[:, k:end] @ wd[:, k:end].t()
+                all_lost += fp32_step(part)
+            total += part
+            if r > 0:
+                all_lost += fp32_step(total) / 2
+        return total, all_lost.double()
+
+    z, bound = lost(1024)
+    want = torch.logsumexp(z, 1)
+    bound = (torch.softmax(z, 1) * bound).sum(1).mean()
+    rest = ((64 + V / 64 / 32 * 8 + 16) * 2.0 ** -24 + 2.0 ** -22 * want.abs()).mean()
+    one = (torch.softmax(z, 1) * lost(D)[1]).sum(1).mean() / 2
+    assert float(one) > float(bound + rest)
+    assert float((want - lse.double()).mean()) <= float(bound + rest)
+    assert float((lse.double() - want).mean()) <= float(rest)
