@@ -277,8 +277,9 @@ sgemm_status_t sgemm_host(int64_t M, int64_t N, int64_t K, float alpha,
  * sgemm_release_workspace().
  * Graphs: a stream's workspaces are allocated by its first call of a kind and size. Make that call
  * before capturing the stream: a captured call that needs a larger workspace is refused
- * (SGEMM_ERR_LAUNCH). Workspaces that later calls outgrow, and those of destroyed streams, are kept,
- * so a graph stays valid until sgemm_release_workspace(). A graph uses the workspaces of the
+ * (SGEMM_ERR_LAUNCH). A workspace that has to grow does so by half of its size at least, so it may be that
+ * much larger than what a call is said to need below. Workspaces that later calls outgrow, and those of destroyed
+ * streams, are kept, so a graph stays valid until sgemm_release_workspace(). A graph uses the workspaces of the
  * stream that it was captured on: its replays must not overlap that stream's other calls, nor
  * the replays of another graph captured there.
  */
@@ -378,7 +379,9 @@ sgemm_status_t sgemm_moe(sgemm_dtype_t dtype, sgemm_activation_t act, int64_t T,
  *
  * so a restored value is within a / 254 (and two roundings) of x, and a itself comes back as it was. A block of zeros
  * has S = 0; one that holds an infinity or a NaN restores to NaN throughout. Q in rows of a multiple of 16 bytes at a
- * 16-byte aligned base is read and written fastest; any other is taken too.
+ * 16-byte aligned base is read and written fastest; any other is taken too. Codes are read in the aligned 8-byte words
+ * that hold them: what else is in a row's first and last word (before Q or after its last row, at most 7 bytes) is read too, and
+ * not used.
  */
 /* The checkpoint (Q, S) of X (M x N, ldx >= max(1, N)). M == 0 or N == 0 is a no-op. */
 sgemm_status_t sgemm_checkpoint8(sgemm_dtype_t dtype, int64_t M, int64_t N, const void *X, int64_t ldx, int8_t *Q,
@@ -403,8 +406,7 @@ sgemm_status_t sgemm_linear_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, 
  * sgemm_linear_backward from checkpoints of X (M x K) and of the pre-activation Z (M x N): its results are those of
  * sgemm_linear_backward on the restored values, to the bit. (Zq, Zs) are read unless act is none, (Xq, Xs) only for dW
  * (NULL otherwise). X is restored in a workspace of 2 * M * K' bytes; Z is read from its codes, through a workspace
- * only where their rows are not 8-byte aligned (in the last 8 bytes of such rows what follows the row is read, and not
- * used).
+ * only where their rows are not 8-byte aligned.
  */
 sgemm_status_t sgemm_linear_backward_checkpoint8(sgemm_dtype_t dtype, sgemm_op_t transw, int64_t M, int64_t N,
                                                  int64_t K, const void *dY, int64_t lddy, const int8_t *Zq,
@@ -439,8 +441,9 @@ sgemm_status_t sgemm_cross_entropy(sgemm_dtype_t dtype, sgemm_op_t transw, int64
  *     dX = dz . op(W)^T (T x D, lddx >= D),   dW = X^T . dz in W's layout (lddw as ldw)
  *
  * dX and dW may each be NULL (not computed). With T == 0, dW is set to zero. The logits are computed again, a piece
- * of the vocabulary at a time. A piece's dz lives in a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
- * sums over several pieces in another of 4 * T' * D' bytes (T and D rounded up to multiples of 256). The products read dz
+ * of the vocabulary at a time. A piece's dz needs a workspace of 2 * T * max(4096, 2^28 / T) bytes at most, dX's fp32
+ * sums over several pieces another of 4 * T' * D' bytes (T and D rounded up to multiples of 256); both stay until
+ * sgemm_release_workspace(). The products read dz
  * in the call's dtype, for weights dloss / m, m the largest finite |dloss[t]| of the tokens that count (incd == 0: m =
  * dloss[0] if that is finite, else 1), in half times 2^14; the outputs are multiplied by m (in half, divided by 2^14). So
  * equal dloss are not rounded at all, and half holds probabilities down to 2^-38 (a token whose dloss is below 2^-38 of
