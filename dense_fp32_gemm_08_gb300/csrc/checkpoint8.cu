@@ -14,13 +14,14 @@ namespace sg {
 namespace {
 
 // Rows under way per lane. (16384 x 14336 saved with 2, 3, 4 at their best occupancy: 121, 111, 108 us, restored:
-// 107, 103, 103 us. 4095 x 3001 in unaligned rows, saved: 11.3, 13.0, 12.7 us.)
+// 107, 103, 103 us. 4095 x 3001 in unaligned rows, saved: 11.3, 13.0, 12.7 us. All before the codes were made in paired
+// operations, which the figures above have.)
 __host__ __device__ constexpr int save_rows(bool vec) { return vec ? 4 : 2; }
 constexpr int kRestoreRows = 4;
 
 // A row's chunks of 16 (saving) or 8 columns over lanes (4, 8, 16 or 32 to a row), groups of 32 lanes over warps. A CTA's eight
 // warps cover `wide` neighbouring groups (a power of two) of 8 / wide row tasks; a row task is
-// 4 steps of 32 / lanes rows. (Powers of two: a division per task cost as much as its rows.)
+// as many steps of 32 / lanes rows as a lane has rows under way. (Powers of two: a division per task cost as much as its rows.)
 struct Split8 {
     int lane_bits, wide_bits, groups, row_tasks;
     dim3 grid() const {
