@@ -7,6 +7,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import training_case as case  # noqa: E402
+from layer_case import worst  # noqa: E402
+
 pytestmark = pytest.mark.gpu
 
 DTYPES = [torch.bfloat16, torch.float16]
@@ -176,3 +179,94 @@ def test_logits_are_summed_in_runs(sgemm_lib):
     assert float(one) > float(bound + rest)
     assert float((want - lse.double()).mean()) <= float(bound + rest)
     assert float((lse.double() - want).mean()) <= float(rest)
+
+
+def certain(T, V, D, dtype, transw, seed=0):
+    """Half of the labels all but certain, some that do not count."""
+    w = normal(seed + 1, V, D, dtype=dtype, scale=1.28 / math.sqrt(D))
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    labels = torch.randint(V, (T,), generator=g, device="cuda")
+    sure = (8.5 + math.log(V / 56) / 1.28 ** 2) * (torch.arange(T, device="cuda") % 2)[:, None]
+    x = (normal(seed + 2, T, D, dtype=dtype).float() + sure * w[labels].float()).to(dtype)
+    labels[::5] = -100
+    dloss = torch.randn(T, generator=g, device="cuda") / T
+    return x, w if transw == "T" else w.t().contiguous(), labels, dloss
+
+
+def wider(t, pad, offset=0):
+    rows, cols = t.shape
+    buf = torch.full((rows * (cols + pad) + offset,), math.nan, dtype=t.dtype, device="cuda")
+    view = buf[offset:].view(rows, cols + pad)[:, :cols]
+    view.copy_(t)
+    return view
+
+
+def both(sg, x, w, labels, dloss, transw, stream=None):
+    loss, lse = sg.cross_entropy(x, w, labels, transw=transw, stream=stream)
+    return (loss, lse, *sg.cross_entropy_backward(dloss, x, w, labels, lse, transw=transw, stream=stream))
+
+
+@pytest.mark.parametrize("T,V,D", [(5, 77, 129), (40, 700, 265), (700, 3001, 200), (8300, 60, 71)])
+@pytest.mark.parametrize("transw", ["T", "N"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_certain_labels_in_other_layouts(sgemm_lib, dtype, transw, T, V, D):
+    """The same values in wider or unaligned rows, weights of the tokens in a strided column: the same results to the
+    bit; and those within the tolerances of the definitions."""
+    sg = sgemm_lib
+    x, w, labels, dloss = certain(T, V, D, dtype, transw, seed=T)
+    want = both(sg, x, w, labels, dloss, transw)
+    column = torch.zeros(T, 3, device="cuda")
+    column[:, 1] = dloss
+    for pad, offset in ((3, 0), (8, 0), (0, 1), (5, 8)):
+        got = both(sg, wider(x, pad, offset), wider(w, pad, offset), labels, column[:, 1], transw)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+    loss, lse, dx, dw = want
+    rloss, rlse, _, tol, ltol, _ = case.head_ref(x, w, labels, transw)
+    assert worst(lse, rlse, ltol) <= 1.0 and worst(loss, rloss, tol) <= 1.0
+    rdx, rdw, dxtol, dwtol = case.head_grad_ref(dloss, x, w, labels, lse, transw)
+    assert worst(dx, rdx, dxtol) <= 1.0 and worst(dw, rdw, dwtol) <= 1.0
+    assert not dx[::5].any()
+
+
+@pytest.mark.parametrize("T,V", TOKENS_AND_ENTRIES)
+def test_certain_labels_on_a_stream_and_in_a_graph(sgemm_lib, T, V):
+    sg = sgemm_lib
+    args = certain(T, V, 264, torch.bfloat16, "T", seed=V)
+    want = both(sg, *args, "T")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = both(sg, *args, "T", stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            got = both(sg, *args, "T")
+        for _ in range(3):
+            for t in got:
+                t.fill_(7.0)
+            graph.replay()
+        s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sg.sgemm_device_status() == sg.SGEMM_OK
+
+
+@pytest.mark.parametrize("transw", ["T", "N"])
+def test_one_entry_has_no_loss(sgemm_lib, transw):
+    """A vocabulary of one entry: lse is its logit z, the loss and p - 1 are zero but for lse's roundings. With m = z log2 e
+    rounded, the sum is 2^(z log2 e - m), off by 2^-22 (the hardware's exponential) and its rounding; its logarithm by that
+    and 2^-24; m ln 2 is added in two parts, rounded to a step of z at the end, and once more with the label's logit
+    (within a step too): e = 2^-21 + 3 |z| 2^-23 bounds the loss and |p - 1|, and its products the gradients."""
+    sg = sgemm_lib
+    for T in (1, 70, 9000):  # (the last on the pair product)
+        x, w, labels = inputs(T, 1, 520, transw=transw, seed=T)
+        labels[1::3] = -100
+        loss, lse, dx, dw = both(sg, x, w, labels, torch.ones(T, device="cuda"), transw)
+        row = w.double().reshape(-1)
+        z = x.double() @ row
+        e = (2.0 ** -21 + 3 * z.abs() * 2.0 ** -23) * 1.01 * (labels >= 0)
+        assert bool((loss >= 0).all()) and bool((loss.double() <= e).all())
+        assert bool(((lse.double() - z).abs() <= e)[labels >= 0].all())
+        assert bool((dx.double().abs() <= e[:, None] * row.abs() * 1.01).all())
+        assert bool((dw.double().abs().reshape(-1) <= e @ x.double().abs() * 1.01).all())
