@@ -98,23 +98,24 @@ __device__ __forceinline__ float label_logit(const LabelProduct &p, long long t,
     using H = Half16<T>;
     KeptSum sum;
     const uint16_t *x = p.x + t * p.ldx;
+    const unsigned D = p.D;  // (the last step may pass 2^31)
     if (p.w_dv) {
         const uint16_t *w = p.w + v;
-        for (int d0 = lane; d0 < p.D; d0 += 32 * 4 * UNROLL) {
+        for (unsigned d0 = lane; d0 < D; d0 += 32 * 4 * UNROLL) {
             uint16_t xv[4 * UNROLL], wv[4 * UNROLL];
 #pragma unroll
             for (int i = 0; i < 4 * UNROLL; ++i) {
-                const int d = d0 + 32 * i;
-                xv[i] = d < p.D ? __ldg(x + d) : 0;
-                wv[i] = d < p.D ? __ldg(w + d * p.ldw) : 0;
+                const unsigned d = d0 + 32 * i;
+                xv[i] = d < D ? __ldg(x + d) : 0;
+                wv[i] = d < D ? __ldg(w + d * p.ldw) : 0;
             }
 #pragma unroll
             for (int i = 0; i < 4 * UNROLL; ++i) sum.add(__fmul_rn(H::widen(xv[i]), H::widen(wv[i])));
         }
     } else {
         const uint16_t *w = p.w + v * p.ldw;
-        const int whole = p.D & ~7;
-        for (int d0 = 8 * lane; d0 < whole; d0 += 256 * UNROLL) {
+        const unsigned whole = D & ~7u;
+        for (unsigned d0 = 8 * lane; d0 < whole; d0 += 256 * UNROLL) {
             uint4 xv[UNROLL], wv[UNROLL];
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) {
@@ -135,7 +136,7 @@ __device__ __forceinline__ float label_logit(const LabelProduct &p, long long t,
                 }
             }
         }
-        if (whole + lane < p.D) sum.add(__fmul_rn(H::widen(__ldg(x + whole + lane)), H::widen(__ldg(w + whole + lane))));
+        if (whole + lane < D) sum.add(__fmul_rn(H::widen(__ldg(x + whole + lane)), H::widen(__ldg(w + whole + lane))));
     }
 #pragma unroll
     for (int m = 16; m > 0; m /= 2) {
@@ -356,8 +357,9 @@ cudaError_t head16_launch(const Head16 &head, cudaStream_t stream, const char **
             err = stream_gemm16_extra_launch(g, kPairLogits, extra, stream, detail);
             if (err != cudaSuccess) return err;
             const int wide = n_parts > 128;
-            err = launch_early(h.dtype == kBf16 ? join_rows_kernel<__nv_bfloat16> : join_rows_kernel<__half>, dim3(static_cast<unsigned>(wide ? T : (T + kRowWarps - 1) / kRowWarps)),
-                               32 * kRowWarps, 0, stream, parts, ld_parts, n_parts, wide, out);
+            err = launch_early(h.dtype == kBf16 ? join_rows_kernel<__nv_bfloat16> : join_rows_kernel<__half>,
+                               dim3(static_cast<unsigned>(wide ? T : (T + kRowWarps - 1) / kRowWarps)), 32 * kRowWarps, 0,
+                               stream, parts, ld_parts, n_parts, wide, out);
         } else {
             err = pair_gemm16_extra_launch(&g, 1, kPairLogits, extra, stream, detail);
             if (err != cudaSuccess) return err;
